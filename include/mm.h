@@ -18,6 +18,9 @@
  *
  *   CONV  2-D convolution through the GEMM (mm_conv2d_f32 below).
  *
+ *   Also: products with 16-bit inputs, products of rows grouped by expert with their
+ *         gradients, and products of 8-bit integers with scales (below).
+ *
  * Conventions shared by every entry point:
  *   - Layout: row-major. Element (i, k) of A lives at A[i * lda + k], (k, j) of B
  *     at B[k * ldb + j], (i, j) of C at C[i * ldc + j]. The pages lay matrices out
@@ -264,6 +267,123 @@ int mm_gemm_f16_config(int cfg, int64_t M, int64_t N, int64_t K,
                        const uint16_t *A, int64_t lda,
                        const uint16_t *B, int64_t ldb,
                        float *C, int64_t ldc, void *stream);
+
+/* Element types of the operands declared `void *` below. */
+typedef enum mm_type {
+    MM_TYPE_F32 = 0,
+    MM_TYPE_BF16 = 1,
+    MM_TYPE_F16 = 2
+} mm_type;
+
+/*
+ * mm_gemm_bf16_grouped / mm_gemm_f16_grouped: products whose rows are grouped, each group
+ * with a right-hand matrix of its own (a layer of experts: row i is a token, sorted by the
+ * expert it was routed to). With g(i) the group of row i,
+ *
+ *   C[i][j] = sum over k in [0, K) of A[i][k] * B_g(i)[k][j]
+ *
+ *   groups    number of groups, 0 <= groups <= 65535.
+ *   M         rows of A and C, N columns of C, K the inner size; each 0 .. 2^31 - 1.
+ *   offsets   device memory, groups + 1 entries, 8-byte aligned: rows offsets[g] <= i <
+ *             offsets[g + 1] are group g's. They are read on the device only (the call does
+ *             not wait for them) and must not decrease. Entries outside [0, M] count as the
+ *             nearer bound; a group whose end is not above its start is empty. Rows of C that
+ *             belong to no group are left untouched. Where offsets decrease, so that groups
+ *             overlap, the rows of C are unspecified; nothing outside them is written.
+ *   A, lda    M x K, 16-bit elements (bf16 or IEEE binary16), lda >= max(1, K).
+ *   B, ldb, stride_b, trans_b   matrix of group g at B + g * stride_b (elements, >= 0; 0
+ *             shares one matrix): trans_b = 0: K x N, ldb >= max(1, N); trans_b = 1: stored
+ *             N x K, element (k, j) at j * ldb + k, ldb >= max(1, K).
+ *   C, c_type, ldc   M x N of c_type (MM_TYPE_*), ldc >= max(1, N). Sums are fp32 and rounded
+ *             once, to nearest even; values beyond the type's range become infinities.
+ * The gradient of these products with respect to A is one of them: dA = dC x B^T, the call
+ * with trans_b the other way round, N and K exchanged.
+ * M == 0, N == 0 or groups == 0: nothing is enqueued. K == 0: the groups' rows are zeros.
+ * Layout, ownership, stream and errors as for mm_gemm_f32; MM_ERR_INVALID_ARG also for an
+ * unknown type, a negative stride, trans_b not 0 or 1, or offsets NULL or misaligned.
+ */
+int mm_gemm_bf16_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                         const uint16_t *A, int64_t lda,
+                         const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b,
+                         void *C, int c_type, int64_t ldc, void *stream);
+int mm_gemm_f16_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                        const uint16_t *A, int64_t lda,
+                        const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b,
+                        void *C, int c_type, int64_t ldc, void *stream);
+
+/*
+ * mm_gemm_bf16_grouped_grad_b / mm_gemm_f16_grouped_grad_b: the gradient of the grouped
+ * product with respect to its right-hand matrices, from the gradient G of C (M x N):
+ *
+ *   D_g[k][j] = sum over the rows i of group g of A[i][k] * G[i][j]
+ *
+ *   A, lda    M x K, lda >= max(1, K); G, ldg: M x N, ldg >= max(1, N); 16-bit elements.
+ *   D, d_type, ldd, stride_d   K x N of group g at D + g * stride_d (elements, >= 0), of
+ *             d_type, ldd >= max(1, N). Every group's matrix is written; an empty group's is
+ *             zeros. The D_g must not overlap (undefined, not checked).
+ * With right-hand matrices stored N x K (trans_b = 1) exchange A and G (and N and K): the
+ * result is then stored N x K too. Each element is one sum in a fixed order, so results are
+ * deterministic. Rows of no group are not read. N == 0, K == 0 or groups == 0: nothing is
+ * enqueued. Other arguments and errors as for mm_gemm_bf16_grouped.
+ */
+int mm_gemm_bf16_grouped_grad_b(int64_t groups, int64_t M, int64_t N, int64_t K,
+                                const int64_t *offsets, const uint16_t *A, int64_t lda,
+                                const uint16_t *G, int64_t ldg,
+                                void *D, int d_type, int64_t ldd, int64_t stride_d, void *stream);
+int mm_gemm_f16_grouped_grad_b(int64_t groups, int64_t M, int64_t N, int64_t K,
+                               const int64_t *offsets, const uint16_t *A, int64_t lda,
+                               const uint16_t *G, int64_t ldg,
+                               void *D, int d_type, int64_t ldd, int64_t stride_d, void *stream);
+
+/*
+ * mm_quantize_i8: rows of a matrix to 8-bit integers, one scale for each row (a token's
+ * activations, or an output channel's weights):
+ *
+ *   scale[i] = amax_i / 127 (rounded to fp32),  amax_i = max over j of |X[i][j]|
+ *   Q[i][j]  = 127 X[i][j] / amax_i, the exact quotient rounded to the nearest integer,
+ *              halves to the even one; so -127 <= Q <= 127 and Q[i][j] * scale[i] ~ X[i][j].
+ *
+ *   X, x_type, ldx   rows x cols of x_type (MM_TYPE_*), ldx >= max(1, cols).
+ *   Q, ldq    rows x cols of 8-bit integers, written, ldq >= max(1, cols).
+ *   scale     rows entries, written.
+ * A row of zeros (or cols == 0) gets scale 0 and zeros. A row that holds an infinity or a NaN
+ * gets scale NaN and zeros, so that every product with it is NaN. rows == 0: nothing is
+ * enqueued. Errors as for mm_gemm_f32.
+ */
+int mm_quantize_i8(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx,
+                   int8_t *Q, int64_t ldq, float *scale, void *stream);
+
+/*
+ * mm_gemm_i8: product of 8-bit integers with a scale for each row of A (token) and for each
+ * row of B (output channel):
+ *
+ *   C[i][j] = a_scale[i] * b_scale[j] * sum over k in [0, K) of A[i][k] * B[j][k]
+ *
+ *   A, lda    M x K, lda >= max(1, K). B, ldb: N x K, ldb >= max(1, K): both operands have k
+ *             along their rows, as mm_quantize_i8 writes them.
+ *   a_scale   M entries; b_scale: N entries, fp32.
+ *   C, c_type, ldc   M x N of c_type, ldc >= max(1, N).
+ * K <= 2^17 - 1: the sum is then exact in 32 bits for all 8-bit values (-128 included). It is
+ * rounded to fp32, multiplied by a_scale[i], then by b_scale[j], then rounded to c_type. With
+ * K == 0 the sum is 0. M == 0 or N == 0: nothing is enqueued. Errors as for mm_gemm_f32;
+ * MM_ERR_INVALID_ARG also for an unknown type, K above the limit or missing scales.
+ */
+int mm_gemm_i8(int64_t M, int64_t N, int64_t K,
+               const int8_t *A, int64_t lda, const float *a_scale,
+               const int8_t *B, int64_t ldb, const float *b_scale,
+               void *C, int c_type, int64_t ldc, void *stream);
+
+/*
+ * mm_gemm_i8_grouped: mm_gemm_i8 with the rows of A in groups and a right-hand matrix for
+ * each group (groups and offsets as for mm_gemm_bf16_grouped):
+ *   B, ldb, stride_b   N x K of group g at B + g * stride_b (elements, >= 0).
+ *   a_scale   M entries; b_scale: groups x N entries, packed.
+ * Errors as for mm_gemm_i8 and mm_gemm_bf16_grouped.
+ */
+int mm_gemm_i8_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                       const int8_t *A, int64_t lda, const float *a_scale,
+                       const int8_t *B, int64_t ldb, int64_t stride_b, const float *b_scale,
+                       void *C, int c_type, int64_t ldc, void *stream);
 
 /*
  * mm_conv2d_f32: 2-D convolution (cross-correlation, as in neural networks) in fp32,

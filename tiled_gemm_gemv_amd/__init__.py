@@ -6,7 +6,8 @@ the library's HIP kernels. Pointer arguments accept a device address (int) or a
 torch tensor on the GPU; `stream` accepts a hipStream_t address (int), a
 torch.cuda.Stream, or None for torch's current stream on the current device.
 
-gemm(A, B, out=None), gemv(A, x, out=None), conv2d(x, w, ...) etc. are conveniences for torch tensors:
+gemm(A, B, out=None), gemv(A, x, out=None), conv2d(x, w, ...), gemm16_grouped(A, B, offsets),
+gemm_i8(A, B, a_scale, b_scale) etc. are conveniences for torch tensors:
 they check dtypes, devices and strides, allocate the output with torch when none
 is given, and call the C entry points. PyTorch only provides device memory and
 streams here.
@@ -111,6 +112,18 @@ def load():
     lib.mm_conv2d_f32_config_name.restype = ctypes.c_char_p
     lib.mm_conv2d_f32_select.argtypes = [i64] * 13
     lib.mm_conv2d_f32_select.restype = ci
+    for name in ("mm_gemm_bf16_grouped", "mm_gemm_f16_grouped"):
+        getattr(lib, name).argtypes = [i64] * 4 + [vp, vp, i64, vp, i64, i64, ci, vp, ci, i64, vp]
+        getattr(lib, name).restype = ci
+    for name in ("mm_gemm_bf16_grouped_grad_b", "mm_gemm_f16_grouped_grad_b"):
+        getattr(lib, name).argtypes = [i64] * 4 + [vp, vp, i64, vp, i64, vp, ci, i64, i64, vp]
+        getattr(lib, name).restype = ci
+    lib.mm_quantize_i8.argtypes = [i64, i64, vp, ci, i64, vp, i64, vp, vp]
+    lib.mm_quantize_i8.restype = ci
+    lib.mm_gemm_i8.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, ci, i64, vp]
+    lib.mm_gemm_i8.restype = ci
+    lib.mm_gemm_i8_grouped.argtypes = [i64] * 4 + [vp, vp, i64, vp, vp, i64, i64, vp, vp, ci, i64, vp]
+    lib.mm_gemm_i8_grouped.restype = ci
     lib.mm_status_string.argtypes = [ci]
     lib.mm_status_string.restype = ctypes.c_char_p
     lib.mm_last_error.argtypes = []
@@ -306,6 +319,70 @@ def mm_conv2d_f32_select(N, C, H, W, K, R, S, sh, sw, ph, pw, dh, dw):
     return load().mm_conv2d_f32_select(N, C, H, W, K, R, S, sh, sw, ph, pw, dh, dw)
 
 
+MM_TYPE_F32 = 0   # element types, as include/mm.h defines them
+MM_TYPE_BF16 = 1
+MM_TYPE_F16 = 2
+
+
+def mm_gemm_bf16_grouped(groups, M, N, K, offsets, A, lda, B, ldb, stride_b, trans_b, C, c_type, ldc,
+                         stream=None):
+    """C rows of group g = A rows of group g x B_g (bf16 A and B). Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_bf16_grouped(groups, M, N, K, _addr(offsets), _addr(A), lda, _addr(B), ldb,
+                                    stride_b, trans_b, _addr(C), c_type, ldc, _stream(stream)),
+           "mm_gemm_bf16_grouped")
+
+
+def mm_gemm_f16_grouped(groups, M, N, K, offsets, A, lda, B, ldb, stride_b, trans_b, C, c_type, ldc,
+                        stream=None):
+    """C rows of group g = A rows of group g x B_g (fp16 A and B). Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_f16_grouped(groups, M, N, K, _addr(offsets), _addr(A), lda, _addr(B), ldb,
+                                   stride_b, trans_b, _addr(C), c_type, ldc, _stream(stream)),
+           "mm_gemm_f16_grouped")
+
+
+def mm_gemm_bf16_grouped_grad_b(groups, M, N, K, offsets, A, lda, G, ldg, D, d_type, ldd, stride_d,
+                                stream=None):
+    """D_g = (A rows of group g)^T x (G rows of group g) (bf16 A and G). Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_bf16_grouped_grad_b(groups, M, N, K, _addr(offsets), _addr(A), lda, _addr(G),
+                                           ldg, _addr(D), d_type, ldd, stride_d, _stream(stream)),
+           "mm_gemm_bf16_grouped_grad_b")
+
+
+def mm_gemm_f16_grouped_grad_b(groups, M, N, K, offsets, A, lda, G, ldg, D, d_type, ldd, stride_d,
+                               stream=None):
+    """D_g = (A rows of group g)^T x (G rows of group g) (fp16 A and G). Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_f16_grouped_grad_b(groups, M, N, K, _addr(offsets), _addr(A), lda, _addr(G),
+                                          ldg, _addr(D), d_type, ldd, stride_d, _stream(stream)),
+           "mm_gemm_f16_grouped_grad_b")
+
+
+def mm_quantize_i8(rows, cols, X, x_type, ldx, Q, ldq, scale, stream=None):
+    """Rows of X to 8-bit integers Q with a scale each. Raises MMError."""
+    lib = load()
+    _check(lib.mm_quantize_i8(rows, cols, _addr(X), x_type, ldx, _addr(Q), ldq, _addr(scale),
+                              _stream(stream)), "mm_quantize_i8")
+
+
+def mm_gemm_i8(M, N, K, A, lda, a_scale, B, ldb, b_scale, C, c_type, ldc, stream=None):
+    """C = diag(a_scale) (A x B^T) diag(b_scale), 8-bit A (M x K) and B (N x K). Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_i8(M, N, K, _addr(A), lda, _addr(a_scale), _addr(B), ldb, _addr(b_scale),
+                          _addr(C), c_type, ldc, _stream(stream)), "mm_gemm_i8")
+
+
+def mm_gemm_i8_grouped(groups, M, N, K, offsets, A, lda, a_scale, B, ldb, stride_b, b_scale, C, c_type,
+                       ldc, stream=None):
+    """mm_gemm_i8 with rows of A in groups, a B_g and scales for each group. Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_i8_grouped(groups, M, N, K, _addr(offsets), _addr(A), lda, _addr(a_scale),
+                                  _addr(B), ldb, stride_b, _addr(b_scale), _addr(C), c_type, ldc,
+                                  _stream(stream)), "mm_gemm_i8_grouped")
+
+
 def mm_status_string(status):
     return load().mm_status_string(status).decode()
 
@@ -347,6 +424,8 @@ def _matrix(t, name, dtypes=None):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
+    if t.numel() == 0:  # the strides of an empty tensor are arbitrary, and nothing uses them
+        return max(cols, 1)
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     ld = t.stride(0) if rows > 1 else max(cols, 1)
@@ -536,4 +615,177 @@ def conv2d(x, w, stride=(1, 1), pad=(0, 0), dilation=(1, 1), out=None, config=No
         else:
             mm_conv2d_f32_config(config, N, C, H, W, K, R, S, sh, sw, ph, pw, dh, dw, x, w, out,
                                  stream)
+    return out
+
+
+def _mm_type(dtype, name):
+    import torch
+    types = {torch.float32: MM_TYPE_F32, torch.bfloat16: MM_TYPE_BF16, torch.float16: MM_TYPE_F16}
+    if dtype not in types:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return types[dtype]
+
+
+def _stack(t, name, dtypes):
+    """Leading dimension and group stride of a 3-D tensor of matrices."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D (groups, rows, columns)")
+    ld = _matrix(t[0] if t.shape[0] else t.new_empty(t.shape[1:]), name, dtypes)
+    return ld, t.stride(0)
+
+
+def _offsets(t, groups, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int64:
+        raise TypeError("offsets must be an int64 tensor")
+    if t.dim() != 1 or t.shape[0] != groups + 1 or not t.is_contiguous():
+        raise ValueError(f"offsets must be contiguous, with groups + 1 = {groups + 1} entries")
+    _on_device(device, offsets=t)
+
+
+def _scale(t, shape, name, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {shape}")
+    _on_device(device, **{name: t})
+
+
+def _output(out, out_dtype, shape, device):
+    """The output tensor: `out` if given (its dtype must be out_dtype where that is given too),
+    else a new one of out_dtype (float32 by default)."""
+    import torch
+    if out is None:
+        dtype = torch.float32 if out_dtype is None else out_dtype
+        _mm_type(dtype, "out_dtype")
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
+    _on_device(device, out=out)
+    return out
+
+
+def gemm16_grouped(A, B, offsets, trans_b=False, out=None, out_dtype=None, stream=None):
+    """Products of rows grouped by expert: rows offsets[g] <= i < offsets[g + 1] of out are those
+    rows of A (M x K) times B[g], for bf16 or fp16 GPU tensors of the same dtype. B is
+    groups x K x N, or groups x N x K with trans_b (B[g] is then transposed); any row and group
+    strides, unit column stride. offsets is an int64 GPU tensor of groups + 1 entries that do
+    not decrease; the host never reads it. out is float32, bfloat16 or float16 (out_dtype,
+    float32 by default); its rows of no group are left as they are (uninitialised if out was
+    not given). The gradient with respect to A is gemm16_grouped(dout, B, offsets, not trans_b)."""
+    import torch
+    lda = _matrix(A, "A", (torch.bfloat16, torch.float16))
+    ldb, stride_b = _stack(B, "B", (A.dtype,))
+    M, K = A.shape
+    groups, N, K2 = (B.shape[0], B.shape[1], B.shape[2]) if trans_b else (B.shape[0], B.shape[2], B.shape[1])
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
+    _on_device(A.device, B=B)
+    _offsets(offsets, groups, A.device)
+    out = _output(out, out_dtype, (M, N), A.device)
+    c_type = _mm_type(out.dtype, "out")
+    ldc = _matrix(out, "out", (out.dtype,))
+    call = mm_gemm_bf16_grouped if A.dtype == torch.bfloat16 else mm_gemm_f16_grouped
+    with torch.cuda.device(A.device):
+        call(groups, M, N, K, offsets, A, lda, B, ldb, stride_b, 1 if trans_b else 0, out, c_type, ldc, stream)
+    return out
+
+
+def gemm16_grouped_grad_b(A, G, offsets, out=None, out_dtype=None, stream=None):
+    """The gradient of gemm16_grouped(A, B, offsets) with respect to B from the gradient G of its
+    output: out[g] = A[lo:hi].T @ G[lo:hi] over the rows lo = offsets[g] .. hi = offsets[g + 1]
+    (zeros for an empty group), groups x K x N. For B stored groups x N x K (trans_b) exchange A
+    and G. A, G: bf16 or fp16 of the same dtype; out float32 (default), bfloat16 or float16."""
+    import torch
+    lda = _matrix(A, "A", (torch.bfloat16, torch.float16))
+    ldg = _matrix(G, "G", (A.dtype,))
+    M, K = A.shape
+    M2, N = G.shape
+    if M2 != M:
+        raise ValueError(f"row counts differ: {tuple(A.shape)}, {tuple(G.shape)}")
+    _on_device(A.device, G=G)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a 1-D tensor of groups + 1 entries")
+    groups = offsets.shape[0] - 1
+    _offsets(offsets, groups, A.device)
+    out = _output(out, out_dtype, (groups, K, N), A.device)
+    d_type = _mm_type(out.dtype, "out")
+    ldd, stride_d = _stack(out, "out", (out.dtype,))
+    if groups > 1 and K > 0 and N > 0 and stride_d < (K - 1) * ldd + N:
+        raise ValueError("the matrices of out overlap")
+    call = mm_gemm_bf16_grouped_grad_b if A.dtype == torch.bfloat16 else mm_gemm_f16_grouped_grad_b
+    with torch.cuda.device(A.device):
+        call(groups, M, N, K, offsets, A, lda, G, ldg, out, d_type, ldd, stride_d, stream)
+    return out
+
+
+def quantize_i8(x, out=None, scale=None, stream=None):
+    """(q, scale): the rows of x (float32, bfloat16 or float16) as int8 with q[i] * scale[i] ~ x[i],
+    scale[i] = max |x[i]| / 127; values are rounded to the nearest integer, halves to even."""
+    import torch
+    ldx = _matrix(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    rows, cols = x.shape
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    ldq = _matrix(out, "out", (torch.int8,))
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, cols)}")
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _on_device(x.device, out=out)
+    _scale(scale, (rows,), "scale", x.device)
+    with torch.cuda.device(x.device):
+        mm_quantize_i8(rows, cols, x, _mm_type(x.dtype, "x"), ldx, out, ldq, scale, stream)
+    return out, scale
+
+
+def gemm_i8(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
+    """out[i][j] = a_scale[i] b_scale[j] sum_k A[i][k] B[j][k] for int8 GPU tensors A (M x K) and
+    B (N x K), any row strides; out float32 (default), bfloat16 or float16."""
+    import torch
+    lda = _matrix(A, "A", (torch.int8,))
+    ldb = _matrix(B, "B", (torch.int8,))
+    M, K = A.shape
+    N, K2 = B.shape
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
+    _on_device(A.device, B=B)
+    _scale(a_scale, (M,), "a_scale", A.device)
+    _scale(b_scale, (N,), "b_scale", A.device)
+    out = _output(out, out_dtype, (M, N), A.device)
+    c_type = _mm_type(out.dtype, "out")
+    ldc = _matrix(out, "out", (out.dtype,))
+    with torch.cuda.device(A.device):
+        mm_gemm_i8(M, N, K, A, lda, a_scale, B, ldb, b_scale, out, c_type, ldc, stream)
+    return out
+
+
+def gemm_i8_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, stream=None):
+    """gemm_i8 with rows grouped by expert: B groups x N x K, b_scale groups x N, offsets as for
+    gemm16_grouped; rows of no group are left as they are."""
+    import torch
+    lda = _matrix(A, "A", (torch.int8,))
+    ldb, stride_b = _stack(B, "B", (torch.int8,))
+    M, K = A.shape
+    groups, N, K2 = B.shape
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
+    _on_device(A.device, B=B)
+    _offsets(offsets, groups, A.device)
+    _scale(a_scale, (M,), "a_scale", A.device)
+    _scale(b_scale, (groups, N), "b_scale", A.device)
+    out = _output(out, out_dtype, (M, N), A.device)
+    c_type = _mm_type(out.dtype, "out")
+    ldc = _matrix(out, "out", (out.dtype,))
+    with torch.cuda.device(A.device):
+        mm_gemm_i8_grouped(groups, M, N, K, offsets, A, lda, a_scale, B, ldb, stride_b, b_scale, out,
+                           c_type, ldc, stream)
     return out

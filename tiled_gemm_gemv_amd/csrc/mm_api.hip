@@ -240,6 +240,115 @@ int run_conv(int cfg, int64_t N, int64_t C, int64_t H, int64_t W, int64_t K, int
     return from_hip("conv2d launch", mm::conv_launch(cfg, a, static_cast<hipStream_t>(stream)));
 }
 
+// Largest K of the 8-bit products: sums of K products of magnitude up to 2^14 fit 32 bits.
+constexpr int64_t kMaxKInt8 = (int64_t(1) << 17) - 1;
+constexpr int64_t kMaxGroups = 65535;
+
+bool type_ok(int t) { return t == MM_TYPE_F32 || t == MM_TYPE_BF16 || t == MM_TYPE_F16; }
+int type_size(int t) { return t == MM_TYPE_F32 ? 4 : 2; }
+
+// Byte extent of `count` rows x cols matrices, `stride` elements apart, fits in int64.
+bool strided_extent_fits(int64_t count, int64_t stride, int64_t rows, int64_t cols, int64_t ld)
+{
+    if (!extent_fits(rows, cols, ld)) return false;
+    const int64_t one = (rows - 1) * ld + cols, limit = INT64_MAX / 4;
+    return count <= 1 || stride <= (limit - one) / (count - 1);
+}
+
+// Checks of the grouped products; rows mode and gradient mode differ in the operands' shapes.
+// offsets == nullptr with dense == true: the product of one group of all rows.
+int check_group(const mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, int64_t K, bool dense)
+{
+    if (groups < 0 || M < 0 || N < 0 || K < 0) return invalid("negative size");
+    if (groups > kMaxGroups) return invalid("more than 65535 groups");
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return invalid("size above 2^31 - 1");
+    const bool i8 = a.elem == mm::GroupElem::I8;
+    if (i8 && K > kMaxKInt8) return invalid("K above 2^17 - 1 (sums of 8-bit products fit 32 bits up to there)");
+    if (!type_ok(a.c_type)) return invalid("unknown output type");
+    // A is M x K; B_g is K x N, or N x K transposed; in gradient mode B is the M x N gradient
+    // and C_g is K x N
+    const int64_t b_rows = a.grad ? M : a.trans_b ? N : K, b_cols = a.grad ? N : a.trans_b ? K : N;
+    const int64_t c_rows = a.grad ? K : M, b_count = a.grad ? 1 : groups, c_count = a.grad ? groups : 1;
+    if (a.lda < (K > 1 ? K : 1)) return invalid("lda < max(1, K)");
+    if (a.ldb < (b_cols > 1 ? b_cols : 1))
+        return invalid(a.grad ? "ldg < max(1, N)" : a.trans_b ? "ldb < max(1, K)" : "ldb < max(1, N)");
+    if (a.ldc < (N > 1 ? N : 1)) return invalid(a.grad ? "ldd < max(1, N)" : "ldc < max(1, N)");
+    if (a.stride_b < 0 || a.stride_c < 0) return invalid("negative group stride");
+    if (groups == 0) return MM_OK;  // no rows belong to a group: pointers may be NULL
+    const bool has_a = M > 0 && K > 0, has_b = b_rows > 0 && b_cols > 0, has_c = c_rows > 0 && N > 0;
+    if (has_a && !a.A) return invalid("A is NULL");
+    if (has_b && !a.B) return invalid(a.grad ? "G is NULL" : "B is NULL");
+    if (has_c && !a.C) return invalid(a.grad ? "D is NULL" : "C is NULL");
+    if (!dense && !a.offsets) return invalid("offsets is NULL");
+    const int elem = i8 ? 1 : 2;
+    if ((uintptr_t)a.A % elem || (uintptr_t)a.B % elem || (uintptr_t)a.C % type_size(a.c_type))
+        return invalid("pointer not aligned to its element size");
+    if ((uintptr_t)a.offsets % 8) return invalid("offsets not 8-byte aligned");
+    if (i8) {
+        if (M > 0 && !a.sa) return invalid("a_scale is NULL");
+        if (N > 0 && !a.sb) return invalid("b_scale is NULL");
+        if ((uintptr_t)a.sa % 4 || (uintptr_t)a.sb % 4) return invalid("scales not 4-byte aligned");
+    }
+    if (has_a && !extent_fits(M, K, a.lda)) return invalid("A extent overflows");
+    if (has_b && !strided_extent_fits(b_count, a.stride_b, b_rows, b_cols, a.ldb))
+        return invalid(a.grad ? "G extent overflows" : "B extent overflows");
+    if (has_c && !strided_extent_fits(c_count, a.stride_c, c_rows, N, a.ldc))
+        return invalid(a.grad ? "D extent overflows" : "C extent overflows");
+    return MM_OK;
+}
+
+int run_group(mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, int64_t K, bool dense, void *stream)
+{
+    const int st = check_group(a, groups, M, N, K, dense);
+    if (st != MM_OK) return st;
+    if (groups == 0 || N == 0 || (a.grad ? K : M) == 0) return MM_OK;  // no output
+    a.groups = (int)groups;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    return from_hip(a.grad ? "grouped gradient launch" : dense ? "i8 gemm launch" : "grouped gemm launch",
+                    mm::group_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int run_grouped16(mm::GroupElem elem, int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                  const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b,
+                  void *C, int c_type, int64_t ldc, void *stream)
+{
+    if (trans_b != 0 && trans_b != 1) return invalid("trans_b is neither 0 nor 1");
+    mm::GroupArgs a{};
+    a.elem = elem;
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.offsets = offsets;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.stride_b = stride_b;
+    a.trans_b = trans_b == 1;
+    a.c_type = c_type;
+    return run_group(a, groups, M, N, K, false, stream);
+}
+
+int run_grouped16_grad_b(mm::GroupElem elem, int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                         const uint16_t *A, int64_t lda, const uint16_t *G, int64_t ldg, void *D, int d_type,
+                         int64_t ldd, int64_t stride_d, void *stream)
+{
+    mm::GroupArgs a{};
+    a.elem = elem;
+    a.grad = true;
+    a.A = A;
+    a.B = G;
+    a.C = D;
+    a.offsets = offsets;
+    a.lda = lda;
+    a.ldb = ldg;
+    a.ldc = ldd;
+    a.stride_c = stride_d;
+    a.c_type = d_type;
+    return run_group(a, groups, M, N, K, false, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -482,6 +591,106 @@ int mm_conv2d_f32_select(int64_t N, int64_t C, int64_t H, int64_t W, int64_t K, 
                    work) != MM_OK)
         return -1;
     return mm::conv_choose_config(a);
+}
+
+int mm_gemm_bf16_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets, const uint16_t *A,
+                         int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b, void *C,
+                         int c_type, int64_t ldc, void *stream)
+{
+    return run_grouped16(mm::GroupElem::Bf16, groups, M, N, K, offsets, A, lda, B, ldb, stride_b, trans_b, C, c_type,
+                         ldc, stream);
+}
+
+int mm_gemm_f16_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets, const uint16_t *A,
+                        int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b, void *C,
+                        int c_type, int64_t ldc, void *stream)
+{
+    return run_grouped16(mm::GroupElem::F16, groups, M, N, K, offsets, A, lda, B, ldb, stride_b, trans_b, C, c_type,
+                         ldc, stream);
+}
+
+int mm_gemm_bf16_grouped_grad_b(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                                const uint16_t *A, int64_t lda, const uint16_t *G, int64_t ldg, void *D, int d_type,
+                                int64_t ldd, int64_t stride_d, void *stream)
+{
+    return run_grouped16_grad_b(mm::GroupElem::Bf16, groups, M, N, K, offsets, A, lda, G, ldg, D, d_type, ldd,
+                                stride_d, stream);
+}
+
+int mm_gemm_f16_grouped_grad_b(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                               const uint16_t *A, int64_t lda, const uint16_t *G, int64_t ldg, void *D, int d_type,
+                               int64_t ldd, int64_t stride_d, void *stream)
+{
+    return run_grouped16_grad_b(mm::GroupElem::F16, groups, M, N, K, offsets, A, lda, G, ldg, D, d_type, ldd,
+                                stride_d, stream);
+}
+
+int mm_quantize_i8(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx, int8_t *Q, int64_t ldq,
+                   float *scale, void *stream)
+{
+    if (rows < 0 || cols < 0) return invalid("negative size");
+    if (rows > kMaxDim || cols > kMaxDim) return invalid("size above 2^31 - 1");
+    if (!type_ok(x_type)) return invalid("unknown input type");
+    if (ldx < (cols > 1 ? cols : 1)) return invalid("ldx < max(1, cols)");
+    if (ldq < (cols > 1 ? cols : 1)) return invalid("ldq < max(1, cols)");
+    if (rows > 0 && cols > 0 && !X) return invalid("X is NULL");
+    if (rows > 0 && cols > 0 && !Q) return invalid("Q is NULL");
+    if (rows > 0 && !scale) return invalid("scale is NULL");
+    if ((uintptr_t)X % type_size(x_type) || (uintptr_t)scale % 4)
+        return invalid("pointer not aligned to its element size");
+    if (rows > 0 && cols > 0 && !(extent_fits(rows, cols, ldx) && extent_fits(rows, cols, ldq)))
+        return invalid("extent overflows");
+    if (rows == 0) return MM_OK;
+    mm::QuantArgs a;
+    a.X = X;
+    a.Q = Q;
+    a.scale = scale;
+    a.rows = rows;
+    a.cols = cols;
+    a.ldx = ldx;
+    a.ldq = ldq;
+    a.x_type = x_type;
+    return from_hip("quantize launch", mm::quantize_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int mm_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+               int64_t ldb, const float *b_scale, void *C, int c_type, int64_t ldc, void *stream)
+{
+    mm::GroupArgs a{};
+    a.elem = mm::GroupElem::I8;
+    a.trans_b = true;
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.sa = a_scale;
+    a.sb = b_scale;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.c_type = c_type;
+    return run_group(a, 1, M, N, K, true, stream);
+}
+
+int mm_gemm_i8_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets, const int8_t *A,
+                       int64_t lda, const float *a_scale, const int8_t *B, int64_t ldb, int64_t stride_b,
+                       const float *b_scale, void *C, int c_type, int64_t ldc, void *stream)
+{
+    mm::GroupArgs a{};
+    a.elem = mm::GroupElem::I8;
+    a.trans_b = true;
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.offsets = offsets;
+    a.sa = a_scale;
+    a.sb = b_scale;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.stride_b = stride_b;
+    a.stride_sb = N;
+    a.c_type = c_type;
+    return run_group(a, groups, M, N, K, false, stream);
 }
 
 const char *mm_status_string(int status)

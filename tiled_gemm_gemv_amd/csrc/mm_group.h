@@ -1,0 +1,188 @@
+// mm_group.h -- shared by the kernels of the grouped products and of the 8-bit integer
+// product (mm_group_any.hip): element types, the launch
+// arguments, the map from a workgroup to a tile of a group, and the epilogue.
+//
+// The sums. Rows lo_g <= i < hi_g of A (lo_g = offsets[g], hi_g = offsets[g + 1]) belong to
+// group g:
+//   rows mode      C[i][j] = s(i, j) sum over k < K of A[i][k] B_g(k, j)
+//                  s = 1 for 16-bit elements, sa[i] sb_g[j] for 8-bit integers;
+//                  B_g(k, j) = B[g stride_b + k ldb + j] or, "transposed",
+//                  B[g stride_b + j ldb + k]
+//   gradient mode  C_g[p][j] = sum over lo_g <= i < hi_g of A[i][p] B[i][j]
+//
+// The offsets live in device memory and no host code reads them: the grid covers the most
+// tiles that M rows in `groups` groups can need, and each workgroup finds its own tile. They
+// are clamped to [0, M], and a group whose end is not above its start is empty, so whatever
+// they hold no kernel leaves the rows of A and C.
+#pragma once
+
+#include "mm_internal.h"
+
+namespace mm {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// An element type: its storage, its accumulator over 16 values of a 32 x 32 block, and the
+// MFMA that multiplies 32 rows by 32 columns over 32 bytes of k: lane l supplies the 16
+// bytes at k byte 16 (l / 32) of row (or column) l % 32.
+struct ElemBf16 {
+    typedef unsigned short T;
+    typedef f32x16 Acc;
+    static constexpr bool INT8 = false;
+    static __device__ __forceinline__ Acc mma(u32x4 a, u32x4 b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+};
+struct ElemF16 {
+    typedef unsigned short T;
+    typedef f32x16 Acc;
+    static constexpr bool INT8 = false;
+    static __device__ __forceinline__ Acc mma(u32x4 a, u32x4 b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b),
+                                                      c, 0, 0, 0);
+    }
+};
+// Sums of 8-bit products are exact in 32 bits: |sum| <= 2^14 K, and the host admits
+// K <= 2^17 - 1.
+struct ElemI8 {
+    typedef signed char T;
+    typedef i32x16 Acc;
+    static constexpr bool INT8 = true;
+    static __device__ __forceinline__ Acc mma(u32x4 a, u32x4 b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                                     c, 0, 0, 0);
+    }
+};
+
+// Output types (the public MM_TYPE_* values). fp32 sums are rounded once, to nearest even.
+template <int OUT>
+struct OutType;
+template <>
+struct OutType<0> {
+    typedef float T;
+};
+template <>
+struct OutType<1> {
+    typedef __bf16 T;
+};
+template <>
+struct OutType<2> {
+    typedef _Float16 T;
+};
+
+// lo and hi of group g, clamped to [0, M].
+__device__ __forceinline__ void group_range(const int64_t *offsets, int g, int M, int &lo, int &hi)
+{
+    const int64_t a = offsets[g], b = offsets[g + 1];
+    lo = (int)(a < 0 ? 0 : a > M ? M : a);
+    hi = (int)(b < 0 ? 0 : b > M ? M : b);
+    if (hi < lo) hi = lo;
+}
+
+__device__ __forceinline__ unsigned wave_inclusive_sum(unsigned v)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const unsigned u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// A row tile of a group: rows row0 <= i < min(row0 + BM, hi) of group g.
+struct RowTile {
+    int g, row0, hi;
+};
+
+// Number of BM-row tiles over all groups. Every wave of the workgroup calls it (64 groups
+// at a time, one per lane); the result is wave-uniform.
+template <int BM>
+__device__ __forceinline__ unsigned count_row_tiles(const GroupArgs &p)
+{
+    if (!p.offsets) return (unsigned)((p.M + BM - 1) / BM);
+    unsigned total = 0;
+    for (int base = 0; base < p.groups; base += 64) {
+        const int g = base + (threadIdx.x & 63);
+        int lo = 0, hi = 0;
+        if (g < p.groups) group_range(p.offsets, g, p.M, lo, hi);
+        const unsigned incl = wave_inclusive_sum((unsigned)((hi - lo + BM - 1) / BM));
+        total += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return total;
+}
+
+// Row tile number rt in group order; false if there is none (never for rt below
+// count_row_tiles of the same offsets).
+template <int BM>
+__device__ __forceinline__ bool find_row_tile(const GroupArgs &p, unsigned rt, RowTile &t)
+{
+    if (!p.offsets) {
+        t.g = 0;
+        t.row0 = (int)rt * BM;
+        t.hi = p.M;
+        return (int64_t)rt * BM < p.M;
+    }
+    unsigned before = 0;
+    for (int base = 0; base < p.groups; base += 64) {
+        const int g = base + (threadIdx.x & 63);
+        int lo = 0, hi = 0;
+        if (g < p.groups) group_range(p.offsets, g, p.M, lo, hi);
+        const unsigned cnt = (unsigned)((hi - lo + BM - 1) / BM);
+        const unsigned incl = before + wave_inclusive_sum(cnt);
+        const unsigned long long above = __ballot(incl > rt);
+        if (above) {
+            const int l = __ffsll(above) - 1;
+            const unsigned first = __builtin_amdgcn_readlane(incl - cnt, l);
+            t.g = base + l;
+            t.hi = __builtin_amdgcn_readlane(hi, l);
+            const int64_t row0 = __builtin_amdgcn_readlane(lo, l) + (int64_t)(rt - first) * BM;
+            t.row0 = (int)row0;
+            return rt >= first && row0 < t.hi;
+        }
+        before = __builtin_amdgcn_readlane(incl, 63);
+    }
+    return false;
+}
+
+// Most BM-row tiles that M rows in `groups` groups can need: whole tiles, and one partial
+// tile for each group that has a row.
+inline int64_t max_row_tiles(const GroupArgs &a, int bm)
+{
+    if (!a.offsets) return ((int64_t)a.M + bm - 1) / bm;
+    return a.M / bm + (a.groups < a.M ? a.groups : a.M);
+}
+
+// Logical tile of workgroup bid: consecutive logical tiles on one XCD (workgroups are dealt
+// to the 8 XCDs in turn), in groups of 8 row tiles that walk the tile columns together, so
+// that an XCD's L2 serves both panels.
+__device__ __forceinline__ void tile_of_group_block(unsigned bid, unsigned nblocks, unsigned tiles_m, unsigned tiles_n,
+                                                    unsigned &tm, unsigned &tn)
+{
+    constexpr unsigned xcds = 8, group_m = 8;
+    const unsigned q = nblocks / xcds, r = nblocks % xcds;
+    const unsigned xcd = bid % xcds, slot = bid / xcds;
+    const unsigned logical = (xcd < r) ? xcd * (q + 1) + slot : r * (q + 1) + (xcd - r) * q + slot;
+    const unsigned per_group = group_m * tiles_n;
+    const unsigned g = logical / per_group;
+    const unsigned first_m = g * group_m;
+    const unsigned gm = min(tiles_m - first_m, group_m);
+    const unsigned in_g = logical - g * per_group;
+    tm = first_m + in_g % gm;
+    tn = in_g / gm;
+}
+
+}  // namespace
+}  // namespace mm

@@ -144,6 +144,38 @@ int gemm16_select_config(int64_t M, int64_t N, int64_t K);
 hipError_t gemm16_launch(int cfg, bool bf16, const void *A, int64_t lda, const void *B, int64_t ldb,
                          float *C, int64_t ldc, int M, int N, int K, hipStream_t stream);
 
+// Grouped products and the 8-bit integer product (mm_group.h has the sums). Sizes and
+// pointers are validated on the host; offsets (device memory) are not.
+enum class GroupElem { Bf16, F16, I8 };
+struct GroupArgs {
+    const void *A;
+    const void *B;
+    void *C;
+    const int64_t *offsets;    // groups + 1 entries; nullptr: one group of all M rows
+    const float *sa, *sb;      // I8: scales of A's rows and of each group's columns of C
+    int64_t lda, ldb, ldc;
+    int64_t stride_b, stride_c, stride_sb;  // between groups: B, C (gradient mode), sb
+    int groups, M, N, K;       // gradient mode: C_g is K x N, the sum runs over the rows
+    int c_type;                // MM_TYPE_*
+    GroupElem elem;
+    bool trans_b;              // B_g stored N x K (always so for I8)
+    bool grad;                 // gradient mode
+};
+// The kernel for the shape; M, N, groups >= 1 (gradient mode: K, N, groups >= 1).
+hipError_t group_launch(const GroupArgs &a, hipStream_t stream);
+// Any shape and alignment (mm_group_any.hip).
+hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream);
+
+// Rows to 8-bit integers with a scale each (mm_quantize.hip); rows >= 1.
+struct QuantArgs {
+    const void *X;
+    signed char *Q;
+    float *scale;
+    int64_t rows, cols, ldx, ldq;
+    int x_type;                // MM_TYPE_*
+};
+hipError_t quantize_launch(const QuantArgs &a, hipStream_t stream);
+
 // A 2-D convolution (mm_conv.hip): x is N x C x H x W, w is K x C x R x S, y is
 // N x K x P x Q, all packed; strides sh, sw, padding ph, pw, dilation dh, dw.
 struct ConvArgs {
