@@ -16,6 +16,8 @@
 // they hold no kernel leaves the rows of A and C.
 #pragma once
 
+#include <type_traits>
+
 #include "mm_internal.h"
 
 namespace mm {

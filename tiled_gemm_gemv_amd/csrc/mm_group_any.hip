@@ -129,6 +129,11 @@ hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream)
     return a.trans_b ? launch_any<ElemBf16, false, false>(a, stream) : launch_any<ElemBf16, false, true>(a, stream);
 }
 
-hipError_t group_launch(const GroupArgs &a, hipStream_t stream) { return group_any_launch(a, stream); }
+hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
+{
+    hipError_t e;
+    if (group_tile_launch(a, stream, e)) return e;
+    return group_any_launch(a, stream);
+}
 
 }  // namespace mm

@@ -1,0 +1,478 @@
+// mm_group_tile.hip -- large tiles of the grouped products and of the 8-bit integer product
+// (see mm_group.h for the sums), with panels moved HBM -> LDS by the LDS DMA.
+//
+// A workgroup computes a BM x BN tile of C in K-steps of 128 bytes of k (64 16-bit or 128 8-bit
+// elements; v_mfma_*_32x32x* takes 32 bytes of k at once, 4 steps of it). The tile is four
+// quadrants of RH x CH (halves lo, hi of its rows and columns); the waves stand in a GM x GN grid
+// over each quadrant, so a wave owns a QM x QN part of all four. A K-step is four phases, one
+// quadrant each, every phase reading one half panel from LDS into registers and multiplying it:
+//   phase 0  read A lo    A lo x B lo
+//   phase 1  read B hi    A lo x B hi
+//   phase 2  read A hi    A hi x B lo
+//   phase 3  read B lo of the next K-step    A hi x B hi
+// so that each half panel is read from LDS once per K-step and wave.
+//
+// LDS holds two K-steps as half panels. The DMA of a half panel for K-step kt + 2 goes out one
+// phase after its buffer was read for the last time (K-step kt), in the order in which the half
+// panels will be read, so up to seven half panels are on their way while one is used; a wave waits
+// with vmcnt until its own part of the half panel of the next phase has landed, and the barrier
+// that ends the phase makes that hold for every wave.
+//
+// With 8 waves (two per SIMD) the two wave rows run half a phase apart: while one row's waves
+// multiply, the other's read LDS and issue DMA, with a barrier between; the matrix cores always
+// have one wave's MFMAs.
+//
+// Operand layouts in LDS. k along the operand's rows ("D"): rows of 128 bytes, 16-byte chunk c of
+// row r in slot c ^ swz(r), an MFMA operand is one 16-byte read. k across the rows ("T": B stored
+// K x N, and both operands of the gradient): BK rows of 2 RH (2 CH) bytes as stored, an operand is
+// two ds_read_b64_tr_b16 (which transpose 16 x 4 blocks within 16 lanes: lane i receives column i
+// of the four rows that lanes 4c .. 4c + 3 addressed).
+//
+// Edges. Rows of A past the group's end, and rows of a D operand B past N, are clamped to the last
+// one; they feed only elements that are not stored. The columns of a T operand that crosses the
+// matrix' edge start earlier instead (every 16-byte chunk inside its row; elements of C left of
+// the tile's origin belong to the tile before and are not stored again), or, with fewer columns
+// than the tile (a multiple of 8 then), clamp to the last chunk. A partial K-step is run first and
+// ends at the last k: it shares its first `ov` k with the next step (or, in a group of fewer rows
+// than a K-step, reads rows before the group), and both panels are zeroed there once they have
+// landed, so that those k add 0 x 0 whatever the memory holds.
+#include "mm_group.h"
+
+namespace mm {
+namespace {
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+
+template <class E_, bool AT_, bool BT_, int RH_, int CH_, int GM_, int GN_>
+struct GroupTile {
+    typedef E_ E;
+    static constexpr bool AT = AT_, BT = BT_;
+    static constexpr int RH = RH_, CH = CH_, GM = GM_, GN = GN_, BM = 2 * RH, BN = 2 * CH;
+    static constexpr int WAVES = GM * GN, NT = 64 * WAVES;
+    static constexpr bool PP = WAVES == 8;  // two wave rows half a phase apart
+    static constexpr int QM = RH / GM, QN = CH / GN, FM = QM / 32, FN = QN / 32;
+    static constexpr int ES = sizeof(typename E::T), BK = 128 / ES;
+    static constexpr int A_HALF = RH * 128, B_HALF = CH * 128;  // bytes of a half panel
+    static constexpr int STAGE = 2 * (A_HALF + B_HALF);
+    static constexpr int A_LD = A_HALF / 1024 / WAVES, B_LD = B_HALF / 1024 / WAVES;  // 1 KB loads per wave
+    // offsets of the half panels in a stage: B lo, A lo, B hi, A hi
+    static constexpr int B_OFF[2] = {0, B_HALF + A_HALF}, A_OFF[2] = {B_HALF, 2 * B_HALF + A_HALF};
+    static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
+    static_assert(QM % 32 == 0 && QN % 32 == 0, "whole 32 x 32 blocks");
+    static_assert(!PP || GM == 2, "two wave rows");
+    static_assert(2 * STAGE <= 160 * 1024, "two stages in LDS");
+    static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
+};
+
+// D rows of 128 bytes: the 8 slots of one chunk over any 8 (16 on 64 banks) rows are distinct.
+__device__ __forceinline__ int swz_d(int row) { return ((row >> 1) & 7) ^ ((row & 1) << 2); }
+
+// T rows of W columns (2 W bytes): a transposed read touches 64 bytes of four consecutive rows (and
+// of four more 8 rows on); XOR-ing the chunk index spreads them over the bank quarters. Rows of 128
+// bytes (W = 64) span two quarters, chosen by the row's parity already.
+template <int W>
+__device__ __forceinline__ int swz_t(int krow)
+{
+    if constexpr (W == 64) return ((krow >> 1) & 1) * 4;
+    else return (krow & 3) * 4;
+}
+
+// 16 bytes per lane from base + voff into LDS at lds_addr + 16 lane (lds_addr, base wave-uniform).
+// The s_nop is the wait state that a load with LDS needs after the write of M0.
+__device__ __forceinline__ void dma16(unsigned lds_addr, const void *base, unsigned voff)
+{
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds_addr) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N >= 0 && N <= 63, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Wait until at most the loads of the `later` half panels issued last are outstanding, of which the
+// oldest is an A half if A_FIRST (A and B halves alternate).
+template <int S, int LA, int LB, bool A_FIRST>
+__device__ __forceinline__ void wait_halves(int later)
+{
+    constexpr int firsts = (S + 1) / 2, seconds = S / 2;
+    constexpr int loads = A_FIRST ? firsts * LA + seconds * LB : firsts * LB + seconds * LA;
+    if constexpr (S == 0) {
+        wait_vm<0>();
+    } else {
+        if (later >= S) wait_vm<loads>();
+        else wait_halves<S - 1, LA, LB, A_FIRST>(later);
+    }
+}
+
+__device__ __forceinline__ void end_of_slot()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <class T, bool GRAD>
+__global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
+{
+    typedef typename T::E E;
+    typedef typename E::T Elem;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
+
+    // ---- the tile: rows m0 .. m_end of C (of D_g), columns n0 .. N, the sum over k_lo .. k_end
+    const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
+    const int64_t bid = linear_block();
+    int g, m0, m_end, n0, k_lo, k_end;
+    if constexpr (GRAD) {
+        const unsigned tiles_m = (unsigned)((p.K + T::BM - 1) / T::BM);
+        const unsigned per = tiles_m * tiles_n;
+        if (bid >= (int64_t)per * p.groups) return;
+        unsigned tm, tn;
+        tile_of_group_block((unsigned)bid, per * p.groups, tiles_m * p.groups, tiles_n, tm, tn);
+        g = (int)(tm / tiles_m);
+        m0 = (int)(tm % tiles_m) * T::BM;
+        n0 = (int)tn * T::BN;
+        m_end = p.K;
+        group_range(p.offsets, g, p.M, k_lo, k_end);
+    } else {
+        const unsigned tiles_m = count_row_tiles<T::BM>(p);
+        if (bid >= (int64_t)tiles_m * tiles_n) return;
+        unsigned tm, tn;
+        tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        // offsets that decrease can count more tiles than 32 bits hold
+        RowTile t;
+        if (tn >= tiles_n || !find_row_tile<T::BM>(p, tm, t)) return;
+        g = t.g;
+        m0 = t.row0;
+        m_end = t.hi;
+        n0 = (int)tn * T::BN;
+        k_lo = 0;
+        k_end = p.K;
+    }
+    g = __builtin_amdgcn_readfirstlane(g);
+    m0 = __builtin_amdgcn_readfirstlane(m0);
+    m_end = __builtin_amdgcn_readfirstlane(m_end);
+    k_lo = __builtin_amdgcn_readfirstlane(k_lo);
+    k_end = __builtin_amdgcn_readfirstlane(k_end);
+    // origin of the panels: a T operand's columns start early enough to end inside the matrix
+    const int mb0 = T::AT ? (m_end >= T::BM ? min(m0, m_end - T::BM) : 0) : m0;
+    const int nb0 = T::BT ? (p.N >= T::BN ? min(n0, p.N - T::BN) : 0) : n0;
+
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w / T::GN, wn = w % T::GN;
+
+    const int len = k_end - k_lo;
+    const int ov = (T::BK - len % T::BK) % T::BK;
+    const int nk = (len + T::BK - 1) / T::BK;
+    const int halves = 4 * nk;
+
+    const Elem *A = static_cast<const Elem *>(p.A);
+    const Elem *B = static_cast<const Elem *>(p.B) + (GRAD ? 0 : (int64_t)g * p.stride_b);
+
+    // ---- DMA. This lane's byte offsets from the panel's corner at a K-step; the host keeps them
+    // below 2^32.
+    unsigned a_voff[2][T::A_LD], b_voff[2][T::B_LD];
+    // first k of the partial step that is below row 0 of the matrix (groups near its start): those
+    // lanes read row 0
+    auto offsets_of = [&](int k_first) {
+        const int below = k_first < 0 ? -k_first : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < T::A_LD; ++i) {
+                if constexpr (T::AT) {
+                    constexpr int CPR = T::RH / 8;  // chunks per row
+                    const int krow = (64 / CPR) * (T::A_LD * w + i) + lane / CPR;
+                    int col = mb0 + h * T::RH + 8 * ((lane % CPR) ^ swz_t<T::RH>(krow));
+                    if (m_end < T::BM) col = min(col, m_end - 8);
+                    a_voff[h][i] = (unsigned)((max(krow - below, 0) * p.lda + (col - mb0)) * 2);
+                } else {
+                    const int row = 8 * (T::A_LD * w + i) + lane / 8;
+                    const int chunk = (lane % 8) ^ swz_d(row);
+                    a_voff[h][i] = (unsigned)((min(h * T::RH + row, m_end - 1 - mb0)) * p.lda * T::ES + 16 * chunk);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < T::B_LD; ++i) {
+                if constexpr (T::BT) {
+                    constexpr int CPR = T::CH / 8;
+                    const int krow = (64 / CPR) * (T::B_LD * w + i) + lane / CPR;
+                    int col = nb0 + h * T::CH + 8 * ((lane % CPR) ^ swz_t<T::CH>(krow));
+                    if (p.N < T::BN) col = min(col, p.N - 8);
+                    b_voff[h][i] = (unsigned)((max(krow - below, 0) * p.ldb + (col - nb0)) * 2);
+                } else {
+                    const int row = 8 * (T::B_LD * w + i) + lane / 8;
+                    const int chunk = (lane % 8) ^ swz_d(row);
+                    b_voff[h][i] = (unsigned)((min(h * T::CH + row, p.N - 1 - nb0)) * p.ldb * T::ES + 16 * chunk);
+                }
+            }
+        }
+    };
+    const unsigned lds0 = (unsigned)(uintptr_t)(lds_char *)lds;
+    // half panel number 4 kt + i of the reading order (0: B lo, 1: A lo, 2: B hi, 3: A hi)
+    auto issue = [&](int kt, int i) {
+        int k0 = ov ? (kt == 0 ? k_end - T::BK : k_lo + (kt - 1) * T::BK) : k_lo + kt * T::BK;
+        if (GRAD) k0 = max(k0, 0);
+        const unsigned st = lds0 + (kt & 1) * T::STAGE;
+        if (i & 1) {
+            const int h = i >> 1;
+            const Elem *base = T::AT ? A + (int64_t)k0 * p.lda + mb0 : A + (int64_t)mb0 * p.lda + k0;
+#pragma unroll
+            for (int l = 0; l < T::A_LD; ++l) dma16(st + T::A_OFF[h] + (T::A_LD * w + l) * 1024, base, a_voff[h][l]);
+        } else {
+            const int h = i >> 1;
+            const Elem *base = T::BT ? B + (int64_t)k0 * p.ldb + nb0 : B + (int64_t)nb0 * p.ldb + k0;
+#pragma unroll
+            for (int l = 0; l < T::B_LD; ++l) dma16(st + T::B_OFF[h] + (T::B_LD * w + l) * 1024, base, b_voff[h][l]);
+        }
+    };
+
+    // ---- operand reads: 32 bytes of k (MFMA step ks) of the 32-wide block blk of a half panel
+    int d_off[4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) d_off[ks] = (lane & 31) * 128 + 16 * ((2 * ks + (lane >> 5)) ^ swz_d(lane & 31));
+    const int t_g = lane >> 4, t_j = lane & 15;
+    auto t_offset = [&](int blk, auto width) {
+        constexpr int W = decltype(width)::value;
+        const int krow = 8 * (t_g >> 1) + (t_j >> 2), col = 32 * blk + 16 * (t_g & 1) + 4 * (t_j & 3);
+        return krow * 2 * W + 16 * ((col >> 3) ^ swz_t<W>(krow)) + 8 * ((col >> 2) & 1);
+    };
+    int a_toff[T::FM], b_toff[T::FN];
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) a_toff[i] = t_offset(wm * T::FM + i, std::integral_constant<int, T::RH>());
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) b_toff[j] = t_offset(wn * T::FN + j, std::integral_constant<int, T::CH>());
+    auto read_d = [&](const lds_char *half, int blk, int ks) {
+        return *(const lds_u32x4 *)(half + blk * 4096 + d_off[ks]);
+    };
+    auto read_t = [&](const lds_char *half, int toff, int ks, int row_bytes) {
+        const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) v4i16 *)(half + toff + 16 * ks * row_bytes));
+        const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) v4i16 *)(half + toff + (16 * ks + 4) * row_bytes));
+        const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
+        return u32x4{l2[0], l2[1], h2[0], h2[1]};
+    };
+    u32x4 a[4][T::FM], b[2][4][T::FN];
+    auto read_a = [&](int kt, int h) {
+        const lds_char *half = (const lds_char *)lds + (kt & 1) * T::STAGE + T::A_OFF[h];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                if constexpr (T::AT) a[ks][i] = read_t(half, a_toff[i], ks, 2 * T::RH);
+                else a[ks][i] = read_d(half, wm * T::FM + i, ks);
+            }
+    };
+    auto read_b = [&](int kt, int h, u32x4 (&dst)[4][T::FN]) {
+        const lds_char *half = (const lds_char *)lds + (kt & 1) * T::STAGE + T::B_OFF[h];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j) {
+                if constexpr (T::BT) dst[ks][j] = read_t(half, b_toff[j], ks, 2 * T::CH);
+                else dst[ks][j] = read_d(half, wn * T::FN + j, ks);
+            }
+    };
+
+    typename E::Acc acc[2][2][T::FM][T::FN];
+#pragma unroll
+    for (int qa = 0; qa < 2; ++qa)
+#pragma unroll
+        for (int qb = 0; qb < 2; ++qb)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[qa][qb][i][j][r] = 0;
+
+    // the wave's parts of the halves that hold rows and columns of C
+    const bool rows_of[2] = {mb0 + wm * T::QM < m_end, mb0 + T::RH + wm * T::QM < m_end};
+    const bool cols_of[2] = {nb0 + wn * T::QN < p.N, nb0 + T::CH + wn * T::QN < p.N};
+    auto multiply = [&](int qa, int qb) {
+        if (!(rows_of[qa] && cols_of[qb])) return;
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j)
+                    acc[qa][qb][i][j] = E::mma(a[ks][i], b[qb][ks][j], acc[qa][qb][i][j]);
+        __builtin_amdgcn_s_setprio(0);
+    };
+    auto wait_reads = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+    // wait for this wave's part of half panel n; `issued` half panels have been issued
+    auto wait_half = [&](int n, int issued) {
+        if (n >= halves) return;
+        if (n & 1) wait_halves<6, T::A_LD, T::B_LD, false>(issued - 1 - n);
+        else wait_halves<6, T::A_LD, T::B_LD, true>(issued - 1 - n);
+    };
+
+    if (nk > 0) {
+        offsets_of(ov ? k_end - T::BK : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) issue(0, i);
+        if (GRAD && ov && k_end < T::BK) offsets_of(0);
+        if (nk > 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) issue(1, i);
+        }
+        if (ov) {
+            // zeros over the first ov k of both panels, once the whole step has landed everywhere
+            if (nk > 1) wait_vm<2 * (T::A_LD + T::B_LD)>();
+            else wait_vm<0>();
+            end_of_slot();
+            lds_char *st = (lds_char *)lds;
+            auto zero = [&](int off, int rows, bool t) {
+                for (int e = threadIdx.x; e < rows * 8; e += T::NT) {
+                    lds_u32x4 *q = (lds_u32x4 *)(st + off + 16 * e);
+                    if (t) {  // rows of k: 2 rows / 16 chunks each
+                        if (e / (rows / 8) < ov) *q = u32x4{0u, 0u, 0u, 0u};
+                    } else {
+                        const int row = e / 8, c = (e % 8) ^ swz_d(row);
+                        const int bytes = ov * T::ES - 16 * c;  // of this chunk
+                        if (bytes >= 16) {
+                            *q = u32x4{0u, 0u, 0u, 0u};
+                        } else if (bytes > 0) {
+                            u32x4 v = *q;
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) {
+                                const int z = bytes - 4 * d;  // leading bytes of word d to clear
+                                v[d] = z >= 4 ? 0u : z > 0 ? v[d] & (0xffffffffu << (8 * z)) : v[d];
+                            }
+                            *q = v;
+                        }
+                    }
+                }
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                zero(T::A_OFF[h], T::RH, T::AT);
+                zero(T::B_OFF[h], T::CH, T::BT);
+            }
+            wait_reads();
+        } else {
+            wait_half(1, min(halves, 8));
+        }
+        end_of_slot();
+        read_b(0, 0, b[0]);
+        wait_reads();
+        end_of_slot();
+        if (T::PP && wm == 1) end_of_slot();
+        for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i == 0) read_a(kt, 0);
+                if (i == 1) read_b(kt, 1, b[1]);
+                if (i == 2) read_a(kt, 1);
+                if (i == 3 && kt + 1 < nk) read_b(kt + 1, 0, b[0]);
+                if (kt + 2 < nk) issue(kt + 2, i);
+                wait_half(4 * kt + 2 + i, min(halves, 4 * (kt + 2) + i + 1));
+                wait_reads();
+                end_of_slot();
+                if (i == 0) multiply(0, 0);
+                if (i == 1) multiply(0, 1);
+                if (i == 2) multiply(1, 0);
+                if (i == 3) multiply(1, 1);
+                if (T::PP) end_of_slot();
+            }
+        }
+        if (T::PP && wm == 0) end_of_slot();
+    }
+
+    // ---- epilogue: lane l holds column l % 32 and rows 8 (r / 4) + 4 (l / 32) + r % 4 of a block
+    float *row_scale = reinterpret_cast<float *>(lds);
+    if constexpr (E::INT8) {
+        end_of_slot();  // every wave is done with the stages
+        for (int e = threadIdx.x; e < T::BM; e += T::NT) row_scale[e] = p.sa[min(m0 + e, m_end - 1)];
+        __syncthreads();
+    }
+    auto store = [&](auto out) {
+        typedef typename decltype(out)::T O;
+        O *C = static_cast<O *>(p.C) + (GRAD ? (int64_t)g * p.stride_c : 0);
+#pragma unroll
+        for (int qa = 0; qa < 2; ++qa)
+#pragma unroll
+            for (int qb = 0; qb < 2; ++qb)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j) {
+                    const int n = nb0 + qb * T::CH + wn * T::QN + 32 * j + (lane & 31);
+                    if (n >= p.N || (T::BT && n < n0)) continue;
+                    float sb = 1.f;
+                    if constexpr (E::INT8) sb = p.sb[(int64_t)g * p.stride_sb + n];
+#pragma unroll
+                    for (int i = 0; i < T::FM; ++i) {
+                        const int ml = qa * T::RH + wm * T::QM + 32 * i + 4 * (lane >> 5);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int m = mb0 + ml + 8 * (r >> 2) + (r & 3);
+                            if (m >= m_end || (T::AT && m < m0)) continue;
+                            float v = (float)acc[qa][qb][i][j][r];
+                            if constexpr (E::INT8) v = v * row_scale[ml + 8 * (r >> 2) + (r & 3)] * sb;
+                            C[(int64_t)m * p.ldc + n] = (O)v;
+                        }
+                    }
+                }
+    };
+    if (p.c_type == 0) store(OutType<0>());
+    else if (p.c_type == 1) store(OutType<1>());
+    else store(OutType<2>());
+}
+
+// The tile takes the shape: K-steps fit (or, in gradient mode, rows of any number), the columns of
+// T operands fill the tile or whole chunks, and lane offsets fit 32 bits.
+template <class T, bool GRAD>
+bool tile_ok(const GroupArgs &a)
+{
+    constexpr int64_t limit = int64_t(1) << 32;
+    constexpr int largest = 0x7fffffff - 1024;  // a tile's row and column numbers fit an int
+    if (a.M > largest || a.N > largest || a.K > largest) return false;
+    if (!GRAD && a.K < T::BK) return false;
+    if (T::AT && a.K < T::BM && a.K % 8 != 0) return false;
+    if (T::BT && a.N < T::BN && a.N % 8 != 0) return false;
+    const int64_t a_rows = T::AT ? T::BK : T::BM, b_rows = T::BT ? T::BK : T::BN;
+    return ((a_rows - 1) * a.lda + T::BM) * T::ES + 128 < limit && ((b_rows - 1) * a.ldb + T::BN) * T::ES + 128 < limit;
+}
+
+template <class T, bool GRAD>
+hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
+{
+    const int64_t tiles_n = ((int64_t)a.N + T::BN - 1) / T::BN;
+    const int64_t tiles_m = GRAD ? ((int64_t)a.K + T::BM - 1) / T::BM * a.groups : max_row_tiles(a, T::BM);
+    if (tiles_m > 0x7fffffff / tiles_n) return hipErrorInvalidConfiguration;
+    unsigned gx, gy;
+    if (!grid_for(tiles_m * tiles_n, gx, gy)) return hipErrorInvalidConfiguration;
+    GroupArgs arg = a;
+    void *args[] = {&arg};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&group_tile_kernel<T, GRAD>), dim3(gx, gy), dim3(T::NT), args,
+                           0, stream);
+}
+
+template <class E, bool AT, bool BT>
+bool try_tiles(const GroupArgs &a, hipStream_t stream, hipError_t &e)
+{
+    using Large = GroupTile<E, AT, BT, 128, 128, 2, 4>;
+    if (!tile_ok<Large, AT>(a)) return false;
+    e = launch_tile<Large, AT>(a, stream);
+    return true;
+}
+
+}  // namespace
+
+bool group_tile_launch(const GroupArgs &a, hipStream_t stream, hipError_t &e)
+{
+    const bool f16 = a.elem == GroupElem::F16;
+    if (a.elem == GroupElem::I8) return try_tiles<ElemI8, false, false>(a, stream, e);
+    if (a.grad) return f16 ? try_tiles<ElemF16, true, true>(a, stream, e) : try_tiles<ElemBf16, true, true>(a, stream, e);
+    if (a.trans_b)
+        return f16 ? try_tiles<ElemF16, false, false>(a, stream, e) : try_tiles<ElemBf16, false, false>(a, stream, e);
+    return f16 ? try_tiles<ElemF16, false, true>(a, stream, e) : try_tiles<ElemBf16, false, true>(a, stream, e);
+}
+
+}  // namespace mm

@@ -163,6 +163,9 @@ struct GroupArgs {
 };
 // The kernel for the shape; M, N, groups >= 1 (gradient mode: K, N, groups >= 1).
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream);
+// Tiles with panels loaded straight into LDS (mm_group_tile.hip): false where they do not take
+// the shape (nothing is enqueued then); e is the launch's result otherwise.
+bool group_tile_launch(const GroupArgs &a, hipStream_t stream, hipError_t &e);
 // Any shape and alignment (mm_group_any.hip).
 hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream);
 
