@@ -3,24 +3,21 @@
 //
 // A workgroup computes a BM x BN tile of C in K-steps of 128 bytes of k (64 16-bit or 128 8-bit
 // elements; v_mfma_*_32x32x* takes 32 bytes of k at once, 4 steps of it). The tile is four
-// quadrants of RH x CH (halves lo, hi of its rows and columns); the waves stand in a GM x GN grid
+// quadrants of RH x CH (halves lo, hi of its rows and columns); the 4 waves stand in a 2 x 2 grid
 // over each quadrant, so a wave owns a QM x QN part of all four. A K-step is four phases, one
-// quadrant each, every phase reading one half panel from LDS into registers and multiplying it:
-//   phase 0  read A lo    A lo x B lo
-//   phase 1  read B hi    A lo x B hi
-//   phase 2  read A hi    A hi x B lo
-//   phase 3  read B lo of the next K-step    A hi x B hi
-// so that each half panel is read from LDS once per K-step and wave.
+// quadrant each; every phase multiplies operands that are in registers and reads the half panel
+// that a phase after it needs from LDS, between its MFMAs:
+//   phase 0  A lo x B lo    reads B hi
+//   phase 1  A lo x B hi    reads A hi
+//   phase 2  A hi x B hi    reads A lo of the next K-step
+//   phase 3  A hi x B lo    reads B lo of the next K-step, into the registers of B hi
+// so each half panel is read from LDS once per K-step and wave, and the reads are spread evenly.
 //
-// LDS holds two K-steps as half panels. The DMA of a half panel for K-step kt + 2 goes out one
-// phase after its buffer was read for the last time (K-step kt), in the order in which the half
-// panels will be read, so up to seven half panels are on their way while one is used; a wave waits
-// with vmcnt until its own part of the half panel of the next phase has landed, and the barrier
-// that ends the phase makes that hold for every wave.
-//
-// With 8 waves (two per SIMD) the two wave rows run half a phase apart: while one row's waves
-// multiply, the other's read LDS and issue DMA, with a barrier between; the matrix cores always
-// have one wave's MFMAs.
+// LDS holds two K-steps as half panels. The buffer of a half panel is free once every wave has
+// read it; the DMA for the same half two K-steps on goes out one phase later, so six half panels
+// are on their way while one is read. A phase has one barrier, a few MFMAs into it: before it a
+// wave waits until its own loads of the half panel to be read have landed (vmcnt) and until its
+// reads of the phase before are done (lgkmcnt), so that after it both hold for every wave.
 //
 // Operand layouts in LDS. k along the operand's rows ("D"): rows of 128 bytes, 16-byte chunk c of
 // row r in slot c ^ swz(r), an MFMA operand is one 16-byte read. k across the rows ("T": B stored
@@ -51,19 +48,18 @@ struct GroupTile {
     static constexpr bool AT = AT_, BT = BT_;
     static constexpr int RH = RH_, CH = CH_, GM = GM_, GN = GN_, BM = 2 * RH, BN = 2 * CH;
     static constexpr int WAVES = GM * GN, NT = 64 * WAVES;
-    static constexpr bool PP = WAVES == 8;  // two wave rows half a phase apart
     static constexpr int QM = RH / GM, QN = CH / GN, FM = QM / 32, FN = QN / 32;
     static constexpr int ES = sizeof(typename E::T), BK = 128 / ES;
     static constexpr int A_HALF = RH * 128, B_HALF = CH * 128;  // bytes of a half panel
     static constexpr int STAGE = 2 * (A_HALF + B_HALF);
     static constexpr int A_LD = A_HALF / 1024 / WAVES, B_LD = B_HALF / 1024 / WAVES;  // 1 KB loads per wave
-    // offsets of the half panels in a stage: B lo, A lo, B hi, A hi
-    static constexpr int B_OFF[2] = {0, B_HALF + A_HALF}, A_OFF[2] = {B_HALF, 2 * B_HALF + A_HALF};
+    // offsets of the half panels in a stage
+    static constexpr int A_OFF[2] = {0, A_HALF}, B_OFF[2] = {2 * A_HALF, 2 * A_HALF + B_HALF};
     static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
     static_assert(QM % 32 == 0 && QN % 32 == 0, "whole 32 x 32 blocks");
-    static_assert(!PP || GM == 2, "two wave rows");
     static_assert(2 * STAGE <= 160 * 1024, "two stages in LDS");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
+    static_assert((!AT || RH >= 64) && (!BT || CH >= 64), "T rows of at least the 8 chunks that swz_t permutes");
 };
 
 // D rows of 128 bytes: the 8 slots of one chunk over any 8 (16 on 64 banks) rows are distinct.
@@ -75,6 +71,7 @@ __device__ __forceinline__ int swz_d(int row) { return ((row >> 1) & 7) ^ ((row 
 template <int W>
 __device__ __forceinline__ int swz_t(int krow)
 {
+    static_assert(W == 64 || W == 128, "rows of 8 or 16 chunks: the permuted index stays inside the row");
     if constexpr (W == 64) return ((krow >> 1) & 1) * 4;
     else return (krow & 3) * 4;
 }
@@ -93,25 +90,33 @@ __device__ __forceinline__ void wait_vm()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Wait until at most the loads of the `later` half panels issued last are outstanding, of which the
-// oldest is an A half if A_FIRST (A and B halves alternate).
-template <int S, int LA, int LB, bool A_FIRST>
+// Loads per wave of the S half panels after number n (n % 4 == N4) of the order A lo, B lo, B hi,
+// A hi, ...
+template <class T, int N4, int S>
+constexpr int loads_after()
+{
+    int sum = 0;
+    for (int i = 1; i <= S; ++i) sum += ((N4 + i) % 4 == 0 || (N4 + i) % 4 == 3) ? T::A_LD : T::B_LD;
+    return sum;
+}
+
+// Wait until at most the min(later, S) half panels issued after number n are outstanding.
+template <class T, int N4, int S>
 __device__ __forceinline__ void wait_halves(int later)
 {
-    constexpr int firsts = (S + 1) / 2, seconds = S / 2;
-    constexpr int loads = A_FIRST ? firsts * LA + seconds * LB : firsts * LB + seconds * LA;
     if constexpr (S == 0) {
         wait_vm<0>();
     } else {
-        if (later >= S) wait_vm<loads>();
-        else wait_halves<S - 1, LA, LB, A_FIRST>(later);
+        if (later >= S) wait_vm<loads_after<T, N4, S>()>();
+        else wait_halves<T, N4, S - 1>(later);
     }
 }
 
-__device__ __forceinline__ void end_of_slot()
+// A barrier that waits for no memory by itself.
+__device__ __forceinline__ void bare_barrier()
 {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
+    asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -130,10 +135,11 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         const unsigned tiles_m = (unsigned)((p.K + T::BM - 1) / T::BM);
         const unsigned per = tiles_m * tiles_n;
         if (bid >= (int64_t)per * p.groups) return;
+        // each group's tiles over all XCDs: the groups' sums differ in length
         unsigned tm, tn;
-        tile_of_group_block((unsigned)bid, per * p.groups, tiles_m * p.groups, tiles_n, tm, tn);
-        g = (int)(tm / tiles_m);
-        m0 = (int)(tm % tiles_m) * T::BM;
+        g = (int)((unsigned)bid / per);
+        tile_of_group_block((unsigned)bid - g * per, per, tiles_m, tiles_n, tm, tn);
+        m0 = (int)tm * T::BM;
         n0 = (int)tn * T::BN;
         m_end = p.K;
         group_range(p.offsets, g, p.M, k_lo, k_end);
@@ -213,22 +219,24 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         }
     };
     const unsigned lds0 = (unsigned)(uintptr_t)(lds_char *)lds;
-    // half panel number 4 kt + i of the reading order (0: B lo, 1: A lo, 2: B hi, 3: A hi)
-    auto issue = [&](int kt, int i) {
+    // half panel number 4 kt + i of the reading order (0: A lo, 1: B lo, 2: B hi, 3: A hi)
+    auto issue_one = [&](int kt, int i, int l) {  // load l of it
         int k0 = ov ? (kt == 0 ? k_end - T::BK : k_lo + (kt - 1) * T::BK) : k_lo + kt * T::BK;
         if (GRAD) k0 = max(k0, 0);
         const unsigned st = lds0 + (kt & 1) * T::STAGE;
-        if (i & 1) {
-            const int h = i >> 1;
+        if (i == 0 || i == 3) {
+            const int h = i == 3;
             const Elem *base = T::AT ? A + (int64_t)k0 * p.lda + mb0 : A + (int64_t)mb0 * p.lda + k0;
-#pragma unroll
-            for (int l = 0; l < T::A_LD; ++l) dma16(st + T::A_OFF[h] + (T::A_LD * w + l) * 1024, base, a_voff[h][l]);
+            dma16(st + T::A_OFF[h] + (T::A_LD * w + l) * 1024, base, a_voff[h][l]);
         } else {
-            const int h = i >> 1;
+            const int h = i - 1;
             const Elem *base = T::BT ? B + (int64_t)k0 * p.ldb + nb0 : B + (int64_t)nb0 * p.ldb + k0;
-#pragma unroll
-            for (int l = 0; l < T::B_LD; ++l) dma16(st + T::B_OFF[h] + (T::B_LD * w + l) * 1024, base, b_voff[h][l]);
+            dma16(st + T::B_OFF[h] + (T::B_LD * w + l) * 1024, base, b_voff[h][l]);
         }
+    };
+    auto issue = [&](int kt, int i) {
+#pragma unroll
+        for (int l = 0; l < (i == 0 || i == 3 ? T::A_LD : T::B_LD); ++l) issue_one(kt, i, l);
     };
 
     // ---- operand reads: 32 bytes of k (MFMA step ks) of the 32-wide block blk of a half panel
@@ -257,26 +265,18 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
         return u32x4{l2[0], l2[1], h2[0], h2[1]};
     };
-    u32x4 a[4][T::FM], b[2][4][T::FN];
-    auto read_a = [&](int kt, int h) {
-        const lds_char *half = (const lds_char *)lds + (kt & 1) * T::STAGE + T::A_OFF[h];
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int i = 0; i < T::FM; ++i) {
-                if constexpr (T::AT) a[ks][i] = read_t(half, a_toff[i], ks, 2 * T::RH);
-                else a[ks][i] = read_d(half, wm * T::FM + i, ks);
-            }
+    // operands: a[0], a[1]: A lo, A hi; b[s], b[s ^ 1]: B lo, B hi in a K-step of parity s
+    u32x4 a[2][4][T::FM], b[2][4][T::FN];
+    // operand number r (of 4 FM, 4 FN) of a half panel
+    auto read_a = [&](const lds_char *half, int r, u32x4 (&dst)[4][T::FM]) {
+        const int ks = r / T::FM, i = r % T::FM;
+        if constexpr (T::AT) dst[ks][i] = read_t(half, a_toff[i], ks, 2 * T::RH);
+        else dst[ks][i] = read_d(half, wm * T::FM + i, ks);
     };
-    auto read_b = [&](int kt, int h, u32x4 (&dst)[4][T::FN]) {
-        const lds_char *half = (const lds_char *)lds + (kt & 1) * T::STAGE + T::B_OFF[h];
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int j = 0; j < T::FN; ++j) {
-                if constexpr (T::BT) dst[ks][j] = read_t(half, b_toff[j], ks, 2 * T::CH);
-                else dst[ks][j] = read_d(half, wn * T::FN + j, ks);
-            }
+    auto read_b = [&](const lds_char *half, int r, u32x4 (&dst)[4][T::FN]) {
+        const int ks = r / T::FN, j = r % T::FN;
+        if constexpr (T::BT) dst[ks][j] = read_t(half, b_toff[j], ks, 2 * T::CH);
+        else dst[ks][j] = read_d(half, wn * T::FN + j, ks);
     };
 
     typename E::Acc acc[2][2][T::FM][T::FN];
@@ -291,27 +291,56 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[qa][qb][i][j][r] = 0;
 
-    // the wave's parts of the halves that hold rows and columns of C
-    const bool rows_of[2] = {mb0 + wm * T::QM < m_end, mb0 + T::RH + wm * T::QM < m_end};
-    const bool cols_of[2] = {nb0 + wn * T::QN < p.N, nb0 + T::CH + wn * T::QN < p.N};
-    auto multiply = [&](int qa, int qb) {
-        if (!(rows_of[qa] && cols_of[qb])) return;
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-                for (int j = 0; j < T::FN; ++j)
-                    acc[qa][qb][i][j] = E::mma(a[ks][i], b[qb][ks][j], acc[qa][qb][i][j]);
-        __builtin_amdgcn_s_setprio(0);
-    };
     auto wait_reads = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-    // wait for this wave's part of half panel n; `issued` half panels have been issued
-    auto wait_half = [&](int n, int issued) {
-        if (n >= halves) return;
-        if (n & 1) wait_halves<6, T::A_LD, T::B_LD, false>(issued - 1 - n);
-        else wait_halves<6, T::A_LD, T::B_LD, true>(issued - 1 - n);
+
+    // One phase: I of a K-step of parity S. FULL: every half panel that the phase issues and waits
+    // for exists.
+    auto phase = [&](int kt, auto I_, auto S_, auto FULL_) {
+        constexpr int I = decltype(I_)::value, S = decltype(S_)::value;
+        constexpr bool FULL = decltype(FULL_)::value;
+        constexpr int qa = I >= 2, qb = I == 1 || I == 2;
+        constexpr bool reads_a = I == 1 || I == 2;
+        constexpr int NM = 4 * T::FM * T::FN, NR = 4 * (reads_a ? T::FM : T::FN);
+        constexpr int issues = (I + 1) % 4;  // the half panel issued: A lo in phase 3, B lo, B hi, A hi
+        constexpr int NL = issues == 0 || issues == 3 ? T::A_LD : T::B_LD;
+        constexpr int pre = NM / 8;          // MFMAs before the barrier
+        // the reads and loads, mixed evenly, spread evenly over the MFMAs after the barrier
+        constexpr int items = NR + NL, slots = NM - pre;
+        const int stage = ((kt + (I >= 2)) & 1) * T::STAGE;
+        const lds_char *half = (const lds_char *)lds + stage +
+                               (reads_a ? T::A_OFF[I == 1] : T::B_OFF[I == 0]);
+        auto mfma = [&](int m) {
+            const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
+            acc[qa][qb][i][j] = E::mma(a[qa][ks][i], b[S ^ qb][ks][j], acc[qa][qb][i][j]);
+        };
+        auto read = [&](int r) {
+            if constexpr (reads_a) read_a(half, r, a[I == 1]);
+            else read_b(half, r, b[S ^ 1]);
+        };
+#pragma unroll
+        for (int m = 0; m < pre; ++m) mfma(m);
+        const int n = 4 * kt + 2 + I, issued = 4 * kt + 9 + I;
+        if (FULL) wait_vm<loads_after<T, (2 + I) % 4, 6>()>();
+        else if (n < halves) wait_halves<T, (2 + I) % 4, 6>(min(issued, halves) - 1 - n);
+        wait_reads();
+        bare_barrier();
+#pragma unroll
+        for (int m = pre; m < NM; ++m) {
+#pragma unroll
+            for (int t = (m - pre) * items / slots; t < (m - pre + 1) * items / slots; ++t) {
+                const int l = t * NL / items;  // loads among the items before t
+                if ((t + 1) * NL / items == l) read(t - l);
+                else if (FULL || issued < halves) issue_one(kt + 2 + (I == 3), issues, l);
+            }
+            mfma(m);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto k_step = [&](int kt, auto S, auto FULL) {
+        phase(kt, std::integral_constant<int, 0>(), S, FULL);
+        phase(kt, std::integral_constant<int, 1>(), S, FULL);
+        phase(kt, std::integral_constant<int, 2>(), S, FULL);
+        phase(kt, std::integral_constant<int, 3>(), S, FULL);
     };
 
     if (nk > 0) {
@@ -327,7 +356,7 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
             // zeros over the first ov k of both panels, once the whole step has landed everywhere
             if (nk > 1) wait_vm<2 * (T::A_LD + T::B_LD)>();
             else wait_vm<0>();
-            end_of_slot();
+            bare_barrier();
             lds_char *st = (lds_char *)lds;
             auto zero = [&](int off, int rows, bool t) {
                 for (int e = threadIdx.x; e < rows * 8; e += T::NT) {
@@ -358,38 +387,34 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
             }
             wait_reads();
         } else {
-            wait_half(1, min(halves, 8));
+            wait_halves<T, 1, 6>(min(halves, 8) - 2);
         }
-        end_of_slot();
-        read_b(0, 0, b[0]);
-        wait_reads();
-        end_of_slot();
-        if (T::PP && wm == 1) end_of_slot();
-        for (int kt = 0; kt < nk; ++kt) {
+        bare_barrier();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i == 0) read_a(kt, 0);
-                if (i == 1) read_b(kt, 1, b[1]);
-                if (i == 2) read_a(kt, 1);
-                if (i == 3 && kt + 1 < nk) read_b(kt + 1, 0, b[0]);
-                if (kt + 2 < nk) issue(kt + 2, i);
-                wait_half(4 * kt + 2 + i, min(halves, 4 * (kt + 2) + i + 1));
-                wait_reads();
-                end_of_slot();
-                if (i == 0) multiply(0, 0);
-                if (i == 1) multiply(0, 1);
-                if (i == 2) multiply(1, 0);
-                if (i == 3) multiply(1, 1);
-                if (T::PP) end_of_slot();
-            }
+        for (int r = 0; r < 4 * T::FM; ++r) read_a((const lds_char *)lds + T::A_OFF[0], r, a[0]);
+#pragma unroll
+        for (int r = 0; r < 4 * T::FN; ++r) read_b((const lds_char *)lds + T::B_OFF[0], r, b[0]);
+        wait_reads();
+        bare_barrier();
+        if (nk > 2) issue(2, 0);
+        using S0 = std::integral_constant<int, 0>;
+        using S1 = std::integral_constant<int, 1>;
+        int kt = 0;
+        for (; kt + 4 < nk; kt += 2) {
+            k_step(kt, S0(), std::true_type());
+            k_step(kt + 1, S1(), std::true_type());
         }
-        if (T::PP && wm == 0) end_of_slot();
+        for (; kt < nk; kt += 2) {
+            k_step(kt, S0(), std::false_type());
+            if (kt + 1 < nk) k_step(kt + 1, S1(), std::false_type());
+        }
     }
 
     // ---- epilogue: lane l holds column l % 32 and rows 8 (r / 4) + 4 (l / 32) + r % 4 of a block
     float *row_scale = reinterpret_cast<float *>(lds);
     if constexpr (E::INT8) {
-        end_of_slot();  // every wave is done with the stages
+        wait_reads();
+        bare_barrier();  // every wave is done with the stages
         for (int e = threadIdx.x; e < T::BM; e += T::NT) row_scale[e] = p.sa[min(m0 + e, m_end - 1)];
         __syncthreads();
     }
