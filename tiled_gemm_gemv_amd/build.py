@@ -18,7 +18,8 @@ SOURCES = ["mm_api.hip", "mm_gemm.hip", "mm_gemm_direct.hip", "mm_gemm_skinny.hi
            "mm_gemm_h16.hip", "mm_gemm_narrow.hip",
            "mm_conv.hip",
            "mm_gemv.hip", "mm_gemv_t.hip", "mm_static_ws.hip",
-           "mm_group_any.hip", "mm_group_tile.hip", "mm_quantize.hip"]
+           "mm_group_any.hip", "mm_group_tile.hip", "mm_group_rows.hip",
+           "mm_quantize.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

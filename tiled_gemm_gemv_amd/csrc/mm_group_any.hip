@@ -131,6 +131,12 @@ hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream)
 
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
 {
+    constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
+    if (a.M <= largest && a.N <= largest) {
+        const int64_t mean = a.offsets ? ((int64_t)a.M + a.groups - 1) / a.groups : a.M;
+        const int64_t rows = a.offsets && 2 * mean < a.M ? 2 * mean : a.M;
+        if (!a.grad && rows <= 64) return group_rows_launch(a, (int)rows, stream);
+    }
     hipError_t e;
     if (group_tile_launch(a, stream, e)) return e;
     return group_any_launch(a, stream);

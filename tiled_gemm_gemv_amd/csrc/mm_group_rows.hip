@@ -1,0 +1,335 @@
+// mm_group_rows.hip -- grouped products and the 8-bit product with few rows per group (decoding):
+// see mm_group.h for the sums.
+//
+// With up to 16 RB rows to a group the product is a stream of B: 2 (1) bytes of B for every
+// 2 x rows FLOP. B goes from memory straight into the registers that feed the MFMA, no LDS and no
+// barrier in the loop, so every wave keeps its own loads in flight; all waves of a workgroup share
+// the columns, each takes every W-th slice of k, and at the end their partial sums are added in LDS
+// in wave order. v_mfma_f32_16x16x32_* and v_mfma_i32_16x16x64_i8 take 64 bytes of k: lane l
+// supplies the 16 bytes at k byte 16 (l / 16) of row (column) l % 16.
+//
+//   B rows along k (stored N x K): lane l reads the 16 bytes of its column itself: 16 columns x
+//     128 bytes of k per slice.
+//   B rows across k (stored K x N): lane l reads 16 bytes (8 columns) of each of the 8 rows
+//     8 (l / 16) .. + 7 of a slice of 32 k; 128 columns. The MFMA for column 8 i + c wants those 8
+//     rows of one column: a pair of rows is one v_perm_b32, 32 of them for the 64 values.
+// A's rows come from L2 (every workgroup of a group reads the same rows); rows past the group's end
+// repeat its last row and are not stored.
+#include "mm_group.h"
+
+namespace mm {
+namespace {
+
+// 16x16 MFMAs: the accumulator of lane l holds column l % 16 and rows 4 (l / 16) + r, r = 0..3
+struct Rows16Bf16 : ElemBf16 {
+    typedef f32x4 Acc4;
+    static __device__ __forceinline__ Acc4 mma4(u32x4 a, u32x4 b, Acc4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    }
+};
+struct Rows16F16 : ElemF16 {
+    typedef f32x4 Acc4;
+    static __device__ __forceinline__ Acc4 mma4(u32x4 a, u32x4 b, Acc4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
+    }
+};
+struct Rows16I8 : ElemI8 {
+    typedef i32x4 Acc4;
+    static __device__ __forceinline__ Acc4 mma4(u32x4 a, u32x4 b, Acc4 c)
+    {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0,
+                                                     0, 0);
+    }
+};
+
+// 16 bytes from any address
+__device__ __forceinline__ u32x4 load16(const char *p)
+{
+    struct __attribute__((packed)) Bytes {
+        u32x4 v;
+    };
+    return reinterpret_cast<const Bytes *>(p)->v;
+}
+
+// The first `valid` bytes (a multiple of the element size) at p, zeros after; no other byte is read.
+template <class Elem>
+__device__ __forceinline__ u32x4 load16_upto(const char *p, int valid)
+{
+    if (valid >= 16) return load16(p);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    constexpr int es = sizeof(Elem);
+#pragma unroll
+    for (int e = 0; e < 16 / es; ++e)
+        if (e * es < valid) {
+            const unsigned x = es == 1 ? (unsigned)*reinterpret_cast<const unsigned char *>(p + e)
+                                       : (unsigned)*reinterpret_cast<const unsigned short *>(p + 2 * e);
+            v[e * es / 4] |= x << (8 * (e * es % 4));
+        }
+    return v;
+}
+
+// Partial sums of the W waves added in wave order and stored. `mine` holds NC x 4 values per lane:
+// value (c, r) is row 4 (lane / 16) + r, column COLS_C * (lane % 16) + c  (columns 16 c + lane % 16
+// where COLS_C is 0).
+template <class E, int W, int NC, int COLS_C>
+__device__ __forceinline__ void join_and_store(const GroupArgs &p, const typename E::Acc4 (&mine)[NC], char *lds, int g,
+                                               int row0, int row_end, int n0)
+{
+    typedef decltype(mine[0][0] + 0) V;
+    V *part = reinterpret_cast<V *>(lds);  // [wave][row][column]
+    constexpr int COLS = 16 * NC;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int col = COLS_C ? COLS_C * (lane & 15) + c : 16 * c + (lane & 15);
+            part[(w * 16 + 4 * (lane >> 4) + r) * COLS + col] = mine[c][r];
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * COLS; e += 64 * W) {
+        const int row = row0 + e / COLS;
+        const int64_t n = (int64_t)n0 + e % COLS;
+        if (row >= row_end || n >= p.N) continue;
+        V sum = part[e];
+#pragma unroll
+        for (int i = 1; i < W; ++i) sum += part[i * 16 * COLS + e];
+        float v = (float)sum;
+        if constexpr (E::INT8) v = v * p.sa[row] * p.sb[(int64_t)g * p.stride_sb + n];
+        const int64_t at = (int64_t)row * p.ldc + n;
+        if (p.c_type == 0) static_cast<float *>(p.C)[at] = v;
+        else if (p.c_type == 1) static_cast<__bf16 *>(p.C)[at] = (__bf16)v;
+        else static_cast<_Float16 *>(p.C)[at] = (_Float16)v;
+    }
+    __syncthreads();
+}
+
+// The workgroup's row tile (16 RB rows of a group) and strip of columns; false: none.
+template <int ROWS>
+__device__ __forceinline__ bool rows_tile(const GroupArgs &p, int cols, RowTile &t, int &n0)
+{
+    const unsigned strips = (unsigned)(((int64_t)p.N + cols - 1) / cols);
+    const int64_t bid = linear_block();
+    const int64_t rt = bid / strips;
+    if (rt > 0x7fffffff || !find_row_tile<ROWS>(p, (unsigned)rt, t)) return false;
+    n0 = (int)((unsigned)(bid - rt * strips) * (unsigned)cols);
+    t.g = __builtin_amdgcn_readfirstlane(t.g);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.hi = __builtin_amdgcn_readfirstlane(t.hi);
+    return true;
+}
+
+// B rows along k. W waves, 16 NB columns, slices of 128 bytes of k, J of them in flight.
+template <class E, int RB, int NB, int W, int J>
+__global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
+{
+    typedef typename E::T T;
+    __shared__ __attribute__((aligned(16))) char lds[W * 16 * 16 * NB * 4];
+    RowTile t;
+    int n0;
+    if (!rows_tile<16 * RB>(p, 16 * NB, t, n0)) return;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t kb = (int64_t)p.K * sizeof(T);  // bytes along k
+    const char *a[RB], *b[NB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+        a[i] = static_cast<const char *>(p.A) +
+               (int64_t)min(t.row0 + 16 * i + (lane & 15), t.hi - 1) * p.lda * (int)sizeof(T) + 16 * (lane >> 4);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+        b[j] = static_cast<const char *>(p.B) +
+               (t.g * p.stride_b + min((int64_t)n0 + 16 * j + (lane & 15), (int64_t)p.N - 1) * p.ldb) * (int)sizeof(T) +
+               16 * (lane >> 4);
+    typename E::Acc4 acc[RB][NB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = typename E::Acc4{0, 0, 0, 0};
+
+    const int64_t whole = kb / 128;  // whole slices; wave w takes w, w + W, ...
+    u32x4 av[J][2][RB], bv[J][2][NB];
+    int64_t s = w;
+    auto load = [&](int x, int64_t slice) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) bv[x][h][j] = load16(b[j] + slice * 128 + 64 * h);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) av[x][h][i] = load16(a[i] + slice * 128 + 64 * h);
+        }
+    };
+    auto multiply = [&](int x) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) acc[i][j] = E::mma4(av[x][h][i], bv[x][h][j], acc[i][j]);
+    };
+    // J slices loaded ahead; a slice is multiplied, then its registers take the slice J further on
+    if (whole > 0) {
+#pragma unroll
+        for (int x = 0; x < J; ++x) load(x, min(s + (int64_t)x * W, whole - 1));
+        while (s < whole) {
+#pragma unroll
+            for (int x = 0; x < J; ++x) {
+                if (s < whole) multiply(x);
+                if (s + (int64_t)J * W < whole) load(x, s + (int64_t)J * W);
+                s += W;
+            }
+        }
+    }
+    if (kb % 128 != 0 && whole % W == w) {  // the partial slice
+        const int64_t at = whole * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int valid = (int)(kb - at) - 64 * h - 16 * (lane >> 4);
+            u32x4 aa[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) aa[i] = load16_upto<T>(a[i] + at + 64 * h, valid);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const u32x4 bb = load16_upto<T>(b[j] + at + 64 * h, valid);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) acc[i][j] = E::mma4(aa[i], bb, acc[i][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+        join_and_store<E, W, NB, 0>(p, acc[i], lds, t.g, t.row0 + 16 * i, t.hi, n0);
+}
+
+// B rows across k (16-bit elements). W waves, 128 columns, slices of 32 k, J of them in flight.
+template <class E, int RB, int W, int J>
+__global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
+{
+    typedef typename E::T T;
+    __shared__ __attribute__((aligned(16))) char lds[W * 16 * 128 * 4];
+    RowTile t;
+    int n0;
+    if (!rows_tile<16 * RB>(p, 128, t, n0)) return;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const T *a[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+        a[i] = static_cast<const T *>(p.A) + (int64_t)min(t.row0 + 16 * i + (lane & 15), t.hi - 1) * p.lda +
+               8 * (lane >> 4);
+    const int64_t col = (int64_t)n0 + 8 * (lane & 15);
+    const bool full = (int64_t)n0 + 128 <= p.N;  // the strip's columns all exist
+    const int cols = full ? 8 : (int)max((int64_t)0, min((int64_t)8, p.N - col));
+    const T *b = static_cast<const T *>(p.B) + t.g * p.stride_b + (int64_t)(8 * (lane >> 4)) * p.ldb + (cols > 0 ? col : 0);
+    typename E::Acc4 acc[RB][8];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[i][c] = typename E::Acc4{0, 0, 0, 0};
+
+    u32x4 av[J][RB], bv[J][8];
+    auto load = [&](int x, int slice) {
+        const int64_t k0 = (int64_t)slice * 32;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const char *q = reinterpret_cast<const char *>(b + (k0 + r) * p.ldb);
+            bv[x][r] = full ? load16(q) : load16_upto<T>(q, 2 * cols);
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) av[x][i] = load16(reinterpret_cast<const char *>(a[i] + k0));
+    };
+    auto multiply = [&](const u32x4 (&aa)[RB], const u32x4 (&bb)[8]) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            u32x4 o;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o[q] = __builtin_amdgcn_perm(bb[2 * q + 1][c >> 1], bb[2 * q][c >> 1],
+                                             (c & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) acc[i][c] = E::mma4(aa[i], o, acc[i][c]);
+        }
+    };
+    const int whole = p.K / 32;
+    if (whole > 0) {
+        int s = w;
+#pragma unroll
+        for (int x = 0; x < J; ++x) load(x, min(s + x * W, whole - 1));
+        while (s < whole) {
+#pragma unroll
+            for (int x = 0; x < J; ++x) {
+                if (s < whole) multiply(av[x], bv[x]);
+                if (s < whole - J * W) load(x, s + J * W);
+                s += W;
+            }
+        }
+    }
+    if (p.K % 32 != 0 && whole % W == w) {  // the partial slice
+        const int64_t k0 = (int64_t)whole * 32;
+        const int left = p.K - whole * 32 - 8 * (lane >> 4);  // of this lane's 8 k
+        u32x4 aa[RB], bb[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            bb[r] = load16_upto<T>(reinterpret_cast<const char *>(b + (k0 + r) * p.ldb), r < left ? 2 * cols : 0);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) aa[i] = load16_upto<T>(reinterpret_cast<const char *>(a[i] + k0), 2 * left);
+        multiply(aa, bb);
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+        join_and_store<E, W, 8, 8>(p, acc[i], lds, t.g, t.row0 + 16 * i, t.hi, n0);
+}
+
+template <int ROWS>
+hipError_t launch_rows(const void *fn, const GroupArgs &a, int cols, int waves, hipStream_t stream)
+{
+    const int64_t strips = ((int64_t)a.N + cols - 1) / cols, tiles = max_row_tiles(a, ROWS);
+    if (tiles > INT64_MAX / strips) return hipErrorInvalidConfiguration;
+    unsigned gx, gy;
+    if (!grid_for(tiles * strips, gx, gy)) return hipErrorInvalidConfiguration;
+    GroupArgs arg = a;
+    void *args[] = {&arg};
+    return hipLaunchKernel(fn, dim3(gx, gy), dim3(64 * waves), args, 0, stream);
+}
+
+template <class E, int RB, int NB, int W, int J>
+hipError_t launch_d(const GroupArgs &a, hipStream_t stream)
+{
+    return launch_rows<16 * RB>(reinterpret_cast<const void *>(&rows_kernel_d<E, RB, NB, W, J>), a, 16 * NB, W, stream);
+}
+
+template <class E, int RB, int W, int J>
+hipError_t launch_t(const GroupArgs &a, hipStream_t stream)
+{
+    return launch_rows<16 * RB>(reinterpret_cast<const void *>(&rows_kernel_t<E, RB, W, J>), a, 128, W, stream);
+}
+
+template <class E>
+hipError_t rows_d(const GroupArgs &a, int rows, hipStream_t stream)
+{
+    if (rows <= 16) return launch_d<E, 1, 1, 4, 4>(a, stream);
+    if (rows <= 32) return launch_d<E, 2, 2, 4, 2>(a, stream);
+    return launch_d<E, 4, 2, 4, 2>(a, stream);
+}
+
+template <class E>
+hipError_t rows_t(const GroupArgs &a, int rows, hipStream_t stream)
+{
+    if (rows <= 16) return launch_t<E, 1, 8, 2>(a, stream);
+    if (rows <= 32) return launch_t<E, 2, 8, 2>(a, stream);
+    return launch_t<E, 4, 8, 1>(a, stream);
+}
+
+}  // namespace
+
+hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream)
+{
+    if (a.elem == GroupElem::I8) return rows_d<Rows16I8>(a, rows, stream);
+    if (a.trans_b)
+        return a.elem == GroupElem::F16 ? rows_d<Rows16F16>(a, rows, stream) : rows_d<Rows16Bf16>(a, rows, stream);
+    return a.elem == GroupElem::F16 ? rows_t<Rows16F16>(a, rows, stream) : rows_t<Rows16Bf16>(a, rows, stream);
+}
+
+}  // namespace mm

@@ -33,6 +33,8 @@
 // ends at the last k: it shares its first `ov` k with the next step (or, in a group of fewer rows
 // than a K-step, reads rows before the group), and both panels are zeroed there once they have
 // landed, so that those k add 0 x 0 whatever the memory holds.
+#include <math.h>
+
 #include "mm_group.h"
 
 namespace mm {
@@ -480,12 +482,30 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
 }
 
 template <class E, bool AT, bool BT>
-bool try_tiles(const GroupArgs &a, hipStream_t stream, hipError_t &e)
+bool try_tiles(int tile, const GroupArgs &a, hipStream_t stream, hipError_t &e)
 {
     using Large = GroupTile<E, AT, BT, 128, 128, 2, 4>;
-    if (!tile_ok<Large, AT>(a)) return false;
-    e = launch_tile<Large, AT>(a, stream);
+    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 2>;
+    if (tile == 0 && tile_ok<Large, AT>(a)) e = launch_tile<Large, AT>(a, stream);
+    else if (tile_ok<Mid, AT>(a)) e = launch_tile<Mid, AT>(a, stream);
+    else return false;
     return true;
+}
+
+// 0: 256 x 256 tiles, 1: 128 x 128
+int choose_tile(const GroupArgs &a)
+{
+    const double groups = a.offsets ? (double)(a.groups < a.M ? a.groups : a.M) : 1.0;
+    auto tiles = [&](int t) {
+        const double n = (double)(((int64_t)a.N + t - 1) / t);
+        if (a.grad) return n * (double)(((int64_t)a.K + t - 1) / t) * a.groups;
+        if (!a.offsets) return n * (double)(((int64_t)a.M + t - 1) / t);
+        return n * ((double)a.M / t + groups / 2);  // a group's last tile is half full on average
+    };
+    const double large = ceil(tiles(256) / 256);
+    const double mid_tiles = tiles(128), full = floor(mid_tiles / 512), rest = mid_tiles - 512 * full;
+    const double mid = 0.65 * full + (rest > 256 ? 0.65 : rest > 0 ? 0.5 : 0.0);
+    return large <= mid ? 0 : 1;
 }
 
 }  // namespace
@@ -493,11 +513,14 @@ bool try_tiles(const GroupArgs &a, hipStream_t stream, hipError_t &e)
 bool group_tile_launch(const GroupArgs &a, hipStream_t stream, hipError_t &e)
 {
     const bool f16 = a.elem == GroupElem::F16;
-    if (a.elem == GroupElem::I8) return try_tiles<ElemI8, false, false>(a, stream, e);
-    if (a.grad) return f16 ? try_tiles<ElemF16, true, true>(a, stream, e) : try_tiles<ElemBf16, true, true>(a, stream, e);
+    const int t = choose_tile(a);
+    if (a.elem == GroupElem::I8) return try_tiles<ElemI8, false, false>(t, a, stream, e);
+    if (a.grad)
+        return f16 ? try_tiles<ElemF16, true, true>(t, a, stream, e) : try_tiles<ElemBf16, true, true>(t, a, stream, e);
     if (a.trans_b)
-        return f16 ? try_tiles<ElemF16, false, false>(a, stream, e) : try_tiles<ElemBf16, false, false>(a, stream, e);
-    return f16 ? try_tiles<ElemF16, false, true>(a, stream, e) : try_tiles<ElemBf16, false, true>(a, stream, e);
+        return f16 ? try_tiles<ElemF16, false, false>(t, a, stream, e)
+                   : try_tiles<ElemBf16, false, false>(t, a, stream, e);
+    return f16 ? try_tiles<ElemF16, false, true>(t, a, stream, e) : try_tiles<ElemBf16, false, true>(t, a, stream, e);
 }
 
 }  // namespace mm

@@ -166,6 +166,9 @@ hipError_t group_launch(const GroupArgs &a, hipStream_t stream);
 // Tiles with panels loaded straight into LDS (mm_group_tile.hip): false where they do not take
 // the shape (nothing is enqueued then); e is the launch's result otherwise.
 bool group_tile_launch(const GroupArgs &a, hipStream_t stream, hipError_t &e);
+// Few rows per group, about `rows` (mm_group_rows.hip): any shape outside gradient mode with M and
+// N at most 2^31 - 1 - 1024.
+hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream);
 // Any shape and alignment (mm_group_any.hip).
 hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream);
 
