@@ -419,7 +419,7 @@ def _matrix(t, name, dtypes=None):
     dtypes = dtypes or (torch.float32,)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
@@ -618,12 +618,38 @@ def conv2d(x, w, stride=(1, 1), pad=(0, 0), dilation=(1, 1), out=None, config=No
     return out
 
 
-def _mm_type(dtype, name):
+def _run(name, device, stream, *args):
+    """Call the C entry point `name` with `args` and the stream, `device` (an index) current."""
     import torch
-    types = {torch.float32: MM_TYPE_F32, torch.bfloat16: MM_TYPE_BF16, torch.float16: MM_TYPE_F16}
-    if dtype not in types:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
-    return types[dtype]
+    fn = getattr(load(), name)
+    # the current stream's address without a Stream object around it (2.9 us of a 12 us call)
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == device:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s)
+    if status != MM_OK:
+        _check(status, name)
+
+
+def _mm_type(dtype, name):
+    """MM_TYPE_* of a torch dtype."""
+    import torch
+    if dtype is torch.float32:
+        return MM_TYPE_F32
+    if dtype is torch.bfloat16:
+        return MM_TYPE_BF16
+    if dtype is torch.float16:
+        return MM_TYPE_F16
+    raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+
+
+def _same_device(device, **tensors):
+    """Raise ValueError unless every given tensor is on the GPU with index `device`."""
+    for name, t in tensors.items():
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
 def _stack(t, name, dtypes):
@@ -631,46 +657,60 @@ def _stack(t, name, dtypes):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU, got {t.device}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be 3-D (groups, rows, columns)")
-    ld = _matrix(t[0] if t.shape[0] else t.new_empty(t.shape[1:]), name, dtypes)
-    return ld, t.stride(0)
+    _, rows, cols = t.shape
+    stride_g, ld, unit = t.stride()
+    if t.numel() == 0:  # the strides of an empty tensor are arbitrary, and nothing uses them
+        return max(cols, 1), 0
+    if cols > 1 and unit != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows == 1:
+        ld = cols
+    if ld < cols:
+        raise ValueError(f"{name} row stride {ld} is below its width {cols}")
+    return ld, stride_g
 
 
 def _offsets(t, groups, device):
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int64:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int64:
         raise TypeError("offsets must be an int64 tensor")
     if t.dim() != 1 or t.shape[0] != groups + 1 or not t.is_contiguous():
         raise ValueError(f"offsets must be contiguous, with groups + 1 = {groups + 1} entries")
-    _on_device(device, offsets=t)
+    _same_device(device, offsets=t)
 
 
 def _scale(t, shape, name, device):
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
         raise TypeError(f"{name} must be a float32 tensor")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {shape}")
-    _on_device(device, **{name: t})
+    _same_device(device, **{name: t})
 
 
-def _output(out, out_dtype, shape, device):
-    """The output tensor: `out` if given (its dtype must be out_dtype where that is given too),
-    else a new one of out_dtype (float32 by default)."""
+def _output(out, out_dtype, shape, like):
+    """(the output tensor, its MM_TYPE_*): `out` if given (its dtype must be out_dtype where that is
+    given too), else a new one of out_dtype (float32 by default) beside `like`."""
     import torch
     if out is None:
         dtype = torch.float32 if out_dtype is None else out_dtype
-        _mm_type(dtype, "out_dtype")
-        return torch.empty(shape, dtype=dtype, device=device)
+        c_type = _mm_type(dtype, "out_dtype")
+        return like.new_empty(shape, dtype=dtype), c_type
     if not isinstance(out, torch.Tensor):
         raise TypeError("out must be a torch.Tensor")
+    c_type = _mm_type(out.dtype, "out")
     if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    if tuple(out.shape) != shape:
+    if out.shape != shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
-    _on_device(device, out=out)
-    return out
+    _same_device(like.get_device(), out=out)
+    return out, c_type
 
 
 def gemm16_grouped(A, B, offsets, trans_b=False, out=None, out_dtype=None, stream=None):
@@ -684,18 +724,20 @@ def gemm16_grouped(A, B, offsets, trans_b=False, out=None, out_dtype=None, strea
     import torch
     lda = _matrix(A, "A", (torch.bfloat16, torch.float16))
     ldb, stride_b = _stack(B, "B", (A.dtype,))
+    device = A.get_device()
     M, K = A.shape
-    groups, N, K2 = (B.shape[0], B.shape[1], B.shape[2]) if trans_b else (B.shape[0], B.shape[2], B.shape[1])
+    groups, K2, N = B.shape
+    if trans_b:
+        K2, N = N, K2
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
-    _on_device(A.device, B=B)
-    _offsets(offsets, groups, A.device)
-    out = _output(out, out_dtype, (M, N), A.device)
-    c_type = _mm_type(out.dtype, "out")
+    _same_device(device, B=B)
+    _offsets(offsets, groups, device)
+    out, c_type = _output(out, out_dtype, (M, N), A)
     ldc = _matrix(out, "out", (out.dtype,))
-    call = mm_gemm_bf16_grouped if A.dtype == torch.bfloat16 else mm_gemm_f16_grouped
-    with torch.cuda.device(A.device):
-        call(groups, M, N, K, offsets, A, lda, B, ldb, stride_b, 1 if trans_b else 0, out, c_type, ldc, stream)
+    name = "mm_gemm_bf16_grouped" if A.dtype is torch.bfloat16 else "mm_gemm_f16_grouped"
+    _run(name, device, stream, groups, M, N, K, offsets.data_ptr(), A.data_ptr(), lda, B.data_ptr(), ldb,
+         stride_b, 1 if trans_b else 0, out.data_ptr(), c_type, ldc)
     return out
 
 
@@ -707,23 +749,23 @@ def gemm16_grouped_grad_b(A, G, offsets, out=None, out_dtype=None, stream=None):
     import torch
     lda = _matrix(A, "A", (torch.bfloat16, torch.float16))
     ldg = _matrix(G, "G", (A.dtype,))
+    device = A.get_device()
     M, K = A.shape
     M2, N = G.shape
     if M2 != M:
         raise ValueError(f"row counts differ: {tuple(A.shape)}, {tuple(G.shape)}")
-    _on_device(A.device, G=G)
+    _same_device(device, G=G)
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be a 1-D tensor of groups + 1 entries")
     groups = offsets.shape[0] - 1
-    _offsets(offsets, groups, A.device)
-    out = _output(out, out_dtype, (groups, K, N), A.device)
-    d_type = _mm_type(out.dtype, "out")
+    _offsets(offsets, groups, device)
+    out, d_type = _output(out, out_dtype, (groups, K, N), A)
     ldd, stride_d = _stack(out, "out", (out.dtype,))
     if groups > 1 and K > 0 and N > 0 and stride_d < (K - 1) * ldd + N:
         raise ValueError("the matrices of out overlap")
-    call = mm_gemm_bf16_grouped_grad_b if A.dtype == torch.bfloat16 else mm_gemm_f16_grouped_grad_b
-    with torch.cuda.device(A.device):
-        call(groups, M, N, K, offsets, A, lda, G, ldg, out, d_type, ldd, stride_d, stream)
+    name = "mm_gemm_bf16_grouped_grad_b" if A.dtype is torch.bfloat16 else "mm_gemm_f16_grouped_grad_b"
+    _run(name, device, stream, groups, M, N, K, offsets.data_ptr(), A.data_ptr(), lda, G.data_ptr(), ldg,
+         out.data_ptr(), d_type, ldd, stride_d)
     return out
 
 
@@ -732,18 +774,21 @@ def quantize_i8(x, out=None, scale=None, stream=None):
     scale[i] = max |x[i]| / 127; values are rounded to the nearest integer, halves to even."""
     import torch
     ldx = _matrix(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    device = x.get_device()
     rows, cols = x.shape
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-    ldq = _matrix(out, "out", (torch.int8,))
-    if tuple(out.shape) != (rows, cols):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, cols)}")
+        out, ldq = x.new_empty((rows, cols), dtype=torch.int8), max(cols, 1)
+    else:
+        ldq = _matrix(out, "out", (torch.int8,))
+        if out.shape != x.shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, cols)}")
+        _same_device(device, out=out)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _on_device(x.device, out=out)
-    _scale(scale, (rows,), "scale", x.device)
-    with torch.cuda.device(x.device):
-        mm_quantize_i8(rows, cols, x, _mm_type(x.dtype, "x"), ldx, out, ldq, scale, stream)
+        scale = x.new_empty(rows, dtype=torch.float32)
+    else:
+        _scale(scale, (rows,), "scale", device)
+    _run("mm_quantize_i8", device, stream, rows, cols, x.data_ptr(), _mm_type(x.dtype, "x"), ldx, out.data_ptr(),
+         ldq, scale.data_ptr())
     return out, scale
 
 
@@ -753,18 +798,18 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
     import torch
     lda = _matrix(A, "A", (torch.int8,))
     ldb = _matrix(B, "B", (torch.int8,))
+    device = A.get_device()
     M, K = A.shape
     N, K2 = B.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
-    _on_device(A.device, B=B)
-    _scale(a_scale, (M,), "a_scale", A.device)
-    _scale(b_scale, (N,), "b_scale", A.device)
-    out = _output(out, out_dtype, (M, N), A.device)
-    c_type = _mm_type(out.dtype, "out")
+    _same_device(device, B=B)
+    _scale(a_scale, (M,), "a_scale", device)
+    _scale(b_scale, (N,), "b_scale", device)
+    out, c_type = _output(out, out_dtype, (M, N), A)
     ldc = _matrix(out, "out", (out.dtype,))
-    with torch.cuda.device(A.device):
-        mm_gemm_i8(M, N, K, A, lda, a_scale, B, ldb, b_scale, out, c_type, ldc, stream)
+    _run("mm_gemm_i8", device, stream, M, N, K, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb,
+         b_scale.data_ptr(), out.data_ptr(), c_type, ldc)
     return out
 
 
@@ -774,18 +819,17 @@ def gemm_i8_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, s
     import torch
     lda = _matrix(A, "A", (torch.int8,))
     ldb, stride_b = _stack(B, "B", (torch.int8,))
+    device = A.get_device()
     M, K = A.shape
     groups, N, K2 = B.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
-    _on_device(A.device, B=B)
-    _offsets(offsets, groups, A.device)
-    _scale(a_scale, (M,), "a_scale", A.device)
-    _scale(b_scale, (groups, N), "b_scale", A.device)
-    out = _output(out, out_dtype, (M, N), A.device)
-    c_type = _mm_type(out.dtype, "out")
+    _same_device(device, B=B)
+    _offsets(offsets, groups, device)
+    _scale(a_scale, (M,), "a_scale", device)
+    _scale(b_scale, (groups, N), "b_scale", device)
+    out, c_type = _output(out, out_dtype, (M, N), A)
     ldc = _matrix(out, "out", (out.dtype,))
-    with torch.cuda.device(A.device):
-        mm_gemm_i8_grouped(groups, M, N, K, offsets, A, lda, a_scale, B, ldb, stride_b, b_scale, out,
-                           c_type, ldc, stream)
+    _run("mm_gemm_i8_grouped", device, stream, groups, M, N, K, offsets.data_ptr(), A.data_ptr(), lda,
+         a_scale.data_ptr(), B.data_ptr(), ldb, stride_b, b_scale.data_ptr(), out.data_ptr(), c_type, ldc)
     return out

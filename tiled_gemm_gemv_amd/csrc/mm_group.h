@@ -84,6 +84,33 @@ struct OutType<2> {
     typedef _Float16 T;
 };
 
+// 16 bytes from any address (the device's unaligned access mode serves them)
+__device__ __forceinline__ u32x4 load16(const char *p)
+{
+    struct __attribute__((packed)) Bytes {
+        u32x4 v;
+    };
+    return reinterpret_cast<const Bytes *>(p)->v;
+}
+
+// The first `valid` bytes (a multiple of the element size) at p, zeros after; no other byte is read.
+template <class Elem>
+__device__ __forceinline__ u32x4 load16_upto(const char *p, int valid)
+{
+    if (valid >= 16) return load16(p);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    constexpr int es = sizeof(Elem);
+#pragma unroll
+    for (int e = 0; e < 16 / es; ++e)
+        if (e * es < valid) {
+            const unsigned x = es == 1   ? (unsigned)*reinterpret_cast<const unsigned char *>(p + e)
+                               : es == 2 ? (unsigned)*reinterpret_cast<const unsigned short *>(p + 2 * e)
+                                         : *reinterpret_cast<const unsigned *>(p + 4 * e);
+            v[e * es / 4] |= x << (8 * (e * es % 4));
+        }
+    return v;
+}
+
 // lo and hi of group g, clamped to [0, M].
 __device__ __forceinline__ void group_range(const int64_t *offsets, int g, int M, int &lo, int &hi)
 {

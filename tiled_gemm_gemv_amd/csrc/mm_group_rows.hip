@@ -46,32 +46,6 @@ struct Rows16I8 : ElemI8 {
     }
 };
 
-// 16 bytes from any address
-__device__ __forceinline__ u32x4 load16(const char *p)
-{
-    struct __attribute__((packed)) Bytes {
-        u32x4 v;
-    };
-    return reinterpret_cast<const Bytes *>(p)->v;
-}
-
-// The first `valid` bytes (a multiple of the element size) at p, zeros after; no other byte is read.
-template <class Elem>
-__device__ __forceinline__ u32x4 load16_upto(const char *p, int valid)
-{
-    if (valid >= 16) return load16(p);
-    u32x4 v = {0u, 0u, 0u, 0u};
-    constexpr int es = sizeof(Elem);
-#pragma unroll
-    for (int e = 0; e < 16 / es; ++e)
-        if (e * es < valid) {
-            const unsigned x = es == 1 ? (unsigned)*reinterpret_cast<const unsigned char *>(p + e)
-                                       : (unsigned)*reinterpret_cast<const unsigned short *>(p + 2 * e);
-            v[e * es / 4] |= x << (8 * (e * es % 4));
-        }
-    return v;
-}
-
 // Partial sums of the W waves added in wave order and stored. `mine` holds NC x 4 values per lane:
 // value (c, r) is row 4 (lane / 16) + r, column COLS_C * (lane % 16) + c  (columns 16 c + lane % 16
 // where COLS_C is 0).
