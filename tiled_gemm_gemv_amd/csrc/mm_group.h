@@ -16,6 +16,8 @@
 // they hold no kernel leaves the rows of A and C.
 #pragma once
 
+#include <math.h>
+
 #include <type_traits>
 
 #include "mm_internal.h"
@@ -184,6 +186,25 @@ __device__ __forceinline__ bool find_row_tile(const GroupArgs &p, unsigned rt, R
         before = __builtin_amdgcn_readlane(incl, 63);
     }
     return false;
+}
+
+// What the host expects of group sizes that it does not know, for the choice of a kernel: groups
+// with a row (rows spread at random), BM-row tiles (a group's last tile half full on average), and
+// the bytes of the right-hand matrices that are read.
+inline double expected_groups(const GroupArgs &a)
+{
+    if (!a.offsets) return 1;
+    return a.groups * (1 - exp(-(double)a.M / a.groups));
+}
+inline double expected_row_tiles(const GroupArgs &a, int bm)
+{
+    const double groups = expected_groups(a), mean = a.M / groups;
+    if (!a.offsets || a.groups == 1) return (double)(((int64_t)a.M + bm - 1) / bm);
+    return groups * (mean > bm / 2 ? mean / bm + 0.5 : 1.0);
+}
+inline double expected_weight_bytes(const GroupArgs &a)
+{
+    return expected_groups(a) * a.N * (double)a.K * (a.elem == GroupElem::I8 ? 1 : 2);
 }
 
 // Most BM-row tiles that M rows in `groups` groups can need: whole tiles, and one partial

@@ -129,17 +129,36 @@ hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream)
     return a.trans_b ? launch_any<ElemBf16, false, false>(a, stream) : launch_any<ElemBf16, false, true>(a, stream);
 }
 
+// The kernel whose modelled time is least among those that take the shape.
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
 {
+    enum { kAny, kRows16, kRows32, kRows64, kMid, kLarge };
+    int best = kAny;
+    double time = 1e300;
+    auto offer = [&](int kernel, double t) {
+        if (t < time) {
+            best = kernel;
+            time = t;
+        }
+    };
     constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
-    if (a.M <= largest && a.N <= largest) {
-        const int64_t mean = a.offsets ? ((int64_t)a.M + a.groups - 1) / a.groups : a.M;
-        const int64_t rows = a.offsets && 2 * mean < a.M ? 2 * mean : a.M;
-        if (!a.grad && rows <= 64) return group_rows_launch(a, (int)rows, stream);
+    if (a.M <= largest && a.N <= largest && a.K <= largest) {
+        if (!a.grad) {
+            offer(kRows16, group_rows_time(a, 16));
+            offer(kRows32, group_rows_time(a, 32));
+            offer(kRows64, group_rows_time(a, 64));
+        }
+        if (group_tile_ok(a, false)) offer(kMid, group_tile_time(a, false));
+        if (group_tile_ok(a, true)) offer(kLarge, group_tile_time(a, true));
     }
-    hipError_t e;
-    if (group_tile_launch(a, stream, e)) return e;
-    return group_any_launch(a, stream);
+    switch (best) {
+    case kRows16: return group_rows_launch(a, 16, stream);
+    case kRows32: return group_rows_launch(a, 32, stream);
+    case kRows64: return group_rows_launch(a, 64, stream);
+    case kMid: return group_tile_launch(a, false, stream);
+    case kLarge: return group_tile_launch(a, true, stream);
+    default: return group_any_launch(a, stream);
+    }
 }
 
 }  // namespace mm

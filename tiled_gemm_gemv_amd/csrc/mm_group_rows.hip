@@ -10,9 +10,9 @@
 //
 //   B rows along k (stored N x K): lane l reads the 16 bytes of its column itself: 16 columns x
 //     128 bytes of k per slice.
-//   B rows across k (stored K x N): lane l reads 16 bytes (8 columns) of each of the 8 rows
-//     8 (l / 16) .. + 7 of a slice of 32 k; 128 columns. The MFMA for column 8 i + c wants those 8
-//     rows of one column: a pair of rows is one v_perm_b32, 32 of them for the 64 values.
+//   B rows across k (stored K x N): lane l reads CPL columns of each of the 8 rows 8 (l / 16) .. + 7
+//     of a slice of 32 k; 16 CPL columns in all. The MFMA for column CPL i + c wants those 8 rows of
+//     one column: a pair of rows is one v_perm_b32, 4 CPL of them for the lane's 8 CPL values.
 // A's rows come from L2 (every workgroup of a group reads the same rows); rows past the group's end
 // repeat its last row and are not stored.
 #include "mm_group.h"
@@ -178,45 +178,67 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
         join_and_store<E, W, NB, 0>(p, acc[i], lds, t.g, t.row0 + 16 * i, t.hi, n0);
 }
 
-// B rows across k (16-bit elements). W waves, 128 columns, slices of 32 k, J of them in flight.
-template <class E, int RB, int W, int J>
+// The CPL 16-bit values at p (any 2-byte alignment) in CPL / 2 words.
+template <int CPL>
+__device__ __forceinline__ void load_columns(const char *p, unsigned (&v)[CPL / 2])
+{
+    struct __attribute__((packed)) Words {
+        unsigned w[CPL / 2];
+    } x = *reinterpret_cast<const Words *>(p);
+#pragma unroll
+    for (int i = 0; i < CPL / 2; ++i) v[i] = x.w[i];
+}
+template <int CPL>
+__device__ __forceinline__ void load_columns_upto(const char *p, int cols, unsigned (&v)[CPL / 2])
+{
+#pragma unroll
+    for (int i = 0; i < CPL / 2; ++i) v[i] = 0u;
+#pragma unroll
+    for (int e = 0; e < CPL; ++e)
+        if (e < cols) v[e / 2] |= (unsigned)*reinterpret_cast<const unsigned short *>(p + 2 * e) << (16 * (e & 1));
+}
+
+// B rows across k (16-bit elements). W waves, 16 CPL columns, slices of 32 k, J of them in flight.
+template <class E, int RB, int CPL, int W, int J>
 __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
 {
     typedef typename E::T T;
-    __shared__ __attribute__((aligned(16))) char lds[W * 16 * 128 * 4];
+    __shared__ __attribute__((aligned(16))) char lds[W * 16 * 16 * CPL * 4];
     RowTile t;
     int n0;
-    if (!rows_tile<16 * RB>(p, 128, t, n0)) return;
+    if (!rows_tile<16 * RB>(p, 16 * CPL, t, n0)) return;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const T *a[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
         a[i] = static_cast<const T *>(p.A) + (int64_t)min(t.row0 + 16 * i + (lane & 15), t.hi - 1) * p.lda +
                8 * (lane >> 4);
-    const int64_t col = (int64_t)n0 + 8 * (lane & 15);
-    const bool full = (int64_t)n0 + 128 <= p.N;  // the strip's columns all exist
-    const int cols = full ? 8 : (int)max((int64_t)0, min((int64_t)8, p.N - col));
+    const int64_t col = (int64_t)n0 + CPL * (lane & 15);
+    const bool full = (int64_t)n0 + 16 * CPL <= p.N;  // the strip's columns all exist
+    const int cols = full ? CPL : (int)max((int64_t)0, min((int64_t)CPL, p.N - col));
     const T *b = static_cast<const T *>(p.B) + t.g * p.stride_b + (int64_t)(8 * (lane >> 4)) * p.ldb + (cols > 0 ? col : 0);
-    typename E::Acc4 acc[RB][8];
+    typename E::Acc4 acc[RB][CPL];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[i][c] = typename E::Acc4{0, 0, 0, 0};
+        for (int c = 0; c < CPL; ++c) acc[i][c] = typename E::Acc4{0, 0, 0, 0};
 
-    u32x4 av[J][RB], bv[J][8];
+    u32x4 av[J][RB];
+    unsigned bv[J][8][CPL / 2];
     auto load = [&](int x, int slice) {
         const int64_t k0 = (int64_t)slice * 32;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const char *q = reinterpret_cast<const char *>(b + (k0 + r) * p.ldb);
-            bv[x][r] = full ? load16(q) : load16_upto<T>(q, 2 * cols);
+            if (full) load_columns<CPL>(q, bv[x][r]);
+            else load_columns_upto<CPL>(q, cols, bv[x][r]);
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i) av[x][i] = load16(reinterpret_cast<const char *>(a[i] + k0));
     };
-    auto multiply = [&](const u32x4 (&aa)[RB], const u32x4 (&bb)[8]) {
+    auto multiply = [&](const u32x4 (&aa)[RB], const unsigned (&bb)[8][CPL / 2]) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < CPL; ++c) {
             u32x4 o;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -243,17 +265,18 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
     if (p.K % 32 != 0 && whole % W == w) {  // the partial slice
         const int64_t k0 = (int64_t)whole * 32;
         const int left = p.K - whole * 32 - 8 * (lane >> 4);  // of this lane's 8 k
-        u32x4 aa[RB], bb[8];
+        u32x4 aa[RB];
+        unsigned bb[8][CPL / 2];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-            bb[r] = load16_upto<T>(reinterpret_cast<const char *>(b + (k0 + r) * p.ldb), r < left ? 2 * cols : 0);
+            load_columns_upto<CPL>(reinterpret_cast<const char *>(b + (k0 + r) * p.ldb), r < left ? cols : 0, bb[r]);
 #pragma unroll
         for (int i = 0; i < RB; ++i) aa[i] = load16_upto<T>(reinterpret_cast<const char *>(a[i] + k0), 2 * left);
         multiply(aa, bb);
     }
 #pragma unroll
     for (int i = 0; i < RB; ++i)
-        join_and_store<E, W, 8, 8>(p, acc[i], lds, t.g, t.row0 + 16 * i, t.hi, n0);
+        join_and_store<E, W, CPL, CPL>(p, acc[i], lds, t.g, t.row0 + 16 * i, t.hi, n0);
 }
 
 template <int ROWS>
@@ -274,29 +297,57 @@ hipError_t launch_d(const GroupArgs &a, hipStream_t stream)
     return launch_rows<16 * RB>(reinterpret_cast<const void *>(&rows_kernel_d<E, RB, NB, W, J>), a, 16 * NB, W, stream);
 }
 
-template <class E, int RB, int W, int J>
+template <class E, int RB, int CPL, int W, int J>
 hipError_t launch_t(const GroupArgs &a, hipStream_t stream)
 {
-    return launch_rows<16 * RB>(reinterpret_cast<const void *>(&rows_kernel_t<E, RB, W, J>), a, 128, W, stream);
+    return launch_rows<16 * RB>(reinterpret_cast<const void *>(&rows_kernel_t<E, RB, CPL, W, J>), a, 16 * CPL, W, stream);
+}
+
+// Columns per workgroup: with many workgroups wide strips, which read A's rows less often; with few
+// narrow ones, since one workgroup streams no more than about 40 GB/s. Measured at 16 rows: i8, 16
+// groups of 4096 x 2048 38 us in strips of 16, 31 in strips of 32; one of 4096 x 4096 7.1 and 9.0.
+int strip_columns(const GroupArgs &a, int rows)
+{
+    const double tiles = expected_row_tiles(a, rows);
+    if (a.trans_b) return tiles * ((a.N + 31) / 32) >= 768 ? 32 : 16;
+    const double wide = tiles * ((a.N + 127) / 128);
+    if (rows <= 32 && wide < 64) return 32;
+    return wide >= 192 ? 128 : 64;
 }
 
 template <class E>
 hipError_t rows_d(const GroupArgs &a, int rows, hipStream_t stream)
 {
-    if (rows <= 16) return launch_d<E, 1, 1, 4, 4>(a, stream);
-    if (rows <= 32) return launch_d<E, 2, 2, 4, 2>(a, stream);
-    return launch_d<E, 4, 2, 4, 2>(a, stream);
+    const bool wide = strip_columns(a, rows) == 32;
+    if (rows == 16) return wide ? launch_d<E, 1, 2, 4, 4>(a, stream) : launch_d<E, 1, 1, 4, 4>(a, stream);
+    if (rows == 32) return wide ? launch_d<E, 2, 2, 4, 2>(a, stream) : launch_d<E, 2, 1, 4, 4>(a, stream);
+    return wide ? launch_d<E, 4, 2, 4, 2>(a, stream) : launch_d<E, 4, 1, 4, 2>(a, stream);
 }
 
 template <class E>
 hipError_t rows_t(const GroupArgs &a, int rows, hipStream_t stream)
 {
-    if (rows <= 16) return launch_t<E, 1, 8, 2>(a, stream);
-    if (rows <= 32) return launch_t<E, 2, 8, 2>(a, stream);
-    return launch_t<E, 4, 8, 1>(a, stream);
+    const int cols = strip_columns(a, rows);
+    if (rows == 16)
+        return cols == 128  ? launch_t<E, 1, 8, 8, 2>(a, stream)
+               : cols == 64 ? launch_t<E, 1, 4, 8, 4>(a, stream)
+                            : launch_t<E, 1, 2, 8, 6>(a, stream);
+    if (rows == 32)
+        return cols == 128  ? launch_t<E, 2, 8, 8, 2>(a, stream)
+               : cols == 64 ? launch_t<E, 2, 4, 8, 4>(a, stream)
+                            : launch_t<E, 2, 2, 8, 4>(a, stream);
+    return cols == 128 ? launch_t<E, 4, 8, 8, 1>(a, stream) : launch_t<E, 4, 4, 8, 2>(a, stream);
 }
 
 }  // namespace
+
+double group_rows_time(const GroupArgs &a, int rows)
+{
+    const int es = a.elem == GroupElem::I8 ? 1 : 2, cols = strip_columns(a, rows);
+    const double tiles = expected_row_tiles(a, rows) * (double)(((int64_t)a.N + cols - 1) / cols);
+    const double bytes = tiles * (rows + cols) * (double)a.K * es;  // through L2
+    return 4.5 + fmax(bytes / fmin(9e6, 4e4 * tiles), expected_weight_bytes(a) / 5.2e6);
+}
 
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream)
 {

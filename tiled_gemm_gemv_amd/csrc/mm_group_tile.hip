@@ -33,8 +33,6 @@
 // ends at the last k: it shares its first `ov` k with the next step (or, in a group of fewer rows
 // than a K-step, reads rows before the group), and both panels are zeroed there once they have
 // landed, so that those k add 0 x 0 whatever the memory holds.
-#include <math.h>
-
 #include "mm_group.h"
 
 namespace mm {
@@ -54,12 +52,14 @@ struct GroupTile {
     static constexpr int ES = sizeof(typename E::T), BK = 128 / ES;
     static constexpr int A_HALF = RH * 128, B_HALF = CH * 128;  // bytes of a half panel
     static constexpr int STAGE = 2 * (A_HALF + B_HALF);
+    static constexpr int PITCH = BN + 4;  // epilogue: words per row in LDS (rows 4 apart on other banks)
+    static constexpr int LDS = 2 * STAGE > RH * PITCH * 4 ? 2 * STAGE : RH * PITCH * 4;
     static constexpr int A_LD = A_HALF / 1024 / WAVES, B_LD = B_HALF / 1024 / WAVES;  // 1 KB loads per wave
     // offsets of the half panels in a stage
     static constexpr int A_OFF[2] = {0, A_HALF}, B_OFF[2] = {2 * A_HALF, 2 * A_HALF + B_HALF};
     static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
     static_assert(QM % 32 == 0 && QN % 32 == 0, "whole 32 x 32 blocks");
-    static_assert(2 * STAGE <= 160 * 1024, "two stages in LDS");
+    static_assert(LDS <= 160 * 1024, "two stages in LDS");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
     static_assert((!AT || RH >= 64) && (!BT || CH >= 64), "T rows of at least the 8 chunks that swz_t permutes");
 };
@@ -122,12 +122,31 @@ __device__ __forceinline__ void bare_barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Elements first .. last - 1 of 8 consecutive ones to C + at.
+template <class O>
+__device__ __forceinline__ void store_row(void *C, int64_t at, const float (&v)[8], int first, int last)
+{
+    O *c = static_cast<O *>(C) + at;
+    if (first == 0 && last == 8) {
+        struct __attribute__((packed)) Eight {
+            O o[8];
+        } x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.o[e] = (O)v[e];
+        *reinterpret_cast<Eight *>(c) = x;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= first && e < last) c[e] = (O)v[e];
+    }
+}
+
 template <class T, bool GRAD>
 __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
 {
     typedef typename T::E E;
     typedef typename E::T Elem;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
+    __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
 
     // ---- the tile: rows m0 .. m_end of C (of D_g), columns n0 .. N, the sum over k_lo .. k_end
     const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
@@ -412,44 +431,56 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         }
     }
 
-    // ---- epilogue: lane l holds column l % 32 and rows 8 (r / 4) + 4 (l / 32) + r % 4 of a block
-    float *row_scale = reinterpret_cast<float *>(lds);
+    // ---- epilogue: through LDS, one half of the rows at a time, so that whole rows are stored 16
+    // bytes (32 of fp32) per lane. Lane l holds column l % 32 and rows 8 (r / 4) + 4 (l / 32) + r % 4
+    // of a block. Storing from there, one element per lane and instruction, took 7 us of a tile.
+    typedef decltype(acc[0][0][0][0][0] + 0) V;
+    typedef V V4 __attribute__((ext_vector_type(4)));
+    V *tile = reinterpret_cast<V *>(lds);
+    constexpr int per_row = T::BN / 8;  // 8 columns per lane
+    static_assert(T::NT % per_row == 0, "a lane keeps its columns");
+    const int c8 = (int)(threadIdx.x % per_row) * 8, n = nb0 + c8;
+    const int first = T::BT && n < n0 ? n0 - n : 0, last = min(8, p.N - n);  // columns to store
+    float sb[8];
     if constexpr (E::INT8) {
-        wait_reads();
-        bare_barrier();  // every wave is done with the stages
-        for (int e = threadIdx.x; e < T::BM; e += T::NT) row_scale[e] = p.sa[min(m0 + e, m_end - 1)];
-        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sb[e] = e < last ? p.sb[(int64_t)g * p.stride_sb + n + e] : 0.f;
     }
-    auto store = [&](auto out) {
-        typedef typename decltype(out)::T O;
-        O *C = static_cast<O *>(p.C) + (GRAD ? (int64_t)g * p.stride_c : 0);
 #pragma unroll
-        for (int qa = 0; qa < 2; ++qa)
+    for (int qa = 0; qa < 2; ++qa) {
+        if (mb0 + qa * T::RH >= m_end) break;
+        wait_reads();
+        bare_barrier();  // every wave is done with the stages, or with the half before
 #pragma unroll
-            for (int qb = 0; qb < 2; ++qb)
+        for (int qb = 0; qb < 2; ++qb)
 #pragma unroll
-                for (int j = 0; j < T::FN; ++j) {
-                    const int n = nb0 + qb * T::CH + wn * T::QN + 32 * j + (lane & 31);
-                    if (n >= p.N || (T::BT && n < n0)) continue;
-                    float sb = 1.f;
-                    if constexpr (E::INT8) sb = p.sb[(int64_t)g * p.stride_sb + n];
+            for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-                    for (int i = 0; i < T::FM; ++i) {
-                        const int ml = qa * T::RH + wm * T::QM + 32 * i + 4 * (lane >> 5);
+                for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int m = mb0 + ml + 8 * (r >> 2) + (r & 3);
-                            if (m >= m_end || (T::AT && m < m0)) continue;
-                            float v = (float)acc[qa][qb][i][j][r];
-                            if constexpr (E::INT8) v = v * row_scale[ml + 8 * (r >> 2) + (r & 3)] * sb;
-                            C[(int64_t)m * p.ldc + n] = (O)v;
-                        }
-                    }
-                }
-    };
-    if (p.c_type == 0) store(OutType<0>());
-    else if (p.c_type == 1) store(OutType<1>());
-    else store(OutType<2>());
+                    for (int r = 0; r < 16; ++r)
+                        tile[(wm * T::QM + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * T::PITCH + qb * T::CH +
+                             wn * T::QN + 32 * j + (lane & 31)] = acc[qa][qb][i][j][r];
+        __syncthreads();
+        for (int row = threadIdx.x / per_row; row < T::RH; row += T::NT / per_row) {
+            const int m = mb0 + qa * T::RH + row;
+            if (m >= m_end || (T::AT && m < m0) || last <= first) continue;
+            const V4 lo = *reinterpret_cast<const V4 *>(tile + row * T::PITCH + c8);
+            const V4 hi = *reinterpret_cast<const V4 *>(tile + row * T::PITCH + c8 + 4);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (float)(e < 4 ? lo[e] : hi[e - 4]);
+            if constexpr (E::INT8) {
+                const float sa = p.sa[m];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = v[e] * sa * sb[e];
+            }
+            const int64_t at = (GRAD ? (int64_t)g * p.stride_c : 0) + (int64_t)m * p.ldc + n;
+            if (p.c_type == 0) store_row<OutType<0>::T>(p.C, at, v, first, last);
+            else if (p.c_type == 1) store_row<OutType<1>::T>(p.C, at, v, first, last);
+            else store_row<OutType<2>::T>(p.C, at, v, first, last);
+        }
+    }
 }
 
 // The tile takes the shape: K-steps fit (or, in gradient mode, rows of any number), the columns of
@@ -481,46 +512,59 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
                            0, stream);
 }
 
+// Both tiles have the operands' requirements in common but for the size.
 template <class E, bool AT, bool BT>
-bool try_tiles(int tile, const GroupArgs &a, hipStream_t stream, hipError_t &e)
-{
+struct Tiles {
     using Large = GroupTile<E, AT, BT, 128, 128, 2, 4>;
     using Mid = GroupTile<E, AT, BT, 64, 64, 2, 2>;
-    if (tile == 0 && tile_ok<Large, AT>(a)) e = launch_tile<Large, AT>(a, stream);
-    else if (tile_ok<Mid, AT>(a)) e = launch_tile<Mid, AT>(a, stream);
-    else return false;
-    return true;
-}
+    static bool ok(const GroupArgs &a, bool large) { return large ? tile_ok<Large, AT>(a) : tile_ok<Mid, AT>(a); }
+    static hipError_t launch(const GroupArgs &a, bool large, hipStream_t stream)
+    {
+        return large ? launch_tile<Large, AT>(a, stream) : launch_tile<Mid, AT>(a, stream);
+    }
+};
 
-// 0: 256 x 256 tiles, 1: 128 x 128
-int choose_tile(const GroupArgs &a)
+// f(Tiles<...>()) for the call's element type and layouts.
+template <class F>
+auto with_tiles(const GroupArgs &a, F &&f)
 {
-    const double groups = a.offsets ? (double)(a.groups < a.M ? a.groups : a.M) : 1.0;
-    auto tiles = [&](int t) {
-        const double n = (double)(((int64_t)a.N + t - 1) / t);
-        if (a.grad) return n * (double)(((int64_t)a.K + t - 1) / t) * a.groups;
-        if (!a.offsets) return n * (double)(((int64_t)a.M + t - 1) / t);
-        return n * ((double)a.M / t + groups / 2);  // a group's last tile is half full on average
-    };
-    const double large = ceil(tiles(256) / 256);
-    const double mid_tiles = tiles(128), full = floor(mid_tiles / 512), rest = mid_tiles - 512 * full;
-    const double mid = 0.65 * full + (rest > 256 ? 0.65 : rest > 0 ? 0.5 : 0.0);
-    return large <= mid ? 0 : 1;
+    if (a.elem == GroupElem::I8) return f(Tiles<ElemI8, false, false>());
+    const bool f16 = a.elem == GroupElem::F16;
+    if (a.grad) return f16 ? f(Tiles<ElemF16, true, true>()) : f(Tiles<ElemBf16, true, true>());
+    if (a.trans_b) return f16 ? f(Tiles<ElemF16, false, false>()) : f(Tiles<ElemBf16, false, false>());
+    return f16 ? f(Tiles<ElemF16, false, true>()) : f(Tiles<ElemBf16, false, true>());
 }
 
 }  // namespace
 
-bool group_tile_launch(const GroupArgs &a, hipStream_t stream, hipError_t &e)
+double group_tile_time(const GroupArgs &a, bool large)
 {
-    const bool f16 = a.elem == GroupElem::F16;
-    const int t = choose_tile(a);
-    if (a.elem == GroupElem::I8) return try_tiles<ElemI8, false, false>(t, a, stream, e);
-    if (a.grad)
-        return f16 ? try_tiles<ElemF16, true, true>(t, a, stream, e) : try_tiles<ElemBf16, true, true>(t, a, stream, e);
-    if (a.trans_b)
-        return f16 ? try_tiles<ElemF16, false, false>(t, a, stream, e)
-                   : try_tiles<ElemBf16, false, false>(t, a, stream, e);
-    return f16 ? try_tiles<ElemF16, false, true>(t, a, stream, e) : try_tiles<ElemBf16, false, true>(t, a, stream, e);
+    const double sum = a.grad ? (double)a.M / a.groups : (double)a.K;  // length of a tile's sums
+    const double steps = ceil(sum * (a.elem == GroupElem::I8 ? 1 : 2) / 128);
+    const int t = large ? 256 : 128;
+    const double tiles = (double)(((int64_t)a.N + t - 1) / t) *
+                         (a.grad ? (double)(((int64_t)a.K + t - 1) / t) * a.groups : expected_row_tiles(a, t));
+    double time;
+    if (large) {
+        // the groups' sizes are not known here, so neither is the number of rounds: between whole ones
+        const bool known = a.grad || !a.offsets || a.groups == 1;
+        const double rounds = known ? ceil(tiles / 256) : fmax(1.0, tiles / 256 + 0.25);
+        time = rounds * (6 + 1.45 * steps);
+    } else {
+        const double full = floor(tiles / 512), rest = tiles / 512 - full;
+        time = full * (4 + 1.17 * steps) + (rest > 0.5 ? 4 + 1.17 * steps : rest > 0 ? 4 + 0.40 * steps : 0);
+    }
+    return 3 + fmax(time, a.grad ? 0.0 : expected_weight_bytes(a) / 5.2e6);
+}
+
+bool group_tile_ok(const GroupArgs &a, bool large)
+{
+    return with_tiles(a, [&](auto t) { return decltype(t)::ok(a, large); });
+}
+
+hipError_t group_tile_launch(const GroupArgs &a, bool large, hipStream_t stream)
+{
+    return with_tiles(a, [&](auto t) { return decltype(t)::launch(a, large, stream); });
 }
 
 }  // namespace mm

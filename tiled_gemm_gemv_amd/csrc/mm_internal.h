@@ -163,11 +163,14 @@ struct GroupArgs {
 };
 // The kernel for the shape; M, N, groups >= 1 (gradient mode: K, N, groups >= 1).
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream);
-// Tiles with panels loaded straight into LDS (mm_group_tile.hip): false where they do not take
-// the shape (nothing is enqueued then); e is the launch's result otherwise.
-bool group_tile_launch(const GroupArgs &a, hipStream_t stream, hipError_t &e);
-// Few rows per group, about `rows` (mm_group_rows.hip): any shape outside gradient mode with M and
-// N at most 2^31 - 1 - 1024.
+// Tiles of 256 x 256 (large) or 128 x 128 with panels loaded straight into LDS (mm_group_tile.hip):
+// whether they take the shape, their modelled time in microseconds, and the launch.
+bool group_tile_ok(const GroupArgs &a, bool large);
+double group_tile_time(const GroupArgs &a, bool large);
+hipError_t group_tile_launch(const GroupArgs &a, bool large, hipStream_t stream);
+// Tiles of `rows` = 16, 32 or 64 rows for few rows per group (mm_group_rows.hip): any shape outside
+// gradient mode with M, N and K at most 2^31 - 1 - 1024.
+double group_rows_time(const GroupArgs &a, int rows);
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream);
 // Any shape and alignment (mm_group_any.hip).
 hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream);
