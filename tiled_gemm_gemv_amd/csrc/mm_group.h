@@ -95,13 +95,20 @@ __device__ __forceinline__ u32x4 load16(const char *p)
     return reinterpret_cast<const Bytes *>(p)->v;
 }
 
-// The first `valid` bytes (a multiple of the element size) at p, zeros after; no other byte is read.
+// The first `valid` bytes (a multiple of the element size) at p, zeros after; nothing past them is
+// read. `row`: bytes from the start of p's row to the end of those bytes; with 16 or more the 16
+// bytes that end there are read and shifted down, with fewer single elements.
 template <class Elem>
-__device__ __forceinline__ u32x4 load16_upto(const char *p, int valid)
+__device__ __forceinline__ u32x4 load16_upto(const char *p, int valid, int64_t row)
 {
     if (valid >= 16) return load16(p);
     u32x4 v = {0u, 0u, 0u, 0u};
+    if (valid <= 0) return v;
     constexpr int es = sizeof(Elem);
+    if (row >= 16) {
+        const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, load16(p + valid - 16)) >> (8 * (16 - valid));
+        return __builtin_bit_cast(u32x4, x);
+    }
 #pragma unroll
     for (int e = 0; e < 16 / es; ++e)
         if (e * es < valid) {
@@ -205,6 +212,14 @@ inline double expected_row_tiles(const GroupArgs &a, int bm)
 inline double expected_weight_bytes(const GroupArgs &a)
 {
     return expected_groups(a) * a.N * (double)a.K * (a.elem == GroupElem::I8 ? 1 : 2);
+}
+
+// Rows that start at 4-byte boundaries. Loads of others take about twice as long (measured on one
+// shape with K = 1531 and 1536: 50 and 22 us through the rows kernel, 25 and 17 in 128 x 128 tiles).
+inline bool aligned_words(const GroupArgs &a)
+{
+    const int es = a.elem == GroupElem::I8 ? 1 : 2;
+    return (a.lda * es | a.ldb * es | a.stride_b * es | (int64_t)(uintptr_t)a.A | (int64_t)(uintptr_t)a.B) % 4 == 0;
 }
 
 // Most BM-row tiles that M rows in `groups` groups can need: whole tiles, and one partial

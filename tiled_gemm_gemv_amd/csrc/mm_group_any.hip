@@ -144,9 +144,9 @@ hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
     constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
     if (a.M <= largest && a.N <= largest && a.K <= largest) {
         if (!a.grad) {
-            offer(kRows16, group_rows_time(a, 16));
-            offer(kRows32, group_rows_time(a, 32));
-            offer(kRows64, group_rows_time(a, 64));
+            if (group_rows_ok(a, 16)) offer(kRows16, group_rows_time(a, 16));
+            if (group_rows_ok(a, 32)) offer(kRows32, group_rows_time(a, 32));
+            if (group_rows_ok(a, 64)) offer(kRows64, group_rows_time(a, 64));
         }
         if (group_tile_ok(a, false)) offer(kMid, group_tile_time(a, false));
         if (group_tile_ok(a, true)) offer(kLarge, group_tile_time(a, true));

@@ -164,10 +164,10 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
             const int valid = (int)(kb - at) - 64 * h - 16 * (lane >> 4);
             u32x4 aa[RB];
 #pragma unroll
-            for (int i = 0; i < RB; ++i) aa[i] = load16_upto<T>(a[i] + at + 64 * h, valid);
+            for (int i = 0; i < RB; ++i) aa[i] = load16_upto<T>(a[i] + at + 64 * h, valid, kb);
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const u32x4 bb = load16_upto<T>(b[j] + at + 64 * h, valid);
+                const u32x4 bb = load16_upto<T>(b[j] + at + 64 * h, valid, kb);
 #pragma unroll
                 for (int i = 0; i < RB; ++i) acc[i][j] = E::mma4(aa[i], bb, acc[i][j]);
             }
@@ -188,14 +188,23 @@ __device__ __forceinline__ void load_columns(const char *p, unsigned (&v)[CPL / 
 #pragma unroll
     for (int i = 0; i < CPL / 2; ++i) v[i] = x.w[i];
 }
+// The last `cols` of them, moved to the front: value e becomes value e - (CPL - cols).
 template <int CPL>
-__device__ __forceinline__ void load_columns_upto(const char *p, int cols, unsigned (&v)[CPL / 2])
+__device__ __forceinline__ void drop_columns(unsigned (&v)[CPL / 2], int cols)
 {
+    const int sh = 16 * (CPL - cols);
+    if constexpr (CPL == 2) {
+        v[0] >>= sh;
+    } else if constexpr (CPL == 4) {
+        const uint64_t x = (v[0] | (uint64_t)v[1] << 32) >> sh;
+        v[0] = (unsigned)x;
+        v[1] = (unsigned)(x >> 32);
+    } else {
+        const u32x4 x = __builtin_bit_cast(
+            u32x4, __builtin_bit_cast(unsigned __int128, u32x4{v[0], v[1], v[2], v[3]}) >> sh);
 #pragma unroll
-    for (int i = 0; i < CPL / 2; ++i) v[i] = 0u;
-#pragma unroll
-    for (int e = 0; e < CPL; ++e)
-        if (e < cols) v[e / 2] |= (unsigned)*reinterpret_cast<const unsigned short *>(p + 2 * e) << (16 * (e & 1));
+        for (int i = 0; i < 4; ++i) v[i] = x[i];
+    }
 }
 
 // B rows across k (16-bit elements). W waves, 16 CPL columns, slices of 32 k, J of them in flight.
@@ -214,9 +223,12 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
         a[i] = static_cast<const T *>(p.A) + (int64_t)min(t.row0 + 16 * i + (lane & 15), t.hi - 1) * p.lda +
                8 * (lane >> 4);
     const int64_t col = (int64_t)n0 + CPL * (lane & 15);
+    // a lane whose columns cross N reads the last CPL of the row and drops those before its own;
+    // one past N reads them too, for columns that are not stored. N >= CPL.
     const bool full = (int64_t)n0 + 16 * CPL <= p.N;  // the strip's columns all exist
-    const int cols = full ? CPL : (int)max((int64_t)0, min((int64_t)CPL, p.N - col));
-    const T *b = static_cast<const T *>(p.B) + t.g * p.stride_b + (int64_t)(8 * (lane >> 4)) * p.ldb + (cols > 0 ? col : 0);
+    const int cols = (int)(p.N - col < CPL && p.N > col ? p.N - col : CPL);
+    const T *b = static_cast<const T *>(p.B) + t.g * p.stride_b + (int64_t)(8 * (lane >> 4)) * p.ldb +
+                 min(col, (int64_t)p.N - CPL);
     typename E::Acc4 acc[RB][CPL];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
@@ -229,14 +241,16 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
         const int64_t k0 = (int64_t)slice * 32;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const char *q = reinterpret_cast<const char *>(b + (k0 + r) * p.ldb);
-            if (full) load_columns<CPL>(q, bv[x][r]);
-            else load_columns_upto<CPL>(q, cols, bv[x][r]);
+            load_columns<CPL>(reinterpret_cast<const char *>(b + (k0 + r) * p.ldb), bv[x][r]);
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i) av[x][i] = load16(reinterpret_cast<const char *>(a[i] + k0));
     };
-    auto multiply = [&](const u32x4 (&aa)[RB], const unsigned (&bb)[8][CPL / 2]) {
+    auto multiply = [&](const u32x4 (&aa)[RB], unsigned (&bb)[8][CPL / 2]) {
+        if (!full) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) drop_columns<CPL>(bb[r], cols);
+        }
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             u32x4 o;
@@ -268,10 +282,14 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
         u32x4 aa[RB];
         unsigned bb[8][CPL / 2];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            load_columns_upto<CPL>(reinterpret_cast<const char *>(b + (k0 + r) * p.ldb), r < left ? cols : 0, bb[r]);
+        for (int r = 0; r < 8; ++r) {  // rows from K on: row K - 1 read, zeros used
+            load_columns<CPL>(reinterpret_cast<const char *>(b + (k0 + min(r, left - 1)) * p.ldb), bb[r]);
 #pragma unroll
-        for (int i = 0; i < RB; ++i) aa[i] = load16_upto<T>(reinterpret_cast<const char *>(a[i] + k0), 2 * left);
+            for (int i = 0; i < CPL / 2; ++i) bb[r][i] = r < left ? bb[r][i] : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+            aa[i] = load16_upto<T>(reinterpret_cast<const char *>(a[i] + k0), 2 * left, 2 * (int64_t)p.K);
         multiply(aa, bb);
     }
 #pragma unroll
@@ -311,8 +329,8 @@ int strip_columns(const GroupArgs &a, int rows)
     const double tiles = expected_row_tiles(a, rows);
     if (a.trans_b) return tiles * ((a.N + 31) / 32) >= 768 ? 32 : 16;
     const double wide = tiles * ((a.N + 127) / 128);
-    if (rows <= 32 && wide < 64) return 32;
-    return wide >= 192 ? 128 : 64;
+    if (a.N < 4 || (rows <= 32 && wide < 64)) return 32;
+    return a.N >= 8 && wide >= 192 ? 128 : 64;
 }
 
 template <class E>
@@ -334,19 +352,29 @@ hipError_t rows_t(const GroupArgs &a, int rows, hipStream_t stream)
                             : launch_t<E, 1, 2, 8, 6>(a, stream);
     if (rows == 32)
         return cols == 128  ? launch_t<E, 2, 8, 8, 2>(a, stream)
-               : cols == 64 ? launch_t<E, 2, 4, 8, 4>(a, stream)
+               : cols == 64 ? launch_t<E, 2, 4, 8, 2>(a, stream)
                             : launch_t<E, 2, 2, 8, 4>(a, stream);
     return cols == 128 ? launch_t<E, 4, 8, 8, 1>(a, stream) : launch_t<E, 4, 4, 8, 2>(a, stream);
 }
 
 }  // namespace
 
+bool group_rows_ok(const GroupArgs &a, int rows)
+{
+    return a.trans_b || a.N >= (rows == 64 ? 4 : 2);  // a lane's columns of B rows across k
+}
+
+// Fitted to 90 shapes of all operators: a launch and one workgroup's start 4.5 us; what the
+// workgroups read through L2 at 9 TB/s (40 GB/s each where they are few); the right-hand matrices
+// from memory; and rounds of workgroups, each at least its latency and its sums' join.
 double group_rows_time(const GroupArgs &a, int rows)
 {
-    const int es = a.elem == GroupElem::I8 ? 1 : 2, cols = strip_columns(a, rows);
+    const int es = a.elem == GroupElem::I8 ? 1 : 2, cols = strip_columns(a, rows), rb = rows / 16;
     const double tiles = expected_row_tiles(a, rows) * (double)(((int64_t)a.N + cols - 1) / cols);
-    const double bytes = tiles * (rows + cols) * (double)a.K * es;  // through L2
-    return 4.5 + fmax(bytes / fmin(9e6, 4e4 * tiles), expected_weight_bytes(a) / 5.2e6);
+    const double bytes = tiles * (rows + cols) * (double)a.K * es * (aligned_words(a) ? 1.0 : 2.2);
+    const double through = bytes / fmin(9e6, 4e4 * tiles), weights = expected_weight_bytes(a) / 5.2e6;
+    const double rounds = a.trans_b ? ceil(tiles / 768) * (1.5 + 0.5 * rb) : ceil(tiles / 256) * (3 + 1.5 * rb);
+    return 2.5 + fmax(2 + fmax(through, weights), rounds);
 }
 
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream)

@@ -540,7 +540,7 @@ auto with_tiles(const GroupArgs &a, F &&f)
 double group_tile_time(const GroupArgs &a, bool large)
 {
     const double sum = a.grad ? (double)a.M / a.groups : (double)a.K;  // length of a tile's sums
-    const double steps = ceil(sum * (a.elem == GroupElem::I8 ? 1 : 2) / 128);
+    const double steps = ceil(sum * (a.elem == GroupElem::I8 ? 1 : 2) / 128) * (aligned_words(a) ? 1.0 : 1.5);
     const int t = large ? 256 : 128;
     const double tiles = (double)(((int64_t)a.N + t - 1) / t) *
                          (a.grad ? (double)(((int64_t)a.K + t - 1) / t) * a.groups : expected_row_tiles(a, t));

@@ -149,7 +149,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quantize_kernel(QuantAr
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int col = (t + c * TPR) * N;
-        v[c] = load16_upto<X>(x + (int64_t)col * (int)sizeof(X), (cols - col) * (int)sizeof(X));
+        v[c] = load16_upto<X>(x + (int64_t)col * (int)sizeof(X), (cols - col) * (int)sizeof(X), p.cols * sizeof(X));
         top = chunk_top<X>(v[c], top);
     }
     const Quotient k(row_max<TPR>(top_bits<X>(top), part));
@@ -173,7 +173,8 @@ __global__ __launch_bounds__(1024) void quantize_long_kernel(QuantArgs p)
     const char *x = reinterpret_cast<const char *>(static_cast<const X *>(p.X) + row * p.ldx);
     signed char *q = p.Q + row * p.ldq;
     auto load = [&](int64_t col) {
-        return load16_upto<X>(x + col * (int)sizeof(X), (int)min((int64_t)16, (p.cols - col) * (int64_t)sizeof(X)));
+        return load16_upto<X>(x + col * (int)sizeof(X), (int)min((int64_t)16, (p.cols - col) * (int64_t)sizeof(X)),
+                              p.cols * sizeof(X));
     };
     unsigned top = 0;
     for (int64_t col = (int64_t)threadIdx.x * N; col < p.cols; col += 1024 * N) top = chunk_top<X>(load(col), top);
