@@ -12,6 +12,9 @@
 //   phase 2  A hi x B hi    reads A lo of the next K-step
 //   phase 3  A hi x B lo    reads B lo of the next K-step, into the registers of B hi
 // so each half panel is read from LDS once per K-step and wave, and the reads are spread evenly.
+// A tile whose second half of rows holds none of C (the last of a group, often) goes without A hi:
+//   phase 0  A lo x B lo    reads B hi
+//   phase 1  A lo x B hi    reads A lo and B lo of the next K-step, A lo into the registers of A hi
 //
 // LDS holds two K-steps as half panels. The buffer of a half panel is free once every wave has
 // read it; the DMA for the same half two K-steps on goes out one phase later, so six half panels
@@ -94,23 +97,24 @@ __device__ __forceinline__ void wait_vm()
 
 // Loads per wave of the S half panels after number n (n % 4 == N4) of the order A lo, B lo, B hi,
 // A hi, ...
-template <class T, int N4, int S>
+// (P = 4; without A hi, P = 3).
+template <class T, int N4, int S, int P = 4>
 constexpr int loads_after()
 {
     int sum = 0;
-    for (int i = 1; i <= S; ++i) sum += ((N4 + i) % 4 == 0 || (N4 + i) % 4 == 3) ? T::A_LD : T::B_LD;
+    for (int i = 1; i <= S; ++i) sum += ((N4 + i) % P == 0 || (N4 + i) % P == 3) ? T::A_LD : T::B_LD;
     return sum;
 }
 
 // Wait until at most the min(later, S) half panels issued after number n are outstanding.
-template <class T, int N4, int S>
+template <class T, int N4, int S, int P = 4>
 __device__ __forceinline__ void wait_halves(int later)
 {
     if constexpr (S == 0) {
         wait_vm<0>();
     } else {
-        if (later >= S) wait_vm<loads_after<T, N4, S>()>();
-        else wait_halves<T, N4, S - 1>(later);
+        if (later >= S) wait_vm<loads_after<T, N4, S, P>()>();
+        else wait_halves<T, N4, S - 1, P>(later);
     }
 }
 
@@ -141,51 +145,17 @@ __device__ __forceinline__ void store_row(void *C, int64_t at, const float (&v)[
     }
 }
 
-template <class T, bool GRAD>
-__global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
+// Rows m0 .. m_end of C (of D_g), columns n0 .. N, the sum over k_lo .. k_end. LO: the rows end in
+// the tile's first half.
+template <class T, bool GRAD, bool LO>
+__device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, int m0, int m_end, int n0, int k_lo,
+                                          int k_end)
 {
     typedef typename T::E E;
     typedef typename E::T Elem;
-    __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
-
-    // ---- the tile: rows m0 .. m_end of C (of D_g), columns n0 .. N, the sum over k_lo .. k_end
-    const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
-    const int64_t bid = linear_block();
-    int g, m0, m_end, n0, k_lo, k_end;
-    if constexpr (GRAD) {
-        const unsigned tiles_m = (unsigned)((p.K + T::BM - 1) / T::BM);
-        const unsigned per = tiles_m * tiles_n;
-        if (bid >= (int64_t)per * p.groups) return;
-        // each group's tiles over all XCDs: the groups' sums differ in length
-        unsigned tm, tn;
-        g = (int)((unsigned)bid / per);
-        tile_of_group_block((unsigned)bid - g * per, per, tiles_m, tiles_n, tm, tn);
-        m0 = (int)tm * T::BM;
-        n0 = (int)tn * T::BN;
-        m_end = p.K;
-        group_range(p.offsets, g, p.M, k_lo, k_end);
-    } else {
-        const unsigned tiles_m = count_row_tiles<T::BM>(p);
-        if (bid >= (int64_t)tiles_m * tiles_n) return;
-        unsigned tm, tn;
-        tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-        // offsets that decrease can count more tiles than 32 bits hold
-        RowTile t;
-        if (tn >= tiles_n || !find_row_tile<T::BM>(p, tm, t)) return;
-        g = t.g;
-        m0 = t.row0;
-        m_end = t.hi;
-        n0 = (int)tn * T::BN;
-        k_lo = 0;
-        k_end = p.K;
-    }
-    g = __builtin_amdgcn_readfirstlane(g);
-    m0 = __builtin_amdgcn_readfirstlane(m0);
-    m_end = __builtin_amdgcn_readfirstlane(m_end);
-    k_lo = __builtin_amdgcn_readfirstlane(k_lo);
-    k_end = __builtin_amdgcn_readfirstlane(k_end);
     // origin of the panels: a T operand's columns start early enough to end inside the matrix
-    const int mb0 = T::AT ? (m_end >= T::BM ? min(m0, m_end - T::BM) : 0) : m0;
+    constexpr int m_need = LO ? T::RH : T::BM;
+    const int mb0 = T::AT ? (m_end >= m_need ? min(m0, m_end - m_need) : 0) : m0;
     const int nb0 = T::BT ? (p.N >= T::BN ? min(n0, p.N - T::BN) : 0) : n0;
 
     const int lane = threadIdx.x & 63;
@@ -195,7 +165,7 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
     const int len = k_end - k_lo;
     const int ov = (T::BK - len % T::BK) % T::BK;
     const int nk = (len + T::BK - 1) / T::BK;
-    const int halves = 4 * nk;
+    const int halves = (LO ? 3 : 4) * nk;
 
     const Elem *A = static_cast<const Elem *>(p.A);
     const Elem *B = static_cast<const Elem *>(p.B) + (GRAD ? 0 : (int64_t)g * p.stride_b);
@@ -300,9 +270,10 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         else dst[ks][j] = read_d(half, wn * T::FN + j, ks);
     };
 
-    typename E::Acc acc[2][2][T::FM][T::FN];
+    constexpr int HA = LO ? 1 : 2;  // halves of rows
+    typename E::Acc acc[HA][2][T::FM][T::FN];
 #pragma unroll
-    for (int qa = 0; qa < 2; ++qa)
+    for (int qa = 0; qa < HA; ++qa)
 #pragma unroll
         for (int qb = 0; qb < 2; ++qb)
 #pragma unroll
@@ -364,25 +335,66 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         phase(kt, std::integral_constant<int, 3>(), S, FULL);
     };
 
-    if (nk > 0) {
-        offsets_of(ov ? k_end - T::BK : 0);
+    // The same without A hi; half panels are numbered 3 kt + (0: A lo, 1: B lo, 2: B hi), S is the
+    // parity of the K-step: A lo is in a[S], B lo in b[0], B hi in b[1].
+    auto phase_lo = [&](int kt, auto I_, auto S_, auto FULL_) {
+        constexpr int I = decltype(I_)::value, S = decltype(S_)::value;
+        constexpr bool FULL = decltype(FULL_)::value;
+        constexpr int NM = 4 * T::FM * T::FN, NA = I == 1 ? 4 * T::FM : 0, NR = NA + 4 * T::FN;
+        constexpr int NL = I == 0 ? T::A_LD + T::B_LD : T::B_LD;  // phase 0 issues A lo, B lo, phase 1 B hi
+        constexpr int pre = NM / 8, items = NR + NL, slots = NM - pre;
+        const lds_char *stage = (const lds_char *)lds + ((kt + I) & 1) * T::STAGE;
+        auto mfma = [&](int m) {
+            const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
+            acc[0][I][i][j] = E::mma(a[S][ks][i], b[I][ks][j], acc[0][I][i][j]);
+        };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) issue(0, i);
-        if (GRAD && ov && k_end < T::BK) offsets_of(0);
-        if (nk > 1) {
+        for (int m = 0; m < pre; ++m) mfma(m);
+        const int n = 3 * kt + (I == 0 ? 2 : 4), issued = 3 * kt + (I == 0 ? 6 : 8);
+        if (FULL) wait_vm<T::A_LD + 2 * T::B_LD>();
+        else if (n < halves) wait_halves<T, (I == 0 ? 2 : 1), 3, 3>(min(issued, halves) - 1 - n);
+        wait_reads();
+        bare_barrier();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) issue(1, i);
+        for (int m = pre; m < NM; ++m) {
+#pragma unroll
+            for (int t = (m - pre) * items / slots; t < (m - pre + 1) * items / slots; ++t) {
+                const int l = t * NL / items, r = t - l;  // loads and reads among the items before t
+                if ((t + 1) * NL / items == l) {
+                    if (r < NA) read_a(stage + T::A_OFF[0], r, a[S ^ 1]);
+                    else read_b(stage + T::B_OFF[I == 0], r - NA, b[I == 0]);
+                } else if (FULL || kt + 2 < nk) {
+                    if (I == 1) issue_one(kt + 2, 2, l);
+                    else if (l < T::A_LD) issue_one(kt + 2, 0, l);
+                    else issue_one(kt + 2, 1, l - T::A_LD);
+                }
+            }
+            mfma(m);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    auto k_step_lo = [&](int kt, auto S, auto FULL) {
+        phase_lo(kt, std::integral_constant<int, 0>(), S, FULL);
+        phase_lo(kt, std::integral_constant<int, 1>(), S, FULL);
+    };
+
+    if (nk > 0) {
+        constexpr int panels = LO ? 3 : 4;  // half panels per K-step
+        offsets_of(ov ? k_end - T::BK : 0);
+        for (int i = 0; i < panels; ++i) issue(0, i);
+        if (GRAD && ov && k_end < T::BK) offsets_of(0);
+        if (nk > 1)
+            for (int i = 0; i < panels; ++i) issue(1, i);
         if (ov) {
             // zeros over the first ov k of both panels, once the whole step has landed everywhere
-            if (nk > 1) wait_vm<2 * (T::A_LD + T::B_LD)>();
+            if (nk > 1) wait_vm<(LO ? 1 : 2) * T::A_LD + 2 * T::B_LD>();
             else wait_vm<0>();
             bare_barrier();
             lds_char *st = (lds_char *)lds;
             auto zero = [&](int off, int rows, bool t) {
                 for (int e = threadIdx.x; e < rows * 8; e += T::NT) {
                     lds_u32x4 *q = (lds_u32x4 *)(st + off + 16 * e);
-                    if (t) {  // rows of k: 2 rows / 16 chunks each
+                    if (t) {  // rows of k, rows / 8 chunks each
                         if (e / (rows / 8) < ov) *q = u32x4{0u, 0u, 0u, 0u};
                     } else {
                         const int row = e / 8, c = (e % 8) ^ swz_d(row);
@@ -401,14 +413,13 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
                     }
                 }
             };
-#pragma unroll
             for (int h = 0; h < 2; ++h) {
-                zero(T::A_OFF[h], T::RH, T::AT);
+                if (h == 0 || !LO) zero(T::A_OFF[h], T::RH, T::AT);
                 zero(T::B_OFF[h], T::CH, T::BT);
             }
             wait_reads();
         } else {
-            wait_halves<T, 1, 6>(min(halves, 8) - 2);
+            wait_halves<T, 1, 6, panels>(min(halves, 2 * panels) - 2);
         }
         bare_barrier();
 #pragma unroll
@@ -417,17 +428,28 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         for (int r = 0; r < 4 * T::FN; ++r) read_b((const lds_char *)lds + T::B_OFF[0], r, b[0]);
         wait_reads();
         bare_barrier();
-        if (nk > 2) issue(2, 0);
         using S0 = std::integral_constant<int, 0>;
         using S1 = std::integral_constant<int, 1>;
         int kt = 0;
-        for (; kt + 4 < nk; kt += 2) {
-            k_step(kt, S0(), std::true_type());
-            k_step(kt + 1, S1(), std::true_type());
-        }
-        for (; kt < nk; kt += 2) {
-            k_step(kt, S0(), std::false_type());
-            if (kt + 1 < nk) k_step(kt + 1, S1(), std::false_type());
+        if constexpr (LO) {
+            for (; kt + 3 < nk; kt += 2) {
+                k_step_lo(kt, S0(), std::true_type());
+                k_step_lo(kt + 1, S1(), std::true_type());
+            }
+            for (; kt < nk; kt += 2) {
+                k_step_lo(kt, S0(), std::false_type());
+                if (kt + 1 < nk) k_step_lo(kt + 1, S1(), std::false_type());
+            }
+        } else {
+            if (nk > 2) issue(2, 0);
+            for (; kt + 4 < nk; kt += 2) {
+                k_step(kt, S0(), std::true_type());
+                k_step(kt + 1, S1(), std::true_type());
+            }
+            for (; kt < nk; kt += 2) {
+                k_step(kt, S0(), std::false_type());
+                if (kt + 1 < nk) k_step(kt + 1, S1(), std::false_type());
+            }
         }
     }
 
@@ -447,7 +469,7 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         for (int e = 0; e < 8; ++e) sb[e] = e < last ? p.sb[(int64_t)g * p.stride_sb + n + e] : 0.f;
     }
 #pragma unroll
-    for (int qa = 0; qa < 2; ++qa) {
+    for (int qa = 0; qa < HA; ++qa) {
         if (mb0 + qa * T::RH >= m_end) break;
         wait_reads();
         bare_barrier();  // every wave is done with the stages, or with the half before
@@ -481,6 +503,50 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
             else store_row<OutType<2>::T>(p.C, at, v, first, last);
         }
     }
+}
+
+template <class T, bool GRAD>
+__global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
+
+    const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
+    const int64_t bid = linear_block();
+    int g, m0, m_end, n0, k_lo, k_end;
+    if constexpr (GRAD) {
+        const unsigned tiles_m = (unsigned)((p.K + T::BM - 1) / T::BM);
+        const unsigned per = tiles_m * tiles_n;
+        if (bid >= (int64_t)per * p.groups) return;
+        // each group's tiles over all XCDs: the groups' sums differ in length
+        unsigned tm, tn;
+        g = (int)((unsigned)bid / per);
+        tile_of_group_block((unsigned)bid - g * per, per, tiles_m, tiles_n, tm, tn);
+        m0 = (int)tm * T::BM;
+        n0 = (int)tn * T::BN;
+        m_end = p.K;
+        group_range(p.offsets, g, p.M, k_lo, k_end);
+    } else {
+        const unsigned tiles_m = count_row_tiles<T::BM>(p);
+        if (bid >= (int64_t)tiles_m * tiles_n) return;
+        unsigned tm, tn;
+        tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        // offsets that decrease can count more tiles than 32 bits hold
+        RowTile t;
+        if (tn >= tiles_n || !find_row_tile<T::BM>(p, tm, t)) return;
+        g = t.g;
+        m0 = t.row0;
+        m_end = t.hi;
+        n0 = (int)tn * T::BN;
+        k_lo = 0;
+        k_end = p.K;
+    }
+    g = __builtin_amdgcn_readfirstlane(g);
+    m0 = __builtin_amdgcn_readfirstlane(m0);
+    m_end = __builtin_amdgcn_readfirstlane(m_end);
+    k_lo = __builtin_amdgcn_readfirstlane(k_lo);
+    k_end = __builtin_amdgcn_readfirstlane(k_end);
+    if (m_end - m0 <= T::RH) tile_body<T, GRAD, true>(p, lds, g, m0, m_end, n0, k_lo, k_end);
+    else tile_body<T, GRAD, false>(p, lds, g, m0, m_end, n0, k_lo, k_end);
 }
 
 // The tile takes the shape: K-steps fit (or, in gradient mode, rows of any number), the columns of
