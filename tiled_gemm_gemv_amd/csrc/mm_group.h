@@ -34,39 +34,52 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// An element type: its storage, its accumulator over 16 values of a 32 x 32 block, and the
-// MFMA that multiplies 32 rows by 32 columns over 32 bytes of k: lane l supplies the 16
-// bytes at k byte 16 (l / 32) of row (or column) l % 32.
+// An element type: its storage, and the MFMAs that multiply B = 32 rows by 32 columns over 32 bytes
+// of k, or B = 16 by 16 over 64 bytes: lane l supplies the 16 bytes at k byte 16 (l / B) of row
+// (column) l % B. Acc<B>: a lane's values of the block, of column l % B: rows 8 (r / 4) + 4 (l / 32)
+// + r % 4, r < 16, for B = 32; rows 4 (l / 16) + r, r < 4, for B = 16.
+template <int B, class V4, class V16>
+using BlockAcc = std::conditional_t<B == 32, V16, V4>;
+
 struct ElemBf16 {
     typedef unsigned short T;
-    typedef f32x16 Acc;
     static constexpr bool INT8 = false;
-    static __device__ __forceinline__ Acc mma(u32x4 a, u32x4 b, Acc c)
+    template <int B>
+    using Acc = BlockAcc<B, f32x4, f32x16>;
+    template <int B>
+    static __device__ __forceinline__ Acc<B> mma(u32x4 a, u32x4 b, Acc<B> c)
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
-                                                       c, 0, 0, 0);
+        const bf16x8 x = __builtin_bit_cast(bf16x8, a), y = __builtin_bit_cast(bf16x8, b);
+        if constexpr (B == 32) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+        else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
     }
 };
 struct ElemF16 {
     typedef unsigned short T;
-    typedef f32x16 Acc;
     static constexpr bool INT8 = false;
-    static __device__ __forceinline__ Acc mma(u32x4 a, u32x4 b, Acc c)
+    template <int B>
+    using Acc = BlockAcc<B, f32x4, f32x16>;
+    template <int B>
+    static __device__ __forceinline__ Acc<B> mma(u32x4 a, u32x4 b, Acc<B> c)
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b),
-                                                      c, 0, 0, 0);
+        const f16x8 x = __builtin_bit_cast(f16x8, a), y = __builtin_bit_cast(f16x8, b);
+        if constexpr (B == 32) return __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, c, 0, 0, 0);
+        else return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
     }
 };
 // Sums of 8-bit products are exact in 32 bits: |sum| <= 2^14 K, and the host admits
 // K <= 2^17 - 1.
 struct ElemI8 {
     typedef signed char T;
-    typedef i32x16 Acc;
     static constexpr bool INT8 = true;
-    static __device__ __forceinline__ Acc mma(u32x4 a, u32x4 b, Acc c)
+    template <int B>
+    using Acc = BlockAcc<B, i32x4, i32x16>;
+    template <int B>
+    static __device__ __forceinline__ Acc<B> mma(u32x4 a, u32x4 b, Acc<B> c)
     {
-        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
-                                                     c, 0, 0, 0);
+        const i32x4 x = __builtin_bit_cast(i32x4, a), y = __builtin_bit_cast(i32x4, b);
+        if constexpr (B == 32) return __builtin_amdgcn_mfma_i32_32x32x32_i8(x, y, c, 0, 0, 0);
+        else return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
     }
 };
 

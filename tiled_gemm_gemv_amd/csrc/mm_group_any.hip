@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void group_any_kernel(GroupArgs p)
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-    typename E::Acc acc;
+    typename E::template Acc<32> acc;
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[r] = 0;
 
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256) void group_any_kernel(GroupArgs p)
         for (int s = 0; s < kStepBytes / 32; ++s) {
             const char *a = lds + (wm + (lane & 31)) * kPitch + 32 * s + 16 * (lane >> 5);
             const char *b = lds + (kTile + wn + (lane & 31)) * kPitch + 32 * s + 16 * (lane >> 5);
-            acc = E::mma(*reinterpret_cast<const u32x4 *>(a), *reinterpret_cast<const u32x4 *>(b), acc);
+            acc = E::template mma<32>(*reinterpret_cast<const u32x4 *>(a), *reinterpret_cast<const u32x4 *>(b), acc);
         }
         __syncthreads();
     }

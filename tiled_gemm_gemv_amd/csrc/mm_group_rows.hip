@@ -20,37 +20,11 @@
 namespace mm {
 namespace {
 
-// 16x16 MFMAs: the accumulator of lane l holds column l % 16 and rows 4 (l / 16) + r, r = 0..3
-struct Rows16Bf16 : ElemBf16 {
-    typedef f32x4 Acc4;
-    static __device__ __forceinline__ Acc4 mma4(u32x4 a, u32x4 b, Acc4 c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
-                                                       0, 0, 0);
-    }
-};
-struct Rows16F16 : ElemF16 {
-    typedef f32x4 Acc4;
-    static __device__ __forceinline__ Acc4 mma4(u32x4 a, u32x4 b, Acc4 c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
-                                                      0, 0);
-    }
-};
-struct Rows16I8 : ElemI8 {
-    typedef i32x4 Acc4;
-    static __device__ __forceinline__ Acc4 mma4(u32x4 a, u32x4 b, Acc4 c)
-    {
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0,
-                                                     0, 0);
-    }
-};
-
 // Partial sums of the W waves added in wave order and stored. `mine` holds NC x 4 values per lane:
 // value (c, r) is row 4 (lane / 16) + r, column COLS_C * (lane % 16) + c  (columns 16 c + lane % 16
 // where COLS_C is 0).
 template <class E, int W, int NC, int COLS_C>
-__device__ __forceinline__ void join_and_store(const GroupArgs &p, const typename E::Acc4 (&mine)[NC], char *lds, int g,
+__device__ __forceinline__ void join_and_store(const GroupArgs &p, const typename E::template Acc<16> (&mine)[NC], char *lds, int g,
                                                int row0, int row_end, int n0)
 {
     typedef decltype(mine[0][0] + 0) V;
@@ -118,11 +92,11 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
         b[j] = static_cast<const char *>(p.B) +
                (t.g * p.stride_b + min((int64_t)n0 + 16 * j + (lane & 15), (int64_t)p.N - 1) * p.ldb) * (int)sizeof(T) +
                16 * (lane >> 4);
-    typename E::Acc4 acc[RB][NB];
+    typename E::template Acc<16> acc[RB][NB];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = typename E::Acc4{0, 0, 0, 0};
+        for (int j = 0; j < NB; ++j) acc[i][j] = typename E::template Acc<16>{0, 0, 0, 0};
 
     const int64_t whole = kb / 128;  // whole slices; wave w takes w, w + W, ...
     u32x4 av[J][2][RB], bv[J][2][NB];
@@ -142,7 +116,7 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
 #pragma unroll
             for (int i = 0; i < RB; ++i)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] = E::mma4(av[x][h][i], bv[x][h][j], acc[i][j]);
+                for (int j = 0; j < NB; ++j) acc[i][j] = E::template mma<16>(av[x][h][i], bv[x][h][j], acc[i][j]);
     };
     // J slices loaded ahead; a slice is multiplied, then its registers take the slice J further on
     if (whole > 0) {
@@ -169,7 +143,7 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
             for (int j = 0; j < NB; ++j) {
                 const u32x4 bb = load16_upto<T>(b[j] + at + 64 * h, valid, kb);
 #pragma unroll
-                for (int i = 0; i < RB; ++i) acc[i][j] = E::mma4(aa[i], bb, acc[i][j]);
+                for (int i = 0; i < RB; ++i) acc[i][j] = E::template mma<16>(aa[i], bb, acc[i][j]);
             }
         }
     }
@@ -229,11 +203,11 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
     const int cols = (int)(p.N - col < CPL && p.N > col ? p.N - col : CPL);
     const T *b = static_cast<const T *>(p.B) + t.g * p.stride_b + (int64_t)(8 * (lane >> 4)) * p.ldb +
                  min(col, (int64_t)p.N - CPL);
-    typename E::Acc4 acc[RB][CPL];
+    typename E::template Acc<16> acc[RB][CPL];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) acc[i][c] = typename E::Acc4{0, 0, 0, 0};
+        for (int c = 0; c < CPL; ++c) acc[i][c] = typename E::template Acc<16>{0, 0, 0, 0};
 
     u32x4 av[J][RB];
     unsigned bv[J][8][CPL / 2];
@@ -259,7 +233,7 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
                 o[q] = __builtin_amdgcn_perm(bb[2 * q + 1][c >> 1], bb[2 * q][c >> 1],
                                              (c & 1) ? 0x07060302u : 0x05040100u);
 #pragma unroll
-            for (int i = 0; i < RB; ++i) acc[i][c] = E::mma4(aa[i], o, acc[i][c]);
+            for (int i = 0; i < RB; ++i) acc[i][c] = E::template mma<16>(aa[i], o, acc[i][c]);
         }
     };
     const int whole = p.K / 32;
@@ -379,10 +353,10 @@ double group_rows_time(const GroupArgs &a, int rows)
 
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream)
 {
-    if (a.elem == GroupElem::I8) return rows_d<Rows16I8>(a, rows, stream);
+    if (a.elem == GroupElem::I8) return rows_d<ElemI8>(a, rows, stream);
     if (a.trans_b)
-        return a.elem == GroupElem::F16 ? rows_d<Rows16F16>(a, rows, stream) : rows_d<Rows16Bf16>(a, rows, stream);
-    return a.elem == GroupElem::F16 ? rows_t<Rows16F16>(a, rows, stream) : rows_t<Rows16Bf16>(a, rows, stream);
+        return a.elem == GroupElem::F16 ? rows_d<ElemF16>(a, rows, stream) : rows_d<ElemBf16>(a, rows, stream);
+    return a.elem == GroupElem::F16 ? rows_t<ElemF16>(a, rows, stream) : rows_t<ElemBf16>(a, rows, stream);
 }
 
 }  // namespace mm

@@ -45,13 +45,15 @@ typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-template <class E_, bool AT_, bool BT_, int RH_, int CH_, int GM_, int GN_>
+template <class E_, bool AT_, bool BT_, int RH_, int CH_, int GM_, int GN_, int MB_>
 struct GroupTile {
     typedef E_ E;
     static constexpr bool AT = AT_, BT = BT_;
     static constexpr int RH = RH_, CH = CH_, GM = GM_, GN = GN_, BM = 2 * RH, BN = 2 * CH;
     static constexpr int WAVES = GM * GN, NT = 64 * WAVES;
-    static constexpr int QM = RH / GM, QN = CH / GN, FM = QM / 32, FN = QN / 32;
+    static constexpr int QM = RH / GM, QN = CH / GN;
+    static constexpr int MB = MB_, FM = QM / MB, FN = QN / MB;  // MFMA blocks of a wave's part
+    static constexpr int KS = MB == 32 ? 4 : 2, ACC = MB * MB / 64;  // MFMA steps per K-step, values per lane and block
     static constexpr int ES = sizeof(typename E::T), BK = 128 / ES;
     static constexpr int A_HALF = RH * 128, B_HALF = CH * 128;  // bytes of a half panel
     static constexpr int STAGE = 2 * (A_HALF + B_HALF);
@@ -61,7 +63,7 @@ struct GroupTile {
     // offsets of the half panels in a stage
     static constexpr int A_OFF[2] = {0, A_HALF}, B_OFF[2] = {2 * A_HALF, 2 * A_HALF + B_HALF};
     static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
-    static_assert(QM % 32 == 0 && QN % 32 == 0, "whole 32 x 32 blocks");
+    static_assert(QM % MB == 0 && QN % MB == 0, "whole blocks");
     static_assert(LDS <= 160 * 1024, "two stages in LDS");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
     static_assert((!AT || RH >= 64) && (!BT || CH >= 64), "T rows of at least the 8 chunks that swz_t permutes");
@@ -77,8 +79,8 @@ template <int W>
 __device__ __forceinline__ int swz_t(int krow)
 {
     static_assert(W == 64 || W == 128, "rows of 8 or 16 chunks: the permuted index stays inside the row");
-    if constexpr (W == 64) return ((krow >> 1) & 1) * 4;
-    else return (krow & 3) * 4;
+    if constexpr (W == 64) return ((krow >> 1) & 1) * 4 ^ ((krow >> 3) & 1) * 2;
+    else return (krow & 3) * 4 ^ ((krow >> 3) & 1) * 2;
 }
 
 // 16 bytes per lane from base + voff into LDS at lds_addr + 16 lane (lds_addr, base wave-uniform).
@@ -231,13 +233,15 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     };
 
     // ---- operand reads: 32 bytes of k (MFMA step ks) of the 32-wide block blk of a half panel
-    int d_off[4];
+    int d_off[T::KS];
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) d_off[ks] = (lane & 31) * 128 + 16 * ((2 * ks + (lane >> 5)) ^ swz_d(lane & 31));
+    for (int ks = 0; ks < T::KS; ++ks)
+        d_off[ks] = (lane % T::MB) * 128 + 16 * ((8 / T::KS * ks + lane / T::MB) ^ swz_d(lane % T::MB));
     const int t_g = lane >> 4, t_j = lane & 15;
     auto t_offset = [&](int blk, auto width) {
         constexpr int W = decltype(width)::value;
-        const int krow = 8 * (t_g >> 1) + (t_j >> 2), col = 32 * blk + 16 * (t_g & 1) + 4 * (t_j & 3);
+        const int krow = 8 * (T::MB == 32 ? t_g >> 1 : t_g) + (t_j >> 2);
+        const int col = T::MB * blk + (T::MB == 32 ? 16 * (t_g & 1) : 0) + 4 * (t_j & 3);
         return krow * 2 * W + 16 * ((col >> 3) ^ swz_t<W>(krow)) + 8 * ((col >> 2) & 1);
     };
     int a_toff[T::FM], b_toff[T::FN];
@@ -246,32 +250,33 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) b_toff[j] = t_offset(wn * T::FN + j, std::integral_constant<int, T::CH>());
     auto read_d = [&](const lds_char *half, int blk, int ks) {
-        return *(const lds_u32x4 *)(half + blk * 4096 + d_off[ks]);
+        return *(const lds_u32x4 *)(half + blk * T::MB * 128 + d_off[ks]);
     };
     auto read_t = [&](const lds_char *half, int toff, int ks, int row_bytes) {
+        constexpr int rows = T::BK / T::KS;
         const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) v4i16 *)(half + toff + 16 * ks * row_bytes));
+            (__attribute__((address_space(3))) v4i16 *)(half + toff + rows * ks * row_bytes));
         const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) v4i16 *)(half + toff + (16 * ks + 4) * row_bytes));
+            (__attribute__((address_space(3))) v4i16 *)(half + toff + (rows * ks + 4) * row_bytes));
         const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
         return u32x4{l2[0], l2[1], h2[0], h2[1]};
     };
     // operands: a[0], a[1]: A lo, A hi; b[s], b[s ^ 1]: B lo, B hi in a K-step of parity s
-    u32x4 a[2][4][T::FM], b[2][4][T::FN];
-    // operand number r (of 4 FM, 4 FN) of a half panel
-    auto read_a = [&](const lds_char *half, int r, u32x4 (&dst)[4][T::FM]) {
+    u32x4 a[2][T::KS][T::FM], b[2][T::KS][T::FN];
+    // operand number r (of KS FM, KS FN) of a half panel
+    auto read_a = [&](const lds_char *half, int r, u32x4 (&dst)[T::KS][T::FM]) {
         const int ks = r / T::FM, i = r % T::FM;
         if constexpr (T::AT) dst[ks][i] = read_t(half, a_toff[i], ks, 2 * T::RH);
         else dst[ks][i] = read_d(half, wm * T::FM + i, ks);
     };
-    auto read_b = [&](const lds_char *half, int r, u32x4 (&dst)[4][T::FN]) {
+    auto read_b = [&](const lds_char *half, int r, u32x4 (&dst)[T::KS][T::FN]) {
         const int ks = r / T::FN, j = r % T::FN;
         if constexpr (T::BT) dst[ks][j] = read_t(half, b_toff[j], ks, 2 * T::CH);
         else dst[ks][j] = read_d(half, wn * T::FN + j, ks);
     };
 
     constexpr int HA = LO ? 1 : 2;  // halves of rows
-    typename E::Acc acc[HA][2][T::FM][T::FN];
+    typename E::template Acc<T::MB> acc[HA][2][T::FM][T::FN];
 #pragma unroll
     for (int qa = 0; qa < HA; ++qa)
 #pragma unroll
@@ -281,7 +286,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[qa][qb][i][j][r] = 0;
+                    for (int r = 0; r < T::ACC; ++r) acc[qa][qb][i][j][r] = 0;
 
     auto wait_reads = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
 
@@ -292,7 +297,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         constexpr bool FULL = decltype(FULL_)::value;
         constexpr int qa = I >= 2, qb = I == 1 || I == 2;
         constexpr bool reads_a = I == 1 || I == 2;
-        constexpr int NM = 4 * T::FM * T::FN, NR = 4 * (reads_a ? T::FM : T::FN);
+        constexpr int NM = T::KS * T::FM * T::FN, NR = T::KS * (reads_a ? T::FM : T::FN);
         constexpr int issues = (I + 1) % 4;  // the half panel issued: A lo in phase 3, B lo, B hi, A hi
         constexpr int NL = issues == 0 || issues == 3 ? T::A_LD : T::B_LD;
         constexpr int pre = NM / 8;          // MFMAs before the barrier
@@ -303,7 +308,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                                (reads_a ? T::A_OFF[I == 1] : T::B_OFF[I == 0]);
         auto mfma = [&](int m) {
             const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
-            acc[qa][qb][i][j] = E::mma(a[qa][ks][i], b[S ^ qb][ks][j], acc[qa][qb][i][j]);
+            acc[qa][qb][i][j] = E::template mma<T::MB>(a[qa][ks][i], b[S ^ qb][ks][j], acc[qa][qb][i][j]);
         };
         auto read = [&](int r) {
             if constexpr (reads_a) read_a(half, r, a[I == 1]);
@@ -340,13 +345,13 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     auto phase_lo = [&](int kt, auto I_, auto S_, auto FULL_) {
         constexpr int I = decltype(I_)::value, S = decltype(S_)::value;
         constexpr bool FULL = decltype(FULL_)::value;
-        constexpr int NM = 4 * T::FM * T::FN, NA = I == 1 ? 4 * T::FM : 0, NR = NA + 4 * T::FN;
+        constexpr int NM = T::KS * T::FM * T::FN, NA = I == 1 ? T::KS * T::FM : 0, NR = NA + T::KS * T::FN;
         constexpr int NL = I == 0 ? T::A_LD + T::B_LD : T::B_LD;  // phase 0 issues A lo, B lo, phase 1 B hi
         constexpr int pre = NM / 8, items = NR + NL, slots = NM - pre;
         const lds_char *stage = (const lds_char *)lds + ((kt + I) & 1) * T::STAGE;
         auto mfma = [&](int m) {
             const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
-            acc[0][I][i][j] = E::mma(a[S][ks][i], b[I][ks][j], acc[0][I][i][j]);
+            acc[0][I][i][j] = E::template mma<T::MB>(a[S][ks][i], b[I][ks][j], acc[0][I][i][j]);
         };
 #pragma unroll
         for (int m = 0; m < pre; ++m) mfma(m);
@@ -423,9 +428,9 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         }
         bare_barrier();
 #pragma unroll
-        for (int r = 0; r < 4 * T::FM; ++r) read_a((const lds_char *)lds + T::A_OFF[0], r, a[0]);
+        for (int r = 0; r < T::KS * T::FM; ++r) read_a((const lds_char *)lds + T::A_OFF[0], r, a[0]);
 #pragma unroll
-        for (int r = 0; r < 4 * T::FN; ++r) read_b((const lds_char *)lds + T::B_OFF[0], r, b[0]);
+        for (int r = 0; r < T::KS * T::FN; ++r) read_b((const lds_char *)lds + T::B_OFF[0], r, b[0]);
         wait_reads();
         bare_barrier();
         using S0 = std::integral_constant<int, 0>;
@@ -480,9 +485,9 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        tile[(wm * T::QM + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * T::PITCH + qb * T::CH +
-                             wn * T::QN + 32 * j + (lane & 31)] = acc[qa][qb][i][j][r];
+                    for (int r = 0; r < T::ACC; ++r)
+                        tile[(wm * T::QM + T::MB * i + 8 * (r >> 2) + 4 * (lane / T::MB) + (r & 3)) * T::PITCH +
+                             qb * T::CH + wn * T::QN + T::MB * j + lane % T::MB] = acc[qa][qb][i][j][r];
         __syncthreads();
         for (int row = threadIdx.x / per_row; row < T::RH; row += T::NT / per_row) {
             const int m = mb0 + qa * T::RH + row;
@@ -581,8 +586,8 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
 // Both tiles have the operands' requirements in common but for the size.
 template <class E, bool AT, bool BT>
 struct Tiles {
-    using Large = GroupTile<E, AT, BT, 128, 128, 2, 4>;
-    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 2>;
+    using Large = GroupTile<E, AT, BT, 128, 128, 2, 4, 16>;
+    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 2, 16>;
     static bool ok(const GroupArgs &a, bool large) { return large ? tile_ok<Large, AT>(a) : tile_ok<Mid, AT>(a); }
     static hipError_t launch(const GroupArgs &a, bool large, hipStream_t stream)
     {
