@@ -587,7 +587,7 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
 template <class E, bool AT, bool BT>
 struct Tiles {
     using Large = GroupTile<E, AT, BT, 128, 128, 2, 4, 16>;
-    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 2, 16>;
+    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 2, 32>;
     static bool ok(const GroupArgs &a, bool large) { return large ? tile_ok<Large, AT>(a) : tile_ok<Mid, AT>(a); }
     static hipError_t launch(const GroupArgs &a, bool large, hipStream_t stream)
     {
@@ -620,12 +620,12 @@ double group_tile_time(const GroupArgs &a, bool large)
         // the groups' sizes are not known here, so neither is the number of rounds: between whole ones
         const bool known = a.grad || !a.offsets || a.groups == 1;
         const double rounds = known ? ceil(tiles / 256) : fmax(1.0, tiles / 256 + 0.25);
-        time = rounds * (6 + 1.45 * steps);
+        time = rounds * (6 + 1.35 * steps);
     } else {
         const double full = floor(tiles / 512), rest = tiles / 512 - full;
         time = full * (4 + 1.17 * steps) + (rest > 0.5 ? 4 + 1.17 * steps : rest > 0 ? 4 + 0.40 * steps : 0);
     }
-    return 3 + fmax(time, a.grad ? 0.0 : expected_weight_bytes(a) / 5.2e6);
+    return 3 + fmax(time, a.grad ? 0.0 : expected_weight_bytes(a) / 4.8e6);
 }
 
 bool group_tile_ok(const GroupArgs &a, bool large)
