@@ -142,14 +142,15 @@ __device__ __forceinline__ void group_range(const int64_t *offsets, int g, int M
     if (hi < lo) hi = lo;
 }
 
+// Sum over the lanes up to this one: within rows of 16 lanes, then the rows' sums.
 __device__ __forceinline__ unsigned wave_inclusive_sum(unsigned v)
 {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const unsigned u = __shfl_up(v, d);
-        if (lane >= d) v += u;
-    }
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15: to rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31: to rows 2 and 3
     return v;
 }
 
@@ -260,6 +261,39 @@ __device__ __forceinline__ void tile_of_group_block(unsigned bid, unsigned nbloc
     const unsigned in_g = logical - g * per_group;
     tm = first_m + in_g % gm;
     tn = in_g / gm;
+}
+
+// The row tile and tile column of workgroup bid (tiles_n tile columns); false: none. Wave-uniform,
+// every wave of the workgroup calls it. Offsets that decrease can count more tiles than 32 bits
+// hold: tn is checked, and find_row_tile returns rows of its group only.
+template <int BM>
+__device__ __forceinline__ bool group_tile_of_block(const GroupArgs &p, int64_t bid, unsigned tiles_n, RowTile &t,
+                                                    unsigned &tn)
+{
+    unsigned tm;
+    if (!p.offsets || p.groups > 64) {
+        const unsigned tiles_m = count_row_tiles<BM>(p);
+        if (bid >= (int64_t)tiles_m * tiles_n) return false;
+        tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        return tn < tiles_n && find_row_tile<BM>(p, tm, t);
+    }
+    // the same with the offsets read once
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = 0;
+    if (lane < p.groups) group_range(p.offsets, lane, p.M, lo, hi);
+    const unsigned cnt = (unsigned)((hi - lo + BM - 1) / BM), incl = wave_inclusive_sum(cnt);
+    const unsigned tiles_m = __builtin_amdgcn_readlane(incl, 63);
+    if (bid >= (int64_t)tiles_m * tiles_n) return false;
+    tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+    const unsigned long long above = __ballot(incl > tm);
+    if (tn >= tiles_n || !above) return false;
+    const int l = __ffsll(above) - 1;
+    const unsigned first = __builtin_amdgcn_readlane(incl - cnt, l);
+    t.g = l;
+    t.hi = __builtin_amdgcn_readlane(hi, l);
+    const int64_t row0 = __builtin_amdgcn_readlane(lo, l) + (int64_t)(tm - first) * BM;
+    t.row0 = (int)row0;
+    return tm >= first && row0 < t.hi;
 }
 
 }  // namespace

@@ -489,6 +489,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                         tile[(wm * T::QM + T::MB * i + 8 * (r >> 2) + 4 * (lane / T::MB) + (r & 3)) * T::PITCH +
                              qb * T::CH + wn * T::QN + T::MB * j + lane % T::MB] = acc[qa][qb][i][j][r];
         __syncthreads();
+#pragma unroll 2
         for (int row = threadIdx.x / per_row; row < T::RH; row += T::NT / per_row) {
             const int m = mb0 + qa * T::RH + row;
             if (m >= m_end || (T::AT && m < m0) || last <= first) continue;
@@ -531,13 +532,9 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
         m_end = p.K;
         group_range(p.offsets, g, p.M, k_lo, k_end);
     } else {
-        const unsigned tiles_m = count_row_tiles<T::BM>(p);
-        if (bid >= (int64_t)tiles_m * tiles_n) return;
-        unsigned tm, tn;
-        tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-        // offsets that decrease can count more tiles than 32 bits hold
         RowTile t;
-        if (tn >= tiles_n || !find_row_tile<T::BM>(p, tm, t)) return;
+        unsigned tn;
+        if (!group_tile_of_block<T::BM>(p, bid, tiles_n, t, tn)) return;
         g = t.g;
         m0 = t.row0;
         m_end = t.hi;
@@ -587,7 +584,7 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
 template <class E, bool AT, bool BT>
 struct Tiles {
     using Large = GroupTile<E, AT, BT, 128, 128, 2, 4, 16>;
-    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 2, 32>;
+    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 4, 16>;
     static bool ok(const GroupArgs &a, bool large) { return large ? tile_ok<Large, AT>(a) : tile_ok<Mid, AT>(a); }
     static hipError_t launch(const GroupArgs &a, bool large, hipStream_t stream)
     {
