@@ -645,11 +645,10 @@ def _mm_type(dtype, name):
     raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
 
 
-def _same_device(device, **tensors):
-    """Raise ValueError unless every given tensor is on the GPU with index `device`."""
-    for name, t in tensors.items():
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+def _same_device(t, name, device):
+    """Raise ValueError unless the tensor is on the GPU with index `device`."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
 def _stack(t, name, dtypes):
@@ -682,7 +681,7 @@ def _offsets(t, groups, device):
         raise TypeError("offsets must be an int64 tensor")
     if t.dim() != 1 or t.shape[0] != groups + 1 or not t.is_contiguous():
         raise ValueError(f"offsets must be contiguous, with groups + 1 = {groups + 1} entries")
-    _same_device(device, offsets=t)
+    _same_device(t, "offsets", device)
 
 
 def _scale(t, shape, name, device):
@@ -691,17 +690,18 @@ def _scale(t, shape, name, device):
         raise TypeError(f"{name} must be a float32 tensor")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {shape}")
-    _same_device(device, **{name: t})
+    _same_device(t, name, device)
 
 
 def _output(out, out_dtype, shape, like):
-    """(the output tensor, its MM_TYPE_*): `out` if given (its dtype must be out_dtype where that is
-    given too), else a new one of out_dtype (float32 by default) beside `like`."""
+    """(the output tensor, its MM_TYPE_*, leading dimension, group stride): `out` if given (its dtype
+    must be out_dtype where that is given too), else a new one of out_dtype (float32 by default)."""
     import torch
     if out is None:
         dtype = torch.float32 if out_dtype is None else out_dtype
         c_type = _mm_type(dtype, "out_dtype")
-        return like.new_empty(shape, dtype=dtype), c_type
+        cols = max(shape[-1], 1)
+        return like.new_empty(shape, dtype=dtype), c_type, cols, shape[-2] * cols
     if not isinstance(out, torch.Tensor):
         raise TypeError("out must be a torch.Tensor")
     c_type = _mm_type(out.dtype, "out")
@@ -709,8 +709,10 @@ def _output(out, out_dtype, shape, like):
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     if out.shape != shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {shape}")
-    _same_device(like.get_device(), out=out)
-    return out, c_type
+    _same_device(out, "out", like.get_device())
+    if len(shape) == 2:
+        return out, c_type, _matrix(out, "out", (out.dtype,)), 0
+    return (out, c_type) + _stack(out, "out", (out.dtype,))
 
 
 def gemm16_grouped(A, B, offsets, trans_b=False, out=None, out_dtype=None, stream=None):
@@ -731,10 +733,9 @@ def gemm16_grouped(A, B, offsets, trans_b=False, out=None, out_dtype=None, strea
         K2, N = N, K2
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
-    _same_device(device, B=B)
+    _same_device(B, "B", device)
     _offsets(offsets, groups, device)
-    out, c_type = _output(out, out_dtype, (M, N), A)
-    ldc = _matrix(out, "out", (out.dtype,))
+    out, c_type, ldc, _ = _output(out, out_dtype, (M, N), A)
     name = "mm_gemm_bf16_grouped" if A.dtype is torch.bfloat16 else "mm_gemm_f16_grouped"
     _run(name, device, stream, groups, M, N, K, offsets.data_ptr(), A.data_ptr(), lda, B.data_ptr(), ldb,
          stride_b, 1 if trans_b else 0, out.data_ptr(), c_type, ldc)
@@ -754,13 +755,12 @@ def gemm16_grouped_grad_b(A, G, offsets, out=None, out_dtype=None, stream=None):
     M2, N = G.shape
     if M2 != M:
         raise ValueError(f"row counts differ: {tuple(A.shape)}, {tuple(G.shape)}")
-    _same_device(device, G=G)
+    _same_device(G, "G", device)
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be a 1-D tensor of groups + 1 entries")
     groups = offsets.shape[0] - 1
     _offsets(offsets, groups, device)
-    out, d_type = _output(out, out_dtype, (groups, K, N), A)
-    ldd, stride_d = _stack(out, "out", (out.dtype,))
+    out, d_type, ldd, stride_d = _output(out, out_dtype, (groups, K, N), A)
     if groups > 1 and K > 0 and N > 0 and stride_d < (K - 1) * ldd + N:
         raise ValueError("the matrices of out overlap")
     name = "mm_gemm_bf16_grouped_grad_b" if A.dtype is torch.bfloat16 else "mm_gemm_f16_grouped_grad_b"
@@ -782,7 +782,7 @@ def quantize_i8(x, out=None, scale=None, stream=None):
         ldq = _matrix(out, "out", (torch.int8,))
         if out.shape != x.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, cols)}")
-        _same_device(device, out=out)
+        _same_device(out, "out", device)
     if scale is None:
         scale = x.new_empty(rows, dtype=torch.float32)
     else:
@@ -803,11 +803,10 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
     N, K2 = B.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
-    _same_device(device, B=B)
+    _same_device(B, "B", device)
     _scale(a_scale, (M,), "a_scale", device)
     _scale(b_scale, (N,), "b_scale", device)
-    out, c_type = _output(out, out_dtype, (M, N), A)
-    ldc = _matrix(out, "out", (out.dtype,))
+    out, c_type, ldc, _ = _output(out, out_dtype, (M, N), A)
     _run("mm_gemm_i8", device, stream, M, N, K, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb,
          b_scale.data_ptr(), out.data_ptr(), c_type, ldc)
     return out
@@ -824,12 +823,11 @@ def gemm_i8_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, s
     groups, N, K2 = B.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
-    _same_device(device, B=B)
+    _same_device(B, "B", device)
     _offsets(offsets, groups, device)
     _scale(a_scale, (M,), "a_scale", device)
     _scale(b_scale, (groups, N), "b_scale", device)
-    out, c_type = _output(out, out_dtype, (M, N), A)
-    ldc = _matrix(out, "out", (out.dtype,))
+    out, c_type, ldc, _ = _output(out, out_dtype, (M, N), A)
     _run("mm_gemm_i8_grouped", device, stream, groups, M, N, K, offsets.data_ptr(), A.data_ptr(), lda,
          a_scale.data_ptr(), B.data_ptr(), ldb, stride_b, b_scale.data_ptr(), out.data_ptr(), c_type, ldc)
     return out
