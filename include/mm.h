@@ -282,7 +282,7 @@ typedef enum mm_type {
  *
  *   C[i][j] = sum over k in [0, K) of A[i][k] * B_g(i)[k][j]
  *
- *   groups    number of groups, 0 <= groups <= 65535.
+ *   groups    number of groups, 0 <= groups <= 4096.
  *   M         rows of A and C, N columns of C, K the inner size; each 0 .. 2^31 - 1.
  *   offsets   device memory, groups + 1 entries, 8-byte aligned: rows offsets[g] <= i <
  *             offsets[g + 1] are group g's. They are read on the device only (the call does

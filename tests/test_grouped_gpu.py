@@ -221,6 +221,118 @@ def test_many_groups(dev):
         check(host64(D), want, S, "int", torch.float32)
 
 
+def test_most_groups(dev):
+    # 4096 groups, a few of them with rows, at both ends too
+    counts = np.zeros(4096, int)
+    for g, c in ((0, 3), (63, 1), (64, 70), (1000, 17), (4094, 1), (4095, 130)):
+        counts[g] = c
+    off = ranges(counts)
+    A, W = draw(1, (off[-1], 64), "int", "bf16", dev), draw(2, (1, 64, 72), "int", "bf16", dev)
+    offsets = torch.tensor(off, device=dev)
+    C = mm.gemm16_grouped(A, W.expand(4096, 64, 72), offsets)
+    torch.cuda.synchronize()
+    assert np.array_equal(host64(C), host64(A) @ host64(W[0]))
+    D = mm.gemm16_grouped_grad_b(A, A[:, :16], offsets)
+    torch.cuda.synchronize()
+    D = host64(D)
+    assert not D[counts == 0].any()
+    for g in np.flatnonzero(counts):
+        a = host64(A)[off[g]:off[g + 1]]
+        assert np.array_equal(D[g], a.T @ a[:, :16]), g
+
+
+# Shapes of many tiles: those of 256 x 256 (and 128 x 128) with whole and partial K-steps, one K-step,
+# groups of one row, of a whole number of tiles, ending in a tile's first and second half, and N that
+# is no multiple of 8. References in float64 on the GPU.
+MANY_TILES = [
+    ([1500, 1, 0, 700, 1895], 4100, 136),
+    ([300, 3000, 256, 129], 4096, 777),
+    ([4096], 4128, 64),
+    ([2048, 2048 + 127], 4001, 1024),
+    ([3990, 13], 4096, 128),
+]
+
+
+def close(got, want, S, dist):
+    """got (any type) against float64 want on the GPU, as check() does on the host."""
+    if got.numel() == 0:  # an empty group's rows
+        return
+    if dist == "int":
+        assert torch.equal(got.double(), want.to(got.dtype).double())
+        return
+    tol = 1e-5 * S
+    if got.dtype != torch.float32:
+        tol = tol + want.abs() * (torch.finfo(got.dtype).eps / 2 * (1 + 2.0 ** -7)) + 2.0 ** -25
+    worst = ((got.double() - want).abs() / tol).nan_to_num(nan=1e30).max().item()
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("dtype,out,dist", [("bf16", "bf16", "normal"), ("f16", "f32", "int"), ("bf16", "f16", "int")])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("case", range(len(MANY_TILES)))
+def test_grouped16_many_tiles(dev, case, trans, dtype, out, dist):
+    counts, N, K = MANY_TILES[case]
+    off = ranges(counts)
+    gen = torch.Generator(device=dev).manual_seed(case)
+
+    def make(*shape):
+        if dist == "int":
+            return torch.randint(-2, 3, shape, generator=gen, device=dev).to(DT[dtype])
+        return torch.randn(shape, generator=gen, device=dev).to(DT[dtype])
+
+    A, B = make(off[-1], K), make(len(counts), N, K) if trans else make(len(counts), K, N)
+    C = mm.gemm16_grouped(A, B, torch.tensor(off, device=dev), trans_b=trans, out_dtype=DT[out])
+    for g in range(len(counts)):
+        a, w = A[off[g]:off[g + 1]].double(), B[g].double()
+        w = w.t().contiguous() if trans else w
+        close(C[off[g]:off[g + 1]], a @ w, a.abs() @ w.abs(), dist)
+
+
+@pytest.mark.parametrize("dtype,out,dist", [("bf16", "bf16", "normal"), ("f16", "f32", "int")])
+@pytest.mark.parametrize("counts,N,K", [([130, 0, 700], 2050, 2048), ([64, 1, 200, 66], 2304, 1928), ([1500], 4097, 4200),
+                                        ([3000, 5, 127], 2056, 2185)])
+def test_grad_b_many_tiles(dev, counts, N, K, dtype, out, dist):
+    off = ranges(counts)
+    gen = torch.Generator(device=dev).manual_seed(K)
+
+    def make(*shape):
+        if dist == "int":
+            return torch.randint(-2, 3, shape, generator=gen, device=dev).to(DT[dtype])
+        return torch.randn(shape, generator=gen, device=dev).to(DT[dtype])
+
+    A, G = make(off[-1], K), make(off[-1], N)
+    D = mm.gemm16_grouped_grad_b(A, G, torch.tensor(off, device=dev), out_dtype=DT[out])
+    for g in range(len(counts)):
+        a, b = A[off[g]:off[g + 1]].double().t().contiguous(), G[off[g]:off[g + 1]].double()
+        close(D[g], a @ b, a.abs() @ b.abs(), dist)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 128), (3000, 5003, 777), (4225, 4096, 1024), (8192, 2049, 130)])
+def test_i8_many_tiles(dev, M, N, K, out):
+    A, B = int8(1, (M, K), dev), int8(2, (N, K), dev)
+    sa, sb = scales(3, M, dev), scales(4, N, dev)
+    C = mm.gemm_i8(A, B, sa, sb, out_dtype=DT[out])
+    want = (A.double() @ B.double().t().contiguous()) * sa.double()[:, None] * sb.double()
+    half = 0 if out == "f32" else torch.finfo(DT[out]).eps / 2 * (1 + 2.0 ** -20)
+    err = (C.double() - want).abs()
+    assert (err <= want.abs() * (4 * 2.0 ** -24 + half)).all().item()
+
+
+def test_i8_no_inner_size(dev):
+    # the empty sum: zero times the scales
+    sa, sb = scales(3, 5, dev), scales(4, 40, dev)
+    sa[2] = float("nan")
+    e = torch.empty((5, 0), dtype=torch.int8, device=dev), torch.empty((40, 0), dtype=torch.int8, device=dev)
+    C = mm.gemm_i8(*e, sa, sb, out=torch.full((5, 40), 7.0, device=dev))
+    torch.cuda.synchronize()
+    assert torch.isnan(C[2]).all().item() and (C[[0, 1, 3, 4]] == 0).all().item()
+    C = mm.gemm_i8_grouped(e[0], e[1][None], torch.tensor([1, 5], device=dev), sa, sb[None],
+                           out=torch.full((5, 40), 7.0, device=dev))
+    torch.cuda.synchronize()
+    assert (C[0] == 7).all().item() and torch.isnan(C[2]).all().item() and (C[[1, 3, 4]] == 0).all().item()
+
+
 def test_shared_matrix_and_no_inner_size(dev):
     # group stride 0 shares B; K = 0 gives zero rows, rows of no group untouched
     A, B = draw(1, (70, 128), "int", "f16", dev), draw(2, (1, 128, 96), "int", "f16", dev)

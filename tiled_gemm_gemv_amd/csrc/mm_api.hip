@@ -242,7 +242,7 @@ int run_conv(int cfg, int64_t N, int64_t C, int64_t H, int64_t W, int64_t K, int
 
 // Largest K of the 8-bit products: sums of K products of magnitude up to 2^14 fit 32 bits.
 constexpr int64_t kMaxKInt8 = (int64_t(1) << 17) - 1;
-constexpr int64_t kMaxGroups = 65535;
+constexpr int64_t kMaxGroups = 4096;  // a workgroup finds its group among them by itself
 
 bool type_ok(int t) { return t == MM_TYPE_F32 || t == MM_TYPE_BF16 || t == MM_TYPE_F16; }
 int type_size(int t) { return t == MM_TYPE_F32 ? 4 : 2; }
@@ -260,7 +260,7 @@ bool strided_extent_fits(int64_t count, int64_t stride, int64_t rows, int64_t co
 int check_group(const mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, int64_t K, bool dense)
 {
     if (groups < 0 || M < 0 || N < 0 || K < 0) return invalid("negative size");
-    if (groups > kMaxGroups) return invalid("more than 65535 groups");
+    if (groups > kMaxGroups) return invalid("more than 4096 groups");
     if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return invalid("size above 2^31 - 1");
     const bool i8 = a.elem == mm::GroupElem::I8;
     if (i8 && K > kMaxKInt8) return invalid("K above 2^17 - 1 (sums of 8-bit products fit 32 bits up to there)");

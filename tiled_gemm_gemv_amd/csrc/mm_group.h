@@ -159,55 +159,70 @@ struct RowTile {
     int g, row0, hi;
 };
 
-// Number of BM-row tiles over all groups. Every wave of the workgroup calls it (64 groups
-// at a time, one per lane); the result is wave-uniform.
+// The groups' BM-row tiles, numbered in group order, and where a tile is. Every wave of a workgroup
+// builds it for itself (all values wave-uniform but `run`, `incl`, `lo`, `hi`): lane l counts the
+// tiles of groups l R .. l R + R - 1, R = ceil(groups / 64), and a scan over the lanes gives the
+// rest; up to 64 groups (R = 1) the lane keeps its group's range.
 template <int BM>
-__device__ __forceinline__ unsigned count_row_tiles(const GroupArgs &p)
-{
-    if (!p.offsets) return (unsigned)((p.M + BM - 1) / BM);
-    unsigned total = 0;
-    for (int base = 0; base < p.groups; base += 64) {
-        const int g = base + (threadIdx.x & 63);
-        int lo = 0, hi = 0;
-        if (g < p.groups) group_range(p.offsets, g, p.M, lo, hi);
-        const unsigned incl = wave_inclusive_sum((unsigned)((hi - lo + BM - 1) / BM));
-        total += __builtin_amdgcn_readlane(incl, 63);
-    }
-    return total;
-}
+struct RowTiles {
+    unsigned total;       // tiles in all
+    unsigned run, incl;   // tiles of this lane's groups, and of the lanes up to it
+    int R, lo, hi;
 
-// Row tile number rt in group order; false if there is none (never for rt below
-// count_row_tiles of the same offsets).
-template <int BM>
-__device__ __forceinline__ bool find_row_tile(const GroupArgs &p, unsigned rt, RowTile &t)
-{
-    if (!p.offsets) {
-        t.g = 0;
-        t.row0 = (int)rt * BM;
-        t.hi = p.M;
-        return (int64_t)rt * BM < p.M;
-    }
-    unsigned before = 0;
-    for (int base = 0; base < p.groups; base += 64) {
-        const int g = base + (threadIdx.x & 63);
-        int lo = 0, hi = 0;
-        if (g < p.groups) group_range(p.offsets, g, p.M, lo, hi);
-        const unsigned cnt = (unsigned)((hi - lo + BM - 1) / BM);
-        const unsigned incl = before + wave_inclusive_sum(cnt);
-        const unsigned long long above = __ballot(incl > rt);
-        if (above) {
-            const int l = __ffsll(above) - 1;
-            const unsigned first = __builtin_amdgcn_readlane(incl - cnt, l);
-            t.g = base + l;
-            t.hi = __builtin_amdgcn_readlane(hi, l);
-            const int64_t row0 = __builtin_amdgcn_readlane(lo, l) + (int64_t)(rt - first) * BM;
-            t.row0 = (int)row0;
-            return rt >= first && row0 < t.hi;
+    static __device__ __forceinline__ unsigned count(int lo, int hi) { return (unsigned)((hi - lo + BM - 1) / BM); }
+
+    __device__ __forceinline__ RowTiles(const GroupArgs &p)
+    {
+        if (!p.offsets) {
+            total = (unsigned)((p.M + BM - 1) / BM);
+            return;
         }
-        before = __builtin_amdgcn_readlane(incl, 63);
+        const int lane = threadIdx.x & 63;
+        R = (p.groups + 63) / 64;
+        run = 0;
+        lo = hi = 0;
+        for (int g = lane * R; g < min(lane * R + R, p.groups); ++g) {
+            group_range(p.offsets, g, p.M, lo, hi);
+            run += count(lo, hi);
+        }
+        incl = wave_inclusive_sum(run);
+        total = __builtin_amdgcn_readlane(incl, 63);
     }
-    return false;
-}
+
+    // Tile number rt. False if there is none; never for rt < total of offsets that do not decrease.
+    // Others may count more tiles than 32 bits hold: the rows returned are the group's all the same.
+    __device__ __forceinline__ bool find(const GroupArgs &p, unsigned rt, RowTile &t) const
+    {
+        if (!p.offsets) {
+            t.g = 0;
+            t.row0 = (int)rt * BM;
+            t.hi = p.M;
+            return (int64_t)rt * BM < p.M;
+        }
+        unsigned long long above = __ballot(incl > rt);
+        if (!above) return false;
+        int l = __ffsll(above) - 1;
+        unsigned first = __builtin_amdgcn_readlane(incl - run, l);  // the run's first tile
+        int from = lo, to = hi;
+        t.g = l;
+        if (R > 1) {  // the run's groups, one per lane (R <= 64)
+            const int i = threadIdx.x & 63, g = l * R + i;
+            from = to = 0;
+            if (i < R && g < p.groups) group_range(p.offsets, g, p.M, from, to);
+            const unsigned c = count(from, to), upto = first + wave_inclusive_sum(c);
+            above = __ballot(upto > rt);
+            if (!above) return false;
+            const int run0 = l * R;
+            l = __ffsll(above) - 1;
+            first = __builtin_amdgcn_readlane(upto - c, l);
+            t.g = run0 + l;
+        }
+        t.hi = __builtin_amdgcn_readlane(to, l);
+        const int64_t row0 = __builtin_amdgcn_readlane(from, l) + (int64_t)(rt - first) * BM;
+        t.row0 = (int)row0;
+        return rt >= first && row0 < t.hi;
+    }
+};
 
 // What the host expects of group sizes that it does not know, for the choice of a kernel: groups
 // with a row (rows spread at random), BM-row tiles (a group's last tile half full on average), and
@@ -264,36 +279,16 @@ __device__ __forceinline__ void tile_of_group_block(unsigned bid, unsigned nbloc
 }
 
 // The row tile and tile column of workgroup bid (tiles_n tile columns); false: none. Wave-uniform,
-// every wave of the workgroup calls it. Offsets that decrease can count more tiles than 32 bits
-// hold: tn is checked, and find_row_tile returns rows of its group only.
+// every wave of the workgroup calls it.
 template <int BM>
 __device__ __forceinline__ bool group_tile_of_block(const GroupArgs &p, int64_t bid, unsigned tiles_n, RowTile &t,
                                                     unsigned &tn)
 {
+    const RowTiles<BM> tiles(p);
+    if (bid >= (int64_t)tiles.total * tiles_n) return false;
     unsigned tm;
-    if (!p.offsets || p.groups > 64) {
-        const unsigned tiles_m = count_row_tiles<BM>(p);
-        if (bid >= (int64_t)tiles_m * tiles_n) return false;
-        tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-        return tn < tiles_n && find_row_tile<BM>(p, tm, t);
-    }
-    // the same with the offsets read once
-    const int lane = threadIdx.x & 63;
-    int lo = 0, hi = 0;
-    if (lane < p.groups) group_range(p.offsets, lane, p.M, lo, hi);
-    const unsigned cnt = (unsigned)((hi - lo + BM - 1) / BM), incl = wave_inclusive_sum(cnt);
-    const unsigned tiles_m = __builtin_amdgcn_readlane(incl, 63);
-    if (bid >= (int64_t)tiles_m * tiles_n) return false;
-    tile_of_group_block((unsigned)bid, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-    const unsigned long long above = __ballot(incl > tm);
-    if (tn >= tiles_n || !above) return false;
-    const int l = __ffsll(above) - 1;
-    const unsigned first = __builtin_amdgcn_readlane(incl - cnt, l);
-    t.g = l;
-    t.hi = __builtin_amdgcn_readlane(hi, l);
-    const int64_t row0 = __builtin_amdgcn_readlane(lo, l) + (int64_t)(tm - first) * BM;
-    t.row0 = (int)row0;
-    return tm >= first && row0 < t.hi;
+    tile_of_group_block((unsigned)bid, tiles.total * tiles_n, tiles.total, tiles_n, tm, tn);
+    return tn < tiles_n && tiles.find(p, tm, t);  // (tn: where the count overflowed)
 }
 
 }  // namespace

@@ -36,10 +36,10 @@ __global__ __launch_bounds__(256) void group_any_kernel(GroupArgs p)
         m_end = p.K;
         group_range(p.offsets, g, p.M, k_lo, k_end);
     } else {
-        const unsigned tiles_m = count_row_tiles<kTile>(p);
-        if (bid >= (int64_t)tiles_m * tiles_n) return;
+        const RowTiles<kTile> tiles(p);
+        if (bid >= (int64_t)tiles.total * tiles_n) return;
         RowTile t;
-        if (!find_row_tile<kTile>(p, (unsigned)(bid / tiles_n), t)) return;
+        if (!tiles.find(p, (unsigned)(bid / tiles_n), t)) return;
         g = t.g;
         m0 = t.row0;
         m_end = t.hi;

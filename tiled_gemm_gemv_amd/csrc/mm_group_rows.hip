@@ -63,7 +63,7 @@ __device__ __forceinline__ bool rows_tile(const GroupArgs &p, int cols, RowTile 
     const unsigned strips = (unsigned)(((int64_t)p.N + cols - 1) / cols);
     const int64_t bid = linear_block();
     const int64_t rt = bid / strips;
-    if (rt > 0x7fffffff || !find_row_tile<ROWS>(p, (unsigned)rt, t)) return false;
+    if (rt > 0x7fffffff || !RowTiles<ROWS>(p).find(p, (unsigned)rt, t)) return false;
     n0 = (int)((unsigned)(bid - rt * strips) * (unsigned)cols);
     t.g = __builtin_amdgcn_readfirstlane(t.g);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
