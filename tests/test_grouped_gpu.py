@@ -117,6 +117,9 @@ CASES = [
     ([40], 0, 0, 1000, 33),
     ([2, 3], 0, 0, 31, 4099),
     ([5, 1, 7], 0, 0, 2048, 1024),
+    ([1], 0, 0, 130, 2000),
+    ([0, 1, 1, 0], 1, 1, 37, 1024),
+    ([1, 0, 0, 1, 1, 1], 0, 0, 100, 4500),
 ]
 
 
@@ -427,7 +430,7 @@ def check_i8(got, want, dtype):
     assert (err[live] <= tol[live]).all(), float((err[live] / np.maximum(tol[live], 1e-300)).max())
 
 
-I8_SHAPES = [(1, 1, 1), (1, 16, 16), (3, 5, 7), (1, 256, 512), (2, 100, 128), (8, 136, 384), (16, 264, 200),
+I8_SHAPES = [(1, 1, 1), (1, 16, 16), (1, 33, 1024), (1, 70, 2049), (1, 515, 9000), (3, 5, 7), (1, 256, 512), (2, 100, 128), (8, 136, 384), (16, 264, 200),
              (17, 64, 128), (33, 130, 777), (64, 128, 256), (65, 300, 129), (100, 257, 1000), (129, 131, 640),
              (256, 256, 256), (300, 520, 1024), (700, 300, 2049), (513, 1031, 130)]
 

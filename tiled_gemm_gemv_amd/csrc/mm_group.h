@@ -235,7 +235,7 @@ inline double expected_groups(const GroupArgs &a)
 inline double expected_row_tiles(const GroupArgs &a, int bm)
 {
     const double groups = expected_groups(a), mean = a.M / groups;
-    if (!a.offsets || a.groups == 1) return (double)(((int64_t)a.M + bm - 1) / bm);
+    if (!a.offsets || a.groups == 1 || bm == 1) return (double)(((int64_t)a.M + bm - 1) / bm);
     return groups * (mean > bm / 2 ? mean / bm + 0.5 : 1.0);
 }
 inline double expected_weight_bytes(const GroupArgs &a)

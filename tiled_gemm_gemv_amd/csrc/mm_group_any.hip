@@ -132,7 +132,7 @@ hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream)
 // The kernel whose modelled time is least among those that take the shape.
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
 {
-    enum { kAny, kRows16, kRows32, kRows64, kMid, kLarge };
+    enum { kAny, kRows1, kRows16, kRows32, kRows64, kMid, kLarge };
     int best = kAny;
     double time = 1e300;
     auto offer = [&](int kernel, double t) {
@@ -144,6 +144,7 @@ hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
     constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
     if (a.M <= largest && a.N <= largest && a.K <= largest) {
         if (!a.grad) {
+            if (group_rows_ok(a, 1)) offer(kRows1, group_rows_time(a, 1));
             if (group_rows_ok(a, 16)) offer(kRows16, group_rows_time(a, 16));
             if (group_rows_ok(a, 32)) offer(kRows32, group_rows_time(a, 32));
             if (group_rows_ok(a, 64)) offer(kRows64, group_rows_time(a, 64));
@@ -152,6 +153,7 @@ hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
         if (group_tile_ok(a, true)) offer(kLarge, group_tile_time(a, true));
     }
     switch (best) {
+    case kRows1: return group_rows_launch(a, 1, stream);
     case kRows16: return group_rows_launch(a, 16, stream);
     case kRows32: return group_rows_launch(a, 32, stream);
     case kRows64: return group_rows_launch(a, 64, stream);

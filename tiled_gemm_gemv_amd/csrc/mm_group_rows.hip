@@ -15,10 +15,24 @@
 //     one column: a pair of rows is one v_perm_b32, 4 CPL of them for the lane's 8 CPL values.
 // A's rows come from L2 (every workgroup of a group reads the same rows); rows past the group's end
 // repeat its last row and are not stored.
+//
+// With one row to a group and B's rows along k, whole rows of B (1 KB per wave and load) stream
+// faster than the MFMA's 16 pieces of 64 bytes, and the vector units keep up: each wave takes J
+// columns, multiplies its lanes' 16-byte pieces with A's by dot products (v_dot4_i32_i8, or fp32
+// multiply-adds of the 16-bit values) and adds the 64 lanes' sums at the end (fixed order). Cold, i8
+// 1 x 14336 x 4096: 15.6 us through the MFMA, 12.1 this way; 8 rows for 8 of 64 groups of 4096 x 2048:
+// 13.8 and 13.2; with 4 rows at a time 14.4 and 17.4 (registers for fewer waves), so only for one.
 #include "mm_group.h"
 
 namespace mm {
 namespace {
+
+// The same for data read once (not kept in the caches).
+__device__ __forceinline__ u32x4 load16_once(const char *p)
+{
+    typedef unsigned int Words __attribute__((ext_vector_type(4), aligned(1)));
+    return __builtin_nontemporal_load(reinterpret_cast<const Words *>(p));
+}
 
 // Partial sums of the W waves added in wave order and stored. `mine` holds NC x 4 values per lane:
 // value (c, r) is row 4 (lane / 16) + r, column COLS_C * (lane % 16) + c  (columns 16 c + lane % 16
@@ -277,6 +291,108 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_t(GroupArgs p)
         join_and_store<E, W, CPL, CPL>(p, acc[i], lds, t.g, t.row0 + 16 * i, t.hi, n0);
 }
 
+// acc + the products of the 16 bytes x and y.
+template <class E>
+__device__ __forceinline__ auto dot16(u32x4 x, u32x4 y, decltype(typename E::template Acc<16>()[0] + 0) acc)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const unsigned a = x[q], b = y[q];
+        if constexpr (E::INT8) {
+            acc = __builtin_amdgcn_sdot4((int)a, (int)b, acc, false);
+        } else if constexpr (std::is_same_v<E, ElemBf16>) {
+            acc = fmaf(__builtin_bit_cast(float, a << 16), __builtin_bit_cast(float, b << 16), acc);
+            acc = fmaf(__builtin_bit_cast(float, a & 0xffff0000u), __builtin_bit_cast(float, b & 0xffff0000u), acc);
+        } else {
+            typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+            const h2 u = __builtin_bit_cast(h2, a), v = __builtin_bit_cast(h2, b);
+            acc = fmaf((float)u[0], (float)v[0], acc);
+            acc = fmaf((float)u[1], (float)v[1], acc);
+        }
+    }
+    return acc;
+}
+
+// Sum over the lanes, in lane 63 (rows of 16 lanes first, then the rows' sums).
+template <class V>
+__device__ __forceinline__ V wave_sum(V v)
+{
+    auto step = [&](auto ctrl, auto rows) {
+        v += __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value,
+                                                               decltype(rows)::value, 0xf, false));
+    };
+    step(std::integral_constant<int, 0x111>(), std::integral_constant<int, 0xf>());  // row_shr 1, 2, 4, 8
+    step(std::integral_constant<int, 0x112>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x114>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x118>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>());  // row_bcast 15
+    step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>());  // row_bcast 31
+    return v;
+}
+
+// B rows along k, one row of A per workgroup, 4 waves of J columns each, U KB of k at a time.
+template <class E, int J, int U>
+__global__ __launch_bounds__(256) void rows_kernel_dot(GroupArgs p)
+{
+    typedef typename E::T T;
+    typedef decltype(typename E::template Acc<16>()[0] + 0) V;
+    RowTile t;
+    int n0;
+    if (!rows_tile<1>(p, 4 * J, t, n0)) return;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t col0 = (int64_t)n0 + J * w;
+    if (col0 >= p.N) return;  // a whole wave; there is no barrier
+    const int64_t kb = (int64_t)p.K * sizeof(T);  // bytes along k
+    const char *a = static_cast<const char *>(p.A) + (int64_t)t.row0 * p.lda * (int)sizeof(T) + 16 * lane, *b[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        b[j] = static_cast<const char *>(p.B) +
+               (t.g * p.stride_b + min(col0 + j, (int64_t)p.N - 1) * p.ldb) * (int)sizeof(T) + 16 * lane;
+    V acc[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[j] = 0;
+
+    for (int64_t k0 = 0; k0 < kb; k0 += 1024 * U) {
+        u32x4 av[U], bv[J][U];
+        if (k0 + 1024 * U <= kb) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < J; ++j) bv[j][u] = load16_once(b[j] + k0 + 1024 * u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) av[u] = load16(a + k0 + 1024 * u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int valid = (int)(kb - k0) - 1024 * u - 16 * lane;
+#pragma unroll
+                for (int j = 0; j < J; ++j) bv[j][u] = load16_upto<T>(b[j] + k0 + 1024 * u, valid, kb);
+                av[u] = load16_upto<T>(a + k0 + 1024 * u, valid, kb);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < J; ++j) acc[j] = dot16<E>(av[u], bv[j][u], acc[j]);
+    }
+    // lane j < J stores column col0 + j
+    const int64_t n = col0 + lane;
+    const bool live = lane < J && n < p.N;
+    V mine = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int sum = __builtin_amdgcn_readlane(__builtin_bit_cast(int, wave_sum(acc[j])), 63);
+        if (lane == j) mine = __builtin_bit_cast(V, sum);
+    }
+    if (!live) return;
+    float v = (float)mine;
+    if constexpr (E::INT8) v = v * p.sa[t.row0] * p.sb[(int64_t)t.g * p.stride_sb + n];
+    const int64_t at = (int64_t)t.row0 * p.ldc + n;
+    if (p.c_type == 0) static_cast<float *>(p.C)[at] = v;
+    else if (p.c_type == 1) static_cast<__bf16 *>(p.C)[at] = (__bf16)v;
+    else static_cast<_Float16 *>(p.C)[at] = (_Float16)v;
+}
+
 template <int ROWS>
 hipError_t launch_rows(const void *fn, const GroupArgs &a, int cols, int waves, hipStream_t stream)
 {
@@ -313,9 +429,19 @@ int strip_columns(const GroupArgs &a, int rows)
     return a.N >= 8 && wide >= 192 ? 128 : 64;
 }
 
+// J columns of U KB each per wave: 16 KB requested at once where k is that long.
+template <class E>
+hipError_t rows_dot(const GroupArgs &a, hipStream_t stream)
+{
+    if ((int64_t)a.K * (int64_t)sizeof(typename E::T) <= 2048)
+        return launch_rows<1>(reinterpret_cast<const void *>(&rows_kernel_dot<E, 8, 2>), a, 32, 4, stream);
+    return launch_rows<1>(reinterpret_cast<const void *>(&rows_kernel_dot<E, 4, 4>), a, 16, 4, stream);
+}
+
 template <class E>
 hipError_t rows_d(const GroupArgs &a, int rows, hipStream_t stream)
 {
+    if (rows == 1) return rows_dot<E>(a, stream);
     const bool wide = strip_columns(a, rows) == 32;
     if (rows == 16) return wide ? launch_d<E, 1, 2, 4, 2>(a, stream) : launch_d<E, 1, 1, 4, 4>(a, stream);
     if (rows == 32) return wide ? launch_d<E, 2, 2, 4, 2>(a, stream) : launch_d<E, 2, 1, 4, 4>(a, stream);
@@ -341,6 +467,8 @@ hipError_t rows_t(const GroupArgs &a, int rows, hipStream_t stream)
 
 bool group_rows_ok(const GroupArgs &a, int rows)
 {
+    // one row at a time: about one row to a group, and 1 KB of it
+    if (rows == 1) return a.trans_b && a.M <= 1.25 * expected_groups(a) && (int64_t)a.K * (a.elem == GroupElem::I8 ? 1 : 2) >= 1024;
     return a.trans_b || a.N >= (rows == 64 ? 4 : 2);  // a lane's columns of B rows across k
 }
 
@@ -349,6 +477,8 @@ bool group_rows_ok(const GroupArgs &a, int rows)
 // from memory; and rounds of workgroups, each at least its latency and its sums' join.
 double group_rows_time(const GroupArgs &a, int rows)
 {
+    if (rows == 1)
+        return 3.5 + a.M * (double)a.N * a.K * (a.elem == GroupElem::I8 ? 1 : 2) / 5.8e6 * (aligned_words(a) ? 1.0 : 2.2);
     const int es = a.elem == GroupElem::I8 ? 1 : 2, cols = strip_columns(a, rows), rb = rows / 16;
     const double tiles = expected_row_tiles(a, rows) * (double)(((int64_t)a.N + cols - 1) / cols);
     const double bytes = tiles * (rows + cols) * (double)a.K * es * (aligned_words(a) ? 1.0 : 2.2);

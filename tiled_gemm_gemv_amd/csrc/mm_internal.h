@@ -168,7 +168,7 @@ hipError_t group_launch(const GroupArgs &a, hipStream_t stream);
 bool group_tile_ok(const GroupArgs &a, bool large);
 double group_tile_time(const GroupArgs &a, bool large);
 hipError_t group_tile_launch(const GroupArgs &a, bool large, hipStream_t stream);
-// Tiles of `rows` = 16, 32 or 64 rows for few rows per group (mm_group_rows.hip), outside gradient
+// Tiles of `rows` = 1, 16, 32 or 64 rows for few rows per group (mm_group_rows.hip), outside gradient
 // mode, with M, N and K at most 2^31 - 1 - 1024.
 bool group_rows_ok(const GroupArgs &a, int rows);
 double group_rows_time(const GroupArgs &a, int rows);
