@@ -482,7 +482,7 @@ double group_rows_time(const GroupArgs &a, int rows)
     const int es = a.elem == GroupElem::I8 ? 1 : 2, cols = strip_columns(a, rows), rb = rows / 16;
     const double tiles = expected_row_tiles(a, rows) * (double)(((int64_t)a.N + cols - 1) / cols);
     const double bytes = tiles * (rows + cols) * (double)a.K * es * (aligned_words(a) ? 1.0 : 2.2);
-    const double through = bytes / fmin(9e6, 4e4 * tiles), weights = expected_weight_bytes(a) / 5.4e6;
+    const double through = bytes / fmin(a.trans_b ? 9e6 : 5.5e6, 4e4 * tiles), weights = expected_weight_bytes(a) / 5.4e6;
     const double rounds = a.trans_b ? ceil(tiles / 768) * (1.2 + 0.4 * rb) : ceil(tiles / 256) * (2 + 1.25 * rb);
     return 2.5 + fmax(2 + fmax(through, weights), rounds);
 }

@@ -57,14 +57,13 @@ struct GroupTile {
     static constexpr int ES = sizeof(typename E::T), BK = 128 / ES;
     static constexpr int A_HALF = RH * 128, B_HALF = CH * 128;  // bytes of a half panel
     static constexpr int STAGE = 2 * (A_HALF + B_HALF);
-    static constexpr int PITCH = BN + 4;  // epilogue: words per row in LDS (rows 4 apart on other banks)
-    static constexpr int LDS = 2 * STAGE > RH * PITCH * 4 ? 2 * STAGE : RH * PITCH * 4;
     static constexpr int A_LD = A_HALF / 1024 / WAVES, B_LD = B_HALF / 1024 / WAVES;  // 1 KB loads per wave
     // offsets of the half panels in a stage
     static constexpr int A_OFF[2] = {0, A_HALF}, B_OFF[2] = {2 * A_HALF, 2 * A_HALF + B_HALF};
     static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
     static_assert(QM % MB == 0 && QN % MB == 0, "whole blocks");
-    static_assert(LDS <= 160 * 1024, "two stages in LDS");
+    static_assert(2 * STAGE <= 160 * 1024, "two stages in LDS");
+    static_assert(MB == 16 && FN == 2, "the epilogue exchanges two 16 x 16 blocks side by side");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
     static_assert((!AT || RH >= 64) && (!BT || CH >= 64), "T rows of at least the 8 chunks that swz_t permutes");
 };
@@ -128,22 +127,54 @@ __device__ __forceinline__ void bare_barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Elements first .. last - 1 of 8 consecutive ones to C + at.
+// A lane's 4 values of each of two blocks side by side -> 8 consecutive values of its row, as words:
+// a pair of 16-lane rows exchanges blocks (v_permlane16_swap), so that lanes of row g = lane / 16 hold
+// the columns 8 ((g & 1) 2 + (g >> 1)) .. + 7 of the 32. Words: 8 of fp32, 4 of two 16-bit values.
 template <class O>
-__device__ __forceinline__ void store_row(void *C, int64_t at, const float (&v)[8], int first, int last)
+__device__ __forceinline__ void eight_of_row(const float (&v)[2][4], unsigned (&out)[2 * sizeof(O)])
 {
+    constexpr int W = sizeof(O);  // words of 4 values
+    unsigned w[2][W];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (W == 4) {
+                w[j][i] = __builtin_bit_cast(unsigned, v[j][i]);
+            } else {
+                typedef O Pair __attribute__((ext_vector_type(2)));
+                w[j][i] = __builtin_bit_cast(unsigned, Pair{(O)v[j][2 * i], (O)v[j][2 * i + 1]});
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const auto s = __builtin_amdgcn_permlane16_swap(w[0][i], w[1][i], false, false);
+        out[i] = s[0];
+        out[W + i] = s[1];
+    }
+}
+
+// Values first .. last - 1 of the 8 to C + at.
+template <class O>
+__device__ __forceinline__ void store_eight(void *C, int64_t at, const float (&v)[2][4], int first, int last)
+{
+    unsigned w[2 * sizeof(O)];
+    eight_of_row<O>(v, w);  // every lane takes part
     O *c = static_cast<O *>(C) + at;
     if (first == 0 && last == 8) {
-        struct __attribute__((packed)) Eight {
-            O o[8];
+        struct __attribute__((packed)) Words {
+            unsigned w[2 * sizeof(O)];
         } x;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x.o[e] = (O)v[e];
-        *reinterpret_cast<Eight *>(c) = x;
-    } else {
+        for (int i = 0; i < 2 * (int)sizeof(O); ++i) x.w[i] = w[i];
+        *reinterpret_cast<Words *>(c) = x;
+    } else if (first < last) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e >= first && e < last) c[e] = (O)v[e];
+        for (int e = 0; e < 8; ++e) {
+            if (e < first || e >= last) continue;
+            if constexpr (sizeof(O) == 4) c[e] = __builtin_bit_cast(O, w[e]);
+            else c[e] = __builtin_bit_cast(O, (unsigned short)(w[e / 2] >> (16 * (e & 1))));
+        }
     }
 }
 
@@ -276,6 +307,8 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     };
 
     constexpr int HA = LO ? 1 : 2;  // halves of rows
+    // blocks of C transposed (the MFMA's operands exchanged): lane l holds row l % 16 of C and the
+    // columns 4 (l / 16) + r, r < 4
     typename E::template Acc<T::MB> acc[HA][2][T::FM][T::FN];
 #pragma unroll
     for (int qa = 0; qa < HA; ++qa)
@@ -308,7 +341,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                                (reads_a ? T::A_OFF[I == 1] : T::B_OFF[I == 0]);
         auto mfma = [&](int m) {
             const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
-            acc[qa][qb][i][j] = E::template mma<T::MB>(a[qa][ks][i], b[S ^ qb][ks][j], acc[qa][qb][i][j]);
+            acc[qa][qb][i][j] = E::template mma<T::MB>(b[S ^ qb][ks][j], a[qa][ks][i], acc[qa][qb][i][j]);
         };
         auto read = [&](int r) {
             if constexpr (reads_a) read_a(half, r, a[I == 1]);
@@ -351,7 +384,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         const lds_char *stage = (const lds_char *)lds + ((kt + I) & 1) * T::STAGE;
         auto mfma = [&](int m) {
             const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
-            acc[0][I][i][j] = E::template mma<T::MB>(a[S][ks][i], b[I][ks][j], acc[0][I][i][j]);
+            acc[0][I][i][j] = E::template mma<T::MB>(b[I][ks][j], a[S][ks][i], acc[0][I][i][j]);
         };
 #pragma unroll
         for (int m = 0; m < pre; ++m) mfma(m);
@@ -458,63 +491,59 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         }
     }
 
-    // ---- epilogue: through LDS, one half of the rows at a time, so that whole rows are stored 16
-    // bytes (32 of fp32) per lane. Lane l holds column l % 32 and rows 8 (r / 4) + 4 (l / 32) + r % 4
-    // of a block. Storing from there, one element per lane and instruction, took 7 us of a tile.
-    typedef decltype(acc[0][0][0][0][0] + 0) V;
-    typedef V V4 __attribute__((ext_vector_type(4)));
-    V *tile = reinterpret_cast<V *>(lds);
-    constexpr int per_row = T::BN / 8;  // 8 columns per lane
-    static_assert(T::NT % per_row == 0, "a lane keeps its columns");
-    const int c8 = (int)(threadIdx.x % per_row) * 8, n = nb0 + c8;
-    const int first = T::BT && n < n0 ? n0 - n : 0, last = min(8, p.N - n);  // columns to store
-    float sb[8];
+    // ---- epilogue: 16 bytes (32 of fp32) of a row per lane, 16 rows of 32 columns per instruction,
+    // straight from the registers. (Staging the tile in LDS to store whole rows took 4 us of a tile,
+    // single elements from the untransposed blocks 7.)
+    const int lane_row = lane & 15, lane_g = lane >> 4;
+    const int n_lane = nb0 + wn * T::QN + 8 * ((lane_g & 1) * 2 + (lane_g >> 1));
+    float sb[2][2][4];
     if constexpr (E::INT8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sb[e] = e < last ? p.sb[(int64_t)g * p.stride_sb + n + e] : 0.f;
-    }
-#pragma unroll
-    for (int qa = 0; qa < HA; ++qa) {
-        if (mb0 + qa * T::RH >= m_end) break;
-        wait_reads();
-        bare_barrier();  // every wave is done with the stages, or with the half before
 #pragma unroll
         for (int qb = 0; qb < 2; ++qb)
 #pragma unroll
-            for (int i = 0; i < T::FM; ++i)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-                    for (int r = 0; r < T::ACC; ++r)
-                        tile[(wm * T::QM + T::MB * i + 8 * (r >> 2) + 4 * (lane / T::MB) + (r & 3)) * T::PITCH +
-                             qb * T::CH + wn * T::QN + T::MB * j + lane % T::MB] = acc[qa][qb][i][j][r];
-        __syncthreads();
-#pragma unroll 2
-        for (int row = threadIdx.x / per_row; row < T::RH; row += T::NT / per_row) {
-            const int m = mb0 + qa * T::RH + row;
-            if (m >= m_end || (T::AT && m < m0) || last <= first) continue;
-            const V4 lo = *reinterpret_cast<const V4 *>(tile + row * T::PITCH + c8);
-            const V4 hi = *reinterpret_cast<const V4 *>(tile + row * T::PITCH + c8 + 4);
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = (float)(e < 4 ? lo[e] : hi[e - 4]);
-            if constexpr (E::INT8) {
-                const float sa = p.sa[m];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = v[e] * sa * sb[e];
-            }
-            const int64_t at = (GRAD ? (int64_t)g * p.stride_c : 0) + (int64_t)m * p.ldc + n;
-            if (p.c_type == 0) store_row<OutType<0>::T>(p.C, at, v, first, last);
-            else if (p.c_type == 1) store_row<OutType<1>::T>(p.C, at, v, first, last);
-            else store_row<OutType<2>::T>(p.C, at, v, first, last);
-        }
+                for (int r = 0; r < 4; ++r)
+                    sb[qb][j][r] = p.sb[(int64_t)g * p.stride_sb +
+                                        min(nb0 + qb * T::CH + wn * T::QN + 16 * j + 4 * lane_g + r, p.N - 1)];
     }
+    auto store = [&](auto out) {
+        typedef typename decltype(out)::T O;
+#pragma unroll
+        for (int qa = 0; qa < HA; ++qa)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                const int block = mb0 + qa * T::RH + wm * T::QM + 16 * i, m = block + lane_row;
+                if (block >= m_end) break;
+                const bool live = m < m_end && (!T::AT || m >= m0);
+                float sa = 1.f;
+                if constexpr (E::INT8) sa = p.sa[min(m, m_end - 1)];
+                const int64_t row = (GRAD ? (int64_t)g * p.stride_c : 0) + (int64_t)m * p.ldc;
+#pragma unroll
+                for (int qb = 0; qb < 2; ++qb) {
+                    float v[2][4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            v[j][r] = (float)acc[qa][qb][i][j][r];
+                            if constexpr (E::INT8) v[j][r] = v[j][r] * sa * sb[qb][j][r];
+                        }
+                    const int n = n_lane + qb * T::CH;
+                    const int first = T::BT && n < n0 ? n0 - n : 0, last = live ? min(8, p.N - n) : 0;
+                    store_eight<O>(p.C, row + n, v, first, last);
+                }
+            }
+    };
+    if (p.c_type == 0) store(OutType<0>());
+    else if (p.c_type == 1) store(OutType<1>());
+    else store(OutType<2>());
 }
 
 template <class T, bool GRAD>
 __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
 
     const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
     const int64_t bid = linear_block();
@@ -584,7 +613,7 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
 template <class E, bool AT, bool BT>
 struct Tiles {
     using Large = GroupTile<E, AT, BT, 128, 128, 2, 4, 16>;
-    using Mid = GroupTile<E, AT, BT, 64, 64, 2, 4, 16>;
+    using Mid = GroupTile<E, AT, BT, 64, 64, 4, 2, 16>;
     static bool ok(const GroupArgs &a, bool large) { return large ? tile_ok<Large, AT>(a) : tile_ok<Mid, AT>(a); }
     static hipError_t launch(const GroupArgs &a, bool large, hipStream_t stream)
     {
@@ -617,10 +646,10 @@ double group_tile_time(const GroupArgs &a, bool large)
         // the groups' sizes are not known here, so neither is the number of rounds: between whole ones
         const bool known = a.grad || !a.offsets || a.groups == 1;
         const double rounds = known ? ceil(tiles / 256) : fmax(1.0, tiles / 256 + 0.25);
-        time = rounds * (6 + 1.35 * steps);
+        time = rounds * (5.5 + 1.35 * steps);
     } else {
         const double full = floor(tiles / 512), rest = tiles / 512 - full;
-        time = full * (4 + 1.17 * steps) + (rest > 0.5 ? 4 + 1.17 * steps : rest > 0 ? 4 + 0.40 * steps : 0);
+        time = full * (3 + 1.03 * steps) + (rest > 0 ? 2.5 + (0.28 + 0.75 * rest) * steps : 0);
     }
     return 3 + fmax(time, a.grad ? 0.0 : expected_weight_bytes(a) / 4.8e6);
 }
