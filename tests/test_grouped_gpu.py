@@ -250,9 +250,12 @@ def test_most_groups(dev):
 MANY_TILES = [
     ([1500, 1, 0, 700, 1895], 4100, 136),
     ([300, 3000, 256, 129], 4096, 777),
-    ([4096], 4128, 64),
+    ([4096], 4095, 64),
     ([2048, 2048 + 127], 4001, 1024),
     ([3990, 13], 4096, 128),
+    ([4090], 4096, 136),
+    ([3850], 4000, 192),
+    ([3969], 4089, 333),
 ]
 
 
@@ -311,7 +314,8 @@ def test_grad_b_many_tiles(dev, counts, N, K, dtype, out, dist):
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-@pytest.mark.parametrize("M,N,K", [(4096, 4096, 128), (3000, 5003, 777), (4225, 4096, 1024), (8192, 2049, 130)])
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 128), (3000, 5003, 777), (4225, 4096, 1024), (8192, 2049, 130),
+                                   (3850, 4090, 256), (3969, 4000, 300)])
 def test_i8_many_tiles(dev, M, N, K, out):
     A, B = int8(1, (M, K), dev), int8(2, (N, K), dev)
     sa, sb = scales(3, M, dev), scales(4, N, dev)
