@@ -472,19 +472,23 @@ bool group_rows_ok(const GroupArgs &a, int rows)
     return a.trans_b || a.N >= (rows == 64 ? 4 : 2);  // a lane's columns of B rows across k
 }
 
-// Fitted to 90 shapes of all operators: a launch and one workgroup's start 4.5 us; what the
-// workgroups read through L2 at 9 TB/s (40 GB/s each where they are few); the right-hand matrices
-// from memory; and rounds of workgroups, each at least its latency and its sums' join.
+// Fitted to some 200 shapes of all operators: a launch and one workgroup's start 4.5 us; the
+// right-hand matrices from memory at 5.4 TB/s; what is read again, through L2, at 9 TB/s (5 with B's
+// rows across k); 40 GB/s per workgroup where they are few; and rounds of workgroups, each at least
+// its latency and its sums' join.
 double group_rows_time(const GroupArgs &a, int rows)
 {
-    if (rows == 1)
-        return 3.5 + a.M * (double)a.N * a.K * (a.elem == GroupElem::I8 ? 1 : 2) / 5.8e6 * (aligned_words(a) ? 1.0 : 2.2);
-    const int es = a.elem == GroupElem::I8 ? 1 : 2, cols = strip_columns(a, rows), rb = rows / 16;
+    const int es = a.elem == GroupElem::I8 ? 1 : 2;
+    const double unaligned = aligned_words(a) ? 1.0 : 2.2;
+    if (rows == 1) return 3.5 + a.M * (double)a.N * a.K * es / 5.8e6 * unaligned;
+    const int cols = strip_columns(a, rows), rb = rows / 16;
     const double tiles = expected_row_tiles(a, rows) * (double)(((int64_t)a.N + cols - 1) / cols);
-    const double bytes = tiles * (rows + cols) * (double)a.K * es * (aligned_words(a) ? 1.0 : 2.2);
-    const double through = bytes / fmin(a.trans_b ? 9e6 : 5.5e6, 4e4 * tiles), weights = expected_weight_bytes(a) / 5.4e6;
+    const double mean = a.M / expected_groups(a), weights = expected_weight_bytes(a);
+    const double bytes = tiles * (fmin(rows, mean) + cols) * (double)a.K * es;  // rows past a group's end are one row
+    const double again = fmax(0.0, bytes - weights) / (a.trans_b ? 9e6 : 5e6);
+    const double stream = fmax((weights / 5.4e6 + again) * unaligned, bytes / (4e4 * tiles));
     const double rounds = a.trans_b ? ceil(tiles / 768) * (1.2 + 0.4 * rb) : ceil(tiles / 256) * (2 + 1.25 * rb);
-    return 2.5 + fmax(2 + fmax(through, weights), rounds);
+    return 2.5 + fmax(2 + stream, rounds);
 }
 
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream)
