@@ -647,6 +647,57 @@ def test_offsets_past_32_bits(dev):
     check_i8(host64(got), want.T, torch.float32)
 
 
+def test_most_rows(dev):
+    # 2^31 - 1 rows: tile counts and row numbers at the end of 32 bits. One column and one inner
+    # element, so each output is one product, exact in bf16 (8-bit values by powers of two).
+    M = 2 ** 31 - 1
+    a8 = torch.randint(-128, 128, (M, 1), dtype=torch.int8, device=dev)
+    A = a8.to(torch.bfloat16)
+    B = torch.tensor([[[2.0]], [[0.5]], [[-4.0]]], dtype=torch.bfloat16, device=dev)
+    off = torch.tensor([0, M - 33, M - 3, M], device=dev)
+    for trans in (False, True):
+        C = mm.gemm16_grouped(A, B, off, trans_b=trans, out_dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        for g, (lo, hi) in enumerate([(0, M - 33), (M - 33, M - 3), (M - 3, M)]):
+            assert torch.equal(C[lo:hi], A[lo:hi] * B[g]), (trans, g)
+        del C
+    s, one = torch.full((M,), 0.25, device=dev), torch.ones(1, device=dev)
+    C = mm.gemm_i8(a8, torch.ones((1, 1), dtype=torch.int8, device=dev), s, one, out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(C, A * 0.25)
+
+
+SUBNORMAL = [([1, 2, 0, 1], 1100, 600), ([20, 0, 9, 30], 200, 264), ([300, 200], 520, 192), ([40, 3], 31, 40)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts,N,K", SUBNORMAL)
+def test_subnormal_inputs_and_outputs(dev, counts, N, K, trans, dtype):
+    """Subnormal inputs count in full (sums of integers, so exact), and so do fp16 outputs below 2^-14
+    (multiples of 2^-24 with magnitude at most 16 K 2^-24 < 2^-9: rounded, by `check`'s bar)."""
+    E, M = len(counts), sum(counts)
+    off = ranges(counts)
+    offsets = torch.tensor(off, device=dev)
+    Bi = draw(2, (E, N, K) if trans else (E, K, N), "int", dtype, dev)
+    Ai, Gi = draw(1, (M, K), "int", dtype, dev), draw(3, (M, N), "int", dtype, dev)
+    small, large = (2.0 ** -133, 2.0 ** 40) if dtype == "bf16" else (2.0 ** -24, 2.0 ** 6)
+
+    def times(t, factor):  # exact
+        return (t.cpu().double() * factor).to(t.dtype).to(dev)
+
+    want, S = reference(Ai, Bi, off, trans)
+    got = mm.gemm16_grouped(times(Ai, small), times(Bi, large), offsets, trans_b=trans)
+    d = mm.gemm16_grouped_grad_b(times(Ai, large), times(Gi, small), offsets)
+    torch.cuda.synchronize()
+    check(host64(got) / (small * large), want, S, "int", torch.float32)
+    check(host64(d) / (small * large), reference_grad_b(Ai, Gi, off)[0], 0, "int", torch.float32)
+    if dtype == "f16":
+        got = mm.gemm16_grouped(times(Ai, 2.0 ** -14), times(Bi, 2.0 ** -10), offsets, trans_b=trans, out_dtype=torch.float16)
+        torch.cuda.synchronize()
+        check(host64(got), want * 2.0 ** -24, S * 2.0 ** -24, "int", torch.float16)
+
+
 def moe(dev, tokens, experts, top, d, f, seed):
     """Routing of a layer of experts: the sorted token rows, offsets and matrices."""
     g = torch.Generator().manual_seed(seed)

@@ -1,6 +1,7 @@
 // mm_group.h -- shared by the kernels of the grouped products and of the 8-bit integer
-// product (mm_group_any.hip): element types, the launch
-// arguments, the map from a workgroup to a tile of a group, and the epilogue.
+// product (mm_group_tile.hip, mm_group_rows.hip, mm_group_any.hip): element types, loads of any
+// alignment, the map from a workgroup to a tile of a group, and what the host expects of group
+// sizes that it does not know.
 //
 // The sums. Rows lo_g <= i < hi_g of A (lo_g = offsets[g], hi_g = offsets[g + 1]) belong to
 // group g:
@@ -169,12 +170,15 @@ struct RowTiles {
     unsigned run, incl;   // tiles of this lane's groups, and of the lanes up to it
     int R, lo, hi;
 
-    static __device__ __forceinline__ unsigned count(int lo, int hi) { return (unsigned)((hi - lo + BM - 1) / BM); }
+    static __device__ __forceinline__ unsigned count(int lo, int hi)
+    {
+        return ((unsigned)(hi - lo) + (BM - 1)) / BM;  // not as int: up to 2^31 - 1 rows
+    }
 
     __device__ __forceinline__ RowTiles(const GroupArgs &p)
     {
         if (!p.offsets) {
-            total = (unsigned)((p.M + BM - 1) / BM);
+            total = count(0, p.M);
             return;
         }
         const int lane = threadIdx.x & 63;

@@ -22,11 +22,11 @@ __global__ __launch_bounds__(256) void group_any_kernel(GroupArgs p)
     constexpr int BK = kStepBytes / (int)sizeof(T);
     __shared__ __attribute__((aligned(16))) char lds[2 * kTile * kPitch];
 
-    const unsigned tiles_n = (unsigned)((p.N + kTile - 1) / kTile);
+    const unsigned tiles_n = ((unsigned)p.N + kTile - 1) / kTile;
     int g, m0, m_end, k_lo, k_end, n0;
     const int64_t bid = linear_block();
     if constexpr (GRAD) {
-        const unsigned tiles_m = (unsigned)((p.K + kTile - 1) / kTile);
+        const unsigned tiles_m = ((unsigned)p.K + kTile - 1) / kTile;
         const int64_t per = (int64_t)tiles_m * tiles_n;
         if (bid >= per * p.groups) return;
         g = (int)(bid / per);

@@ -1,12 +1,12 @@
 // mm_group_tile.hip -- large tiles of the grouped products and of the 8-bit integer product
 // (see mm_group.h for the sums), with panels moved HBM -> LDS by the LDS DMA.
 //
-// A workgroup computes a BM x BN tile of C in K-steps of 128 bytes of k (64 16-bit or 128 8-bit
-// elements; v_mfma_*_32x32x* takes 32 bytes of k at once, 4 steps of it). The tile is four
-// quadrants of RH x CH (halves lo, hi of its rows and columns); the 4 waves stand in a 2 x 2 grid
-// over each quadrant, so a wave owns a QM x QN part of all four. A K-step is four phases, one
-// quadrant each; every phase multiplies operands that are in registers and reads the half panel
-// that a phase after it needs from LDS, between its MFMAs:
+// A workgroup computes a BM x BN tile of C (256 x 256 or 128 x 128, 8 waves) in K-steps of 128 bytes
+// of k (64 16-bit or 128 8-bit elements; v_mfma_*_16x16x* takes 64 bytes of k at once, 2 steps of it).
+// The tile is four quadrants of RH x CH (halves lo, hi of its rows and columns); the waves stand in a
+// GM x GN grid over each quadrant (2 x 4 and 4 x 2), so a wave owns a QM x QN part of all four. A
+// K-step is four phases, one quadrant each; every phase multiplies operands that are in registers
+// and reads the half panel that a phase after it needs from LDS, between its MFMAs:
 //   phase 0  A lo x B lo    reads B hi
 //   phase 1  A lo x B hi    reads A hi
 //   phase 2  A hi x B hi    reads A lo of the next K-step
@@ -45,15 +45,15 @@ typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-template <class E_, bool AT_, bool BT_, int RH_, int CH_, int GM_, int GN_, int MB_>
+template <class E_, bool AT_, bool BT_, int RH_, int CH_, int GM_, int GN_>
 struct GroupTile {
     typedef E_ E;
     static constexpr bool AT = AT_, BT = BT_;
     static constexpr int RH = RH_, CH = CH_, GM = GM_, GN = GN_, BM = 2 * RH, BN = 2 * CH;
     static constexpr int WAVES = GM * GN, NT = 64 * WAVES;
     static constexpr int QM = RH / GM, QN = CH / GN;
-    static constexpr int MB = MB_, FM = QM / MB, FN = QN / MB;  // MFMA blocks of a wave's part
-    static constexpr int KS = MB == 32 ? 4 : 2, ACC = MB * MB / 64;  // MFMA steps per K-step, values per lane and block
+    static constexpr int MB = 16, FM = QM / MB, FN = QN / MB;  // MFMA blocks of a wave's part
+    static constexpr int KS = 2, ACC = 4;  // MFMA steps per K-step, values per lane and block
     static constexpr int ES = sizeof(typename E::T), BK = 128 / ES;
     static constexpr int A_HALF = RH * 128, B_HALF = CH * 128;  // bytes of a half panel
     static constexpr int STAGE = 2 * (A_HALF + B_HALF);
@@ -63,7 +63,7 @@ struct GroupTile {
     static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
     static_assert(QM % MB == 0 && QN % MB == 0, "whole blocks");
     static_assert(2 * STAGE <= 160 * 1024, "two stages in LDS");
-    static_assert(MB == 16 && FN == 2, "the epilogue exchanges two 16 x 16 blocks side by side");
+    static_assert(FN == 2, "the epilogue exchanges two 16 x 16 blocks side by side");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
     static_assert((!AT || RH >= 64) && (!BT || CH >= 64), "T rows of at least the 8 chunks that swz_t permutes");
 };
@@ -263,7 +263,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         for (int l = 0; l < (i == 0 || i == 3 ? T::A_LD : T::B_LD); ++l) issue_one(kt, i, l);
     };
 
-    // ---- operand reads: 32 bytes of k (MFMA step ks) of the 32-wide block blk of a half panel
+    // ---- operand reads: 64 bytes of k (MFMA step ks) of the 16-wide block blk of a half panel
     int d_off[T::KS];
 #pragma unroll
     for (int ks = 0; ks < T::KS; ++ks)
@@ -271,8 +271,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     const int t_g = lane >> 4, t_j = lane & 15;
     auto t_offset = [&](int blk, auto width) {
         constexpr int W = decltype(width)::value;
-        const int krow = 8 * (T::MB == 32 ? t_g >> 1 : t_g) + (t_j >> 2);
-        const int col = T::MB * blk + (T::MB == 32 ? 16 * (t_g & 1) : 0) + 4 * (t_j & 3);
+        const int krow = 8 * t_g + (t_j >> 2), col = T::MB * blk + 4 * (t_j & 3);
         return krow * 2 * W + 16 * ((col >> 3) ^ swz_t<W>(krow)) + 8 * ((col >> 2) & 1);
     };
     int a_toff[T::FM], b_toff[T::FN];
@@ -612,8 +611,8 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
 // Both tiles have the operands' requirements in common but for the size.
 template <class E, bool AT, bool BT>
 struct Tiles {
-    using Large = GroupTile<E, AT, BT, 128, 128, 2, 4, 16>;
-    using Mid = GroupTile<E, AT, BT, 64, 64, 4, 2, 16>;
+    using Large = GroupTile<E, AT, BT, 128, 128, 2, 4>;
+    using Mid = GroupTile<E, AT, BT, 64, 64, 4, 2>;
     static bool ok(const GroupArgs &a, bool large) { return large ? tile_ok<Large, AT>(a) : tile_ok<Mid, AT>(a); }
     static hipError_t launch(const GroupArgs &a, bool large, hipStream_t stream)
     {
