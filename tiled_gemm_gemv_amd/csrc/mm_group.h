@@ -282,18 +282,5 @@ __device__ __forceinline__ void tile_of_group_block(unsigned bid, unsigned nbloc
     tn = in_g / gm;
 }
 
-// The row tile and tile column of workgroup bid (tiles_n tile columns); false: none. Wave-uniform,
-// every wave of the workgroup calls it.
-template <int BM>
-__device__ __forceinline__ bool group_tile_of_block(const GroupArgs &p, int64_t bid, unsigned tiles_n, RowTile &t,
-                                                    unsigned &tn)
-{
-    const RowTiles<BM> tiles(p);
-    if (bid >= (int64_t)tiles.total * tiles_n) return false;
-    unsigned tm;
-    tile_of_group_block((unsigned)bid, tiles.total * tiles_n, tiles.total, tiles_n, tm, tn);
-    return tn < tiles_n && tiles.find(p, tm, t);  // (tn: where the count overflowed)
-}
-
 }  // namespace
 }  // namespace mm

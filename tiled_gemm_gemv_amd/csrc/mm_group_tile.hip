@@ -63,6 +63,7 @@ struct GroupTile {
     static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
     static_assert(QM % MB == 0 && QN % MB == 0, "whole blocks");
     static_assert(2 * STAGE <= 160 * 1024, "two stages in LDS");
+    static constexpr bool SPLIT = RH == 128;  // one workgroup per CU: the last round's tiles may be split
     static_assert(FN == 2, "the epilogue exchanges two 16 x 16 blocks side by side");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
     static_assert((!AT || RH >= 64) && (!BT || CH >= 64), "T rows of at least the 8 chunks that swz_t permutes");
@@ -539,6 +540,24 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     else store(OutType<2>());
 }
 
+// With one workgroup per CU, where the last round has tiles for at most half of the CUs, each of them
+// is two workgroups' work, its first and second half of rows (bf16 4096 x 6144 x 4096, 1.5 rounds: 165
+// -> 149 us; 2.25 rounds of 32 K-steps 141 -> 129). Workgroup bid of `tiles` tiles: its tile, and the
+// half (-1: the whole tile); false: none.
+constexpr int kCUs = 256;
+template <bool SPLIT>
+__device__ __forceinline__ bool tile_part(int64_t bid, int64_t tiles, unsigned &tile, int &half)
+{
+    const unsigned rest = (unsigned)(tiles % kCUs);
+    half = -1;
+    tile = (unsigned)bid;
+    if (!SPLIT || rest == 0 || rest > kCUs / 2 || bid < tiles - rest) return bid < tiles;
+    const unsigned in = (unsigned)(bid - (tiles - rest));
+    half = (int)(in / rest);
+    tile = (unsigned)(tiles - rest) + in % rest;
+    return half < 2;
+}
+
 template <class T, bool GRAD>
 __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
 {
@@ -546,29 +565,38 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
 
     const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
     const int64_t bid = linear_block();
-    int g, m0, m_end, n0, k_lo, k_end;
+    int g, m0, m_end, n0, k_lo, k_end, half;
+    unsigned tile;
     if constexpr (GRAD) {
         const unsigned tiles_m = (unsigned)((p.K + T::BM - 1) / T::BM);
         const unsigned per = tiles_m * tiles_n;
-        if (bid >= (int64_t)per * p.groups) return;
+        if (!tile_part<T::SPLIT>(bid, (int64_t)per * p.groups, tile, half)) return;
         // each group's tiles over all XCDs: the groups' sums differ in length
         unsigned tm, tn;
-        g = (int)((unsigned)bid / per);
-        tile_of_group_block((unsigned)bid - g * per, per, tiles_m, tiles_n, tm, tn);
+        g = (int)(tile / per);
+        tile_of_group_block(tile - g * per, per, tiles_m, tiles_n, tm, tn);
         m0 = (int)tm * T::BM;
         n0 = (int)tn * T::BN;
         m_end = p.K;
         group_range(p.offsets, g, p.M, k_lo, k_end);
     } else {
         RowTile t;
-        unsigned tn;
-        if (!group_tile_of_block<T::BM>(p, bid, tiles_n, t, tn)) return;
+        unsigned tm, tn;
+        const RowTiles<T::BM> tiles(p);
+        if (!tile_part<T::SPLIT>(bid, (int64_t)tiles.total * tiles_n, tile, half)) return;
+        tile_of_group_block(tile, tiles.total * tiles_n, tiles.total, tiles_n, tm, tn);
+        if (tn >= tiles_n || !tiles.find(p, tm, t)) return;  // (tn: where the count overflowed)
         g = t.g;
         m0 = t.row0;
         m_end = t.hi;
         n0 = (int)tn * T::BN;
         k_lo = 0;
         k_end = p.K;
+    }
+    if (T::SPLIT && half >= 0) {
+        m0 += half * T::RH;
+        if (m0 >= m_end) return;
+        m_end = min(m_end, m0 + T::RH);
     }
     g = __builtin_amdgcn_readfirstlane(g);
     m0 = __builtin_amdgcn_readfirstlane(m0);
@@ -601,7 +629,7 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
     const int64_t tiles_m = GRAD ? ((int64_t)a.K + T::BM - 1) / T::BM * a.groups : max_row_tiles(a, T::BM);
     if (tiles_m > 0x7fffffff / tiles_n) return hipErrorInvalidConfiguration;
     unsigned gx, gy;
-    if (!grid_for(tiles_m * tiles_n, gx, gy)) return hipErrorInvalidConfiguration;
+    if (!grid_for(tiles_m * tiles_n + (T::SPLIT ? kCUs / 2 : 0), gx, gy)) return hipErrorInvalidConfiguration;
     GroupArgs arg = a;
     void *args[] = {&arg};
     return hipLaunchKernel(reinterpret_cast<const void *>(&group_tile_kernel<T, GRAD>), dim3(gx, gy), dim3(T::NT), args,
@@ -644,8 +672,11 @@ double group_tile_time(const GroupArgs &a, bool large)
     if (large) {
         // the groups' sizes are not known here, so neither is the number of rounds: between whole ones
         const bool known = a.grad || !a.offsets || a.groups == 1;
-        const double rounds = known ? ceil(tiles / 256) : fmax(1.0, tiles / 256 + 0.25);
-        time = rounds * (5.5 + 1.35 * steps);
+        const double round = 5.5 + 1.35 * steps, rest = known || tiles <= kCUs / 2 ? fmod(tiles, kCUs) : 0;
+        const double full = known ? floor(tiles / kCUs) : fmax(1.0, tiles / kCUs + 0.1);
+        if (rest == 0) time = full * round;
+        else if (rest > kCUs / 2) time = (full + 1) * round;
+        else time = (tiles <= kCUs / 2 ? 0 : full * round) + 5.5 + (0.45 + 0.3 * rest / (kCUs / 2)) * steps;
     } else {
         const double full = floor(tiles / 512), rest = tiles / 512 - full;
         time = full * (3 + 1.03 * steps) + (rest > 0 ? 2.5 + (0.28 + 0.75 * rest) * steps : 0);
