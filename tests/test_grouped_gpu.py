@@ -313,6 +313,39 @@ def test_grad_b_many_tiles(dev, counts, N, K, dtype, out, dist):
         close(D[g], a @ b, a.abs() @ b.abs(), dist)
 
 
+# Inner sizes below one K-step of the tiles (64 16-bit elements, 128 bytes), from one 16-byte piece on,
+# with NaN beyond the rows' ends and before their starts.
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype,out,dist", [("bf16", "bf16", "normal"), ("f16", "f32", "int")])
+@pytest.mark.parametrize("counts,N,K", [([700, 0, 1, 300], 520, 40), ([3000], 2056, 8), ([129, 600], 1000, 33),
+                                        ([2000, 130], 264, 63), ([255, 1, 257], 1000, 9), ([900], 777, 7)])
+def test_grouped16_short_inner_sizes(dev, counts, N, K, dtype, out, dist, trans):
+    off = ranges(counts)
+    A0, B0 = draw(1, (off[-1], K), dist, dtype, dev), draw(2, (len(counts), N, K) if trans else (len(counts), K, N), dist,
+                                                           dtype, dev)
+    _, A = padded(A0, 3, 5, float("nan"))
+    _, B = padded(B0, 5, 3, float("nan"))
+    want, S = reference(A0, B0, off, trans)
+    for a, b in ((A, B), (A0, B0)):
+        got = mm.gemm16_grouped(a, b, torch.tensor(off, device=dev), trans_b=trans, out_dtype=DT[out])
+        torch.cuda.synchronize()
+        check(host64(got), want, S, dist, DT[out])
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(2000, 4100, 16), (1500, 1000, 17), (700, 777, 100), (3000, 520, 127), (129, 5000, 31),
+                                   (1000, 1000, 15)])
+def test_i8_short_inner_sizes(dev, M, N, K, out):
+    a, b, sa, sb = int8(1, (M, K), dev), int8(2, (N, K), dev), scales(3, M, dev), scales(4, N, dev)
+    want = (host64(a) @ host64(b).T) * host64(sa)[:, None] * host64(sb)
+    _, av = padded(a, 3, 7, 99)
+    _, bv = padded(b, 9, 1, 99)
+    for x, y in ((av, bv), (a, b)):
+        got = mm.gemm_i8(x, y, sa, sb, out_dtype=DT[out])
+        torch.cuda.synchronize()
+        check_i8(host64(got), want, DT[out])
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(4096, 4096, 128), (3000, 5003, 777), (4225, 4096, 1024), (8192, 2049, 130),
                                    (3850, 4090, 256), (3969, 4000, 300)])

@@ -35,7 +35,9 @@
 // than the tile (a multiple of 8 then), clamp to the last chunk. A partial K-step is run first and
 // ends at the last k: it shares its first `ov` k with the next step (or, in a group of fewer rows
 // than a K-step, reads rows before the group), and both panels are zeroed there once they have
-// landed, so that those k add 0 x 0 whatever the memory holds.
+// landed, so that those k add 0 x 0 whatever the memory holds. Outside the gradient a K below one
+// K-step starts at k = 0, and its last, partial chunk ends at the last k instead: the k that it
+// shares with the chunk before are zeroed, and all chunks after it.
 #include "mm_group.h"
 
 namespace mm {
@@ -200,6 +202,8 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     const int ov = (T::BK - len % T::BK) % T::BK;
     const int nk = (len + T::BK - 1) / T::BK;
     const int halves = (LO ? 3 : 4) * nk;
+    // where the partial K-step starts (a saturating subtraction is a vector instruction)
+    const int k_partial = __builtin_amdgcn_readfirstlane(max(k_end - T::BK, 0));
 
     const Elem *A = static_cast<const Elem *>(p.A);
     const Elem *B = static_cast<const Elem *>(p.B) + (GRAD ? 0 : (int64_t)g * p.stride_b);
@@ -211,6 +215,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     // lanes read row 0
     auto offsets_of = [&](int k_first) {
         const int below = k_first < 0 ? -k_first : 0;
+        const int last16 = min(p.K, T::BK) * T::ES - 16;  // the last chunk of a row shorter than a K-step
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -224,7 +229,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                 } else {
                     const int row = 8 * (T::A_LD * w + i) + lane / 8;
                     const int chunk = (lane % 8) ^ swz_d(row);
-                    a_voff[h][i] = (unsigned)((min(h * T::RH + row, m_end - 1 - mb0)) * p.lda * T::ES + 16 * chunk);
+                    a_voff[h][i] = (unsigned)(min(h * T::RH + row, m_end - 1 - mb0) * p.lda * T::ES + min(16 * chunk, last16));
                 }
             }
 #pragma unroll
@@ -234,11 +239,12 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                     const int krow = (64 / CPR) * (T::B_LD * w + i) + lane / CPR;
                     int col = nb0 + h * T::CH + 8 * ((lane % CPR) ^ swz_t<T::CH>(krow));
                     if (p.N < T::BN) col = min(col, p.N - 8);
-                    b_voff[h][i] = (unsigned)((max(krow - below, 0) * p.ldb + (col - nb0)) * 2);
+                    const int k = GRAD ? max(krow - below, 0) : min(krow, p.K - 8 + krow % 8);
+                    b_voff[h][i] = (unsigned)((k * p.ldb + (col - nb0)) * 2);
                 } else {
                     const int row = 8 * (T::B_LD * w + i) + lane / 8;
                     const int chunk = (lane % 8) ^ swz_d(row);
-                    b_voff[h][i] = (unsigned)((min(h * T::CH + row, p.N - 1 - nb0)) * p.ldb * T::ES + 16 * chunk);
+                    b_voff[h][i] = (unsigned)(min(h * T::CH + row, p.N - 1 - nb0) * p.ldb * T::ES + min(16 * chunk, last16));
                 }
             }
         }
@@ -246,8 +252,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     const unsigned lds0 = (unsigned)(uintptr_t)(lds_char *)lds;
     // half panel number 4 kt + i of the reading order (0: A lo, 1: B lo, 2: B hi, 3: A hi)
     auto issue_one = [&](int kt, int i, int l) {  // load l of it
-        int k0 = ov ? (kt == 0 ? k_end - T::BK : k_lo + (kt - 1) * T::BK) : k_lo + kt * T::BK;
-        if (GRAD) k0 = max(k0, 0);
+        const int k0 = ov ? (kt == 0 ? k_partial : k_lo + (kt - 1) * T::BK) : k_lo + kt * T::BK;
         const unsigned st = lds0 + (kt & 1) * T::STAGE;
         if (i == 0 || i == 3) {
             const int h = i == 3;
@@ -429,14 +434,20 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
             else wait_vm<0>();
             bare_barrier();
             lds_char *st = (lds_char *)lds;
+            // leading bytes of chunk c of the K-step to clear (all from 16 on, none below 1)
+            auto clear_of = [&](int c) {
+                if (GRAD || len >= T::BK) return ov * T::ES - 16 * c;
+                return 16 * (c + 1) - len * T::ES;  // what the chunk repeats, or more than all of it
+            };
             auto zero = [&](int off, int rows, bool t) {
                 for (int e = threadIdx.x; e < rows * 8; e += T::NT) {
                     lds_u32x4 *q = (lds_u32x4 *)(st + off + 16 * e);
                     if (t) {  // rows of k, rows / 8 chunks each
-                        if (e / (rows / 8) < ov) *q = u32x4{0u, 0u, 0u, 0u};
+                        const int krow = e / (rows / 8);
+                        if (krow % 8 * T::ES < clear_of(krow / 8)) *q = u32x4{0u, 0u, 0u, 0u};
                     } else {
                         const int row = e / 8, c = (e % 8) ^ swz_d(row);
-                        const int bytes = ov * T::ES - 16 * c;  // of this chunk
+                        const int bytes = clear_of(c);
                         if (bytes >= 16) {
                             *q = u32x4{0u, 0u, 0u, 0u};
                         } else if (bytes > 0) {
@@ -615,7 +626,7 @@ bool tile_ok(const GroupArgs &a)
     constexpr int64_t limit = int64_t(1) << 32;
     constexpr int largest = 0x7fffffff - 1024;  // a tile's row and column numbers fit an int
     if (a.M > largest || a.N > largest || a.K > largest) return false;
-    if (!GRAD && a.K < T::BK) return false;
+    if (!GRAD && a.K * T::ES < 16) return false;  // a chunk
     if (T::AT && a.K < T::BM && a.K % 8 != 0) return false;
     if (T::BT && a.N < T::BN && a.N % 8 != 0) return false;
     const int64_t a_rows = T::AT ? T::BK : T::BM, b_rows = T::BT ? T::BK : T::BN;
