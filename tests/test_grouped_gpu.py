@@ -313,6 +313,26 @@ def test_grad_b_many_tiles(dev, counts, N, K, dtype, out, dist):
         close(D[g], a @ b, a.abs() @ b.abs(), dist)
 
 
+# Matrices of few columns, whole pieces of 8 and others, in each of a tile's quadrants.
+@pytest.mark.parametrize("dtype,out,dist", [("bf16", "bf16", "normal"), ("f16", "f32", "int")])
+@pytest.mark.parametrize("N,K", [(9, 8), (100, 17), (127, 200), (130, 64), (131, 255), (250, 2000), (4000, 241), (8, 3000),
+                                 (199, 2100), (1030, 121), (65, 63)])
+def test_narrow_matrices(dev, N, K, dtype, out, dist):
+    counts = [300, 0, 70, 800]
+    off = ranges(counts)
+    offsets = torch.tensor(off, device=dev)
+    A, B, G = draw(1, (off[-1], K), dist, dtype, dev), draw(2, (len(counts), K, N), dist, dtype, dev), draw(
+        3, (off[-1], N), dist, dtype, dev)
+    C = mm.gemm16_grouped(A, B, offsets, out_dtype=DT[out])
+    buf, D = padded(torch.zeros((len(counts), K, N), dtype=DT[out], device=dev), 3, 5, float("nan"))
+    mm.gemm16_grouped_grad_b(A, G, offsets, out=D)
+    torch.cuda.synchronize()
+    check(host64(C), *reference(A, B, off, False), dist, DT[out])
+    check(host64(D), *reference_grad_b(A, G, off), dist, DT[out])
+    D.fill_(float("nan"))
+    assert torch.isnan(buf).all().item(), "wrote outside the matrices"
+
+
 # Inner sizes below one K-step of the tiles (64 16-bit elements, 128 bytes), from one 16-byte piece on,
 # with NaN beyond the rows' ends and before their starts.
 @pytest.mark.parametrize("trans", [False, True])

@@ -32,7 +32,8 @@
 // one; they feed only elements that are not stored. The columns of a T operand that crosses the
 // matrix' edge start earlier instead (every 16-byte chunk inside its row; elements of C left of
 // the tile's origin belong to the tile before and are not stored again), or, with fewer columns
-// than the tile (a multiple of 8 then), clamp to the last chunk. A partial K-step is run first and
+// than the tile, clamp to the row's last 16 bytes: the last chunk is moved back by what it would have
+// crossed, and so are its elements of C, those that the chunk before holds too not being stored again. A partial K-step is run first and
 // ends at the last k: it shares its first `ov` k with the next step (or, in a group of fewer rows
 // than a K-step, reads rows before the group), and both panels are zeroed there once they have
 // landed, so that those k add 0 x 0 whatever the memory holds. Outside the gradient a K below one
@@ -524,9 +525,14 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         for (int qa = 0; qa < HA; ++qa)
 #pragma unroll
             for (int i = 0; i < T::FM; ++i) {
-                const int block = mb0 + qa * T::RH + wm * T::QM + 16 * i, m = block + lane_row;
+                const int block = mb0 + qa * T::RH + wm * T::QM + 16 * i;
+                int m = block + lane_row;
                 if (block >= m_end) break;
-                const bool live = m < m_end && (!T::AT || m >= m0);
+                bool live = m < m_end && (!T::AT || m >= m0);
+                if (T::AT && m_end < m_need && m >= m_end / 8 * 8) {  // the last chunk, moved back
+                    m -= -m_end & 7;
+                    live = m < m_end && m >= m_end / 8 * 8;
+                }
                 float sa = 1.f;
                 if constexpr (E::INT8) sa = p.sa[min(m, m_end - 1)];
                 const int64_t row = (GRAD ? (int64_t)g * p.stride_c : 0) + (int64_t)m * p.ldc;
@@ -540,8 +546,13 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                             v[j][r] = (float)acc[qa][qb][i][j][r];
                             if constexpr (E::INT8) v[j][r] = v[j][r] * sa * sb[qb][j][r];
                         }
-                    const int n = n_lane + qb * T::CH;
-                    const int first = T::BT && n < n0 ? n0 - n : 0, last = live ? min(8, p.N - n) : 0;
+                    int n = n_lane + qb * T::CH;
+                    int first = T::BT && n < n0 ? n0 - n : 0, last = live ? min(8, p.N - n) : 0;
+                    if (T::BT && p.N < T::BN && n > p.N - 8 && n < p.N) {  // the last chunk, moved back
+                        first = n + 8 - p.N;
+                        last = live ? 8 : 0;
+                        n = p.N - 8;
+                    }
                     store_eight<O>(p.C, row + n, v, first, last);
                 }
             }
@@ -618,8 +629,8 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
     else tile_body<T, GRAD, false>(p, lds, g, m0, m_end, n0, k_lo, k_end);
 }
 
-// The tile takes the shape: K-steps fit (or, in gradient mode, rows of any number), the columns of
-// T operands fill the tile or whole chunks, and lane offsets fit 32 bits.
+// The tile takes the shape: rows of a D operand and of a T operand hold a chunk, and lane offsets fit
+// 32 bits.
 template <class T, bool GRAD>
 bool tile_ok(const GroupArgs &a)
 {
@@ -627,8 +638,7 @@ bool tile_ok(const GroupArgs &a)
     constexpr int largest = 0x7fffffff - 1024;  // a tile's row and column numbers fit an int
     if (a.M > largest || a.N > largest || a.K > largest) return false;
     if (!GRAD && a.K * T::ES < 16) return false;  // a chunk
-    if (T::AT && a.K < T::BM && a.K % 8 != 0) return false;
-    if (T::BT && a.N < T::BN && a.N % 8 != 0) return false;
+    if ((T::AT && a.K < 8) || (T::BT && a.N < 8)) return false;  // a chunk of a T operand's columns
     const int64_t a_rows = T::AT ? T::BK : T::BM, b_rows = T::BT ? T::BK : T::BN;
     return ((a_rows - 1) * a.lda + T::BM) * T::ES + 128 < limit && ((b_rows - 1) * a.ldb + T::BN) * T::ES + 128 < limit;
 }
