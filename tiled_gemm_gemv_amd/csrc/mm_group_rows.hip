@@ -16,6 +16,9 @@
 // A's rows come from L2 (every workgroup of a group reads the same rows); rows past the group's end
 // repeat its last row and are not stored.
 //
+// Bound by the stream of B from memory: 13 experts of 4096 x 2048 bf16 K x N, 16 rows, cold: 38 us,
+// 5.7 TB/s (through 128 x 128 tiles 43).
+//
 // With one row to a group and B's rows along k, whole rows of B (1 KB per wave and load) stream
 // faster than the MFMA's 16 pieces of 64 bytes, and the vector units keep up: each wave takes J
 // columns, multiplies its lanes' 16-byte pieces with A's by dot products (v_dot4_i32_i8, or fp32
@@ -27,7 +30,7 @@
 namespace mm {
 namespace {
 
-// The same for data read once (not kept in the caches).
+// load16 for data read once (not kept in the caches).
 __device__ __forceinline__ u32x4 load16_once(const char *p)
 {
     typedef unsigned int Words __attribute__((ext_vector_type(4), aligned(1)));

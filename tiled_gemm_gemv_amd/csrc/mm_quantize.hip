@@ -18,7 +18,9 @@
 // every product with it is NaN. The largest magnitude is taken over the bits without their sign, as
 // integers: there infinities and NaN are above every number.
 //
-// Bound by memory: each x is read once, kept in registers between the two steps, each q written once.
+// Bound by memory: each x is read once, kept in registers between the two steps, each q written once:
+// bf16 8192 x 14336 66 us, 5.3 TB/s read and written; 8 x 4096 3 us, the launch. Reading the rows twice
+// and single elements took 224 and 15.6 us.
 #include "mm_group.h"
 
 namespace mm {
@@ -196,6 +198,8 @@ hipError_t launch(const QuantArgs &a, hipStream_t stream)
                            dim3(TPR < 256 ? 256 : TPR), args, 0, stream);
 }
 
+// A row's threads: a wave (four rows to a workgroup) up to 128 chunks, else 256 with up to 8 chunks
+// each, else 1024 (up to 64 KB of a row in registers); longer rows are read twice.
 template <class X>
 hipError_t quantize(const QuantArgs &a, hipStream_t stream)
 {
