@@ -134,35 +134,27 @@ hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream)
 // The kernel whose modelled time is least among those that take the shape.
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
 {
-    enum { kAny, kRows1, kRows16, kRows32, kRows64, kMid, kLarge };
-    int best = kAny;
+    enum { kAny, kRows, kTile };
+    int best = kAny, rows = 0;
+    GroupTileKind tile = GroupTileKind::Mid;
     double time = 1e300;
-    auto offer = [&](int kernel, double t) {
-        if (t < time) {
-            best = kernel;
-            time = t;
-        }
-    };
     constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
     if (a.M <= largest && a.N <= largest && a.K <= largest) {
-        if (!a.grad) {
-            if (group_rows_ok(a, 1)) offer(kRows1, group_rows_time(a, 1));
-            if (group_rows_ok(a, 16)) offer(kRows16, group_rows_time(a, 16));
-            if (group_rows_ok(a, 32)) offer(kRows32, group_rows_time(a, 32));
-            if (group_rows_ok(a, 64)) offer(kRows64, group_rows_time(a, 64));
+        if (!a.grad)
+            for (int r : {1, 16, 32, 64}) {
+                if (!group_rows_ok(a, r)) continue;
+                const double t = group_rows_time(a, r);
+                if (t < time) best = kRows, rows = r, time = t;
+            }
+        for (GroupTileKind k : {GroupTileKind::Small4, GroupTileKind::Small, GroupTileKind::Mid, GroupTileKind::Large}) {
+            if (!group_tile_ok(a, k)) continue;
+            const double t = group_tile_time(a, k);
+            if (t < time) best = kTile, tile = k, time = t;
         }
-        if (group_tile_ok(a, false)) offer(kMid, group_tile_time(a, false));
-        if (group_tile_ok(a, true)) offer(kLarge, group_tile_time(a, true));
     }
-    switch (best) {
-    case kRows1: return group_rows_launch(a, 1, stream);
-    case kRows16: return group_rows_launch(a, 16, stream);
-    case kRows32: return group_rows_launch(a, 32, stream);
-    case kRows64: return group_rows_launch(a, 64, stream);
-    case kMid: return group_tile_launch(a, false, stream);
-    case kLarge: return group_tile_launch(a, true, stream);
-    default: return group_any_launch(a, stream);
-    }
+    if (best == kRows) return group_rows_launch(a, rows, stream);
+    if (best == kTile) return group_tile_launch(a, tile, stream);
+    return group_any_launch(a, stream);
 }
 
 }  // namespace mm

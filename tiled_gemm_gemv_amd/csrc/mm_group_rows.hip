@@ -489,7 +489,7 @@ double group_rows_time(const GroupArgs &a, int rows)
     const double mean = a.M / expected_groups(a), weights = expected_weight_bytes(a);
     const double bytes = tiles * (fmin(rows, mean) + cols) * (double)a.K * es;  // rows past a group's end are one row
     const double again = fmax(0.0, bytes - weights) / (a.trans_b ? 9e6 : 5e6);
-    const double stream = fmax((weights / 5.4e6 + again) * unaligned, bytes / (4e4 * tiles));
+    const double stream = fmax(weights / 5.4e6 + again, bytes / (4e4 * tiles)) * unaligned;
     const double rounds = a.trans_b ? ceil(tiles / 768) * (1.2 + 0.4 * rb) : ceil(tiles / 256) * (2 + 1.25 * rb);
     return 2.5 + fmax(2 + stream, rounds);
 }

@@ -1,10 +1,10 @@
 // mm_group_tile.hip -- large tiles of the grouped products and of the 8-bit integer product
 // (see mm_group.h for the sums), with panels moved HBM -> LDS by the LDS DMA.
 //
-// A workgroup computes a BM x BN tile of C (256 x 256 or 128 x 128, 8 waves) in K-steps of 128 bytes
-// of k (64 16-bit or 128 8-bit elements; v_mfma_*_16x16x* takes 64 bytes of k at once, 2 steps of it).
+// A group of waves computes a BM x BN tile of C (256 x 256 or 128 x 128 on 8 waves, 64 x 64 on 2; of
+// the last, 2 or 4 groups in a workgroup share one tile's sums) in K-steps of 128 bytes of k (64 16-bit or 128 8-bit elements; v_mfma_*_16x16x* takes 64 bytes of k at once, 2 steps of it).
 // The tile is four quadrants of RH x CH (halves lo, hi of its rows and columns); the waves stand in a
-// GM x GN grid over each quadrant (2 x 4 and 4 x 2), so a wave owns a QM x QN part of all four. A
+// GM x GN grid over each quadrant (2 x 4, 4 x 2 and 2 x 1), so a wave owns a QM x QN part of all four. A
 // K-step is four phases, one quadrant each; every phase multiplies operands that are in registers
 // and reads the half panel that a phase after it needs from LDS, between its MFMAs:
 //   phase 0  A lo x B lo    reads B hi
@@ -43,7 +43,11 @@
 // Bound by the matrix cores at the clock the power limit leaves (1.64-1.7 GHz; MFMAs busy 67-75% of it,
 // no LDS bank conflicts). 256 x 256, one workgroup per CU: 1.35 us per K-step and round of 256 tiles;
 // bf16 8192 x 14336 x 4096 682 us (1411 TFLOP/s), i8 362-386 us (2.5-2.65 POP/s). 128 x 128, two per
-// CU, for fewer tiles: i8 1000 x 1531 x 777 12 us. Against that, same shapes: 32 x 32 MFMAs instead of
+// CU, for fewer tiles: i8 1000 x 1531 x 777 12 us. With fewer tiles than CUs a tile's panels bound it,
+// which one CU takes from L2 at about 100 GB/s: 64 x 64 tiles spread them over four times the CUs, and
+// the groups of a workgroup keep enough loads on their way (bf16 128 x 4096 x 4096 27.1 us in 128 x 128
+// tiles, 16.6 in 64 x 64; 256 x 2048 x 4096 26.9 and 14.8; two groups to a 128 x 128 tile no faster
+// than one). Against that, same shapes: 32 x 32 MFMAs instead of
 // 16 x 16 8-15% slower (they pass twice the accumulator bytes per product); 4 waves of 128 x 128 the
 // same with 32 x 32 MFMAs; a phase's reads in front of its MFMAs 5-8% slower; workgroups that stay
 // and load their next tile during the stores -1.7% to +8.6%.
@@ -77,7 +81,6 @@ struct GroupTile {
     static constexpr bool SPLIT = RH == 128;  // one workgroup per CU: the last round's tiles may be split
     static_assert(FN == 2, "the epilogue exchanges two 16 x 16 blocks side by side");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
-    static_assert((!AT || RH >= 64) && (!BT || CH >= 64), "T rows of at least the 8 chunks that swz_t permutes");
 };
 
 // D rows of 128 bytes: the 8 slots of one chunk over any 8 (16 on 64 banks) rows are distinct.
@@ -85,12 +88,14 @@ __device__ __forceinline__ int swz_d(int row) { return ((row >> 1) & 7) ^ ((row 
 
 // T rows of W columns (2 W bytes): a transposed read touches 64 bytes of four consecutive rows (and
 // of four more 8 rows on); XOR-ing the chunk index spreads them over the bank quarters. Rows of 128
-// bytes (W = 64) span two quarters, chosen by the row's parity already.
+// bytes (W = 64) span two quarters, chosen by the row's parity already; rows of 64 bytes (W = 32) all
+// four.
 template <int W>
 __device__ __forceinline__ int swz_t(int krow)
 {
-    static_assert(W == 64 || W == 128, "rows of 8 or 16 chunks: the permuted index stays inside the row");
-    if constexpr (W == 64) return ((krow >> 1) & 1) * 4 ^ ((krow >> 3) & 1) * 2;
+    static_assert(W == 32 || W == 64 || W == 128, "rows of 4, 8 or 16 chunks: the permuted index stays inside the row");
+    if constexpr (W == 32) return ((krow >> 3) & 1) * 2;
+    else if constexpr (W == 64) return ((krow >> 1) & 1) * 4 ^ ((krow >> 3) & 1) * 2;
     else return (krow & 3) * 4 ^ ((krow >> 3) & 1) * 2;
 }
 
@@ -191,8 +196,9 @@ __device__ __forceinline__ void store_eight(void *C, int64_t at, const float (&v
 }
 
 // Rows m0 .. m_end of C (of D_g), columns n0 .. N, the sum over k_lo .. k_end. LO: the rows end in
-// the tile's first half.
-template <class T, bool GRAD, bool LO>
+// the tile's first half. The workgroup holds KG groups of T::WAVES waves, each with a KG-th of the
+// K-steps and LDS of its own; the first adds the sums in order and stores them.
+template <class T, bool GRAD, bool LO, int KG>
 __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, int m0, int m_end, int n0, int k_lo,
                                           int k_end)
 {
@@ -204,9 +210,25 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     const int nb0 = T::BT ? (p.N >= T::BN ? min(n0, p.N - T::BN) : 0) : n0;
 
     const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = KG == 1 ? 0 : w_all / T::WAVES, w = w_all - kg * T::WAVES;
     const int wm = w / T::GN, wn = w % T::GN;
 
+    // barriers that a group of waves passes for a sum of `len` elements, below
+    auto barriers = [](int len) {
+        return len == 0 ? 0 : (LO ? 2 : 4) * ((len + T::BK - 1) / T::BK) + 2 + (len % T::BK != 0);
+    };
+    int idle = 0;  // barriers that this group passes less than the other
+    if constexpr (KG > 1) {
+        const int steps = (k_end - k_lo + T::BK - 1) / T::BK;
+        auto first_step = [&](int group) { return (group * steps) / KG; };  // so the last group has the most
+        idle = barriers(k_end - k_lo - first_step(KG - 1) * T::BK);
+        const int lo = k_lo + first_step(kg) * T::BK;
+        if (kg < KG - 1) k_end = k_lo + first_step(kg + 1) * T::BK;
+        k_lo = lo;
+        idle -= barriers(k_end - k_lo);
+        lds += kg * 2 * T::STAGE;
+    }
     const int len = k_end - k_lo;
     const int ov = (T::BK - len % T::BK) % T::BK;
     const int nk = (len + T::BK - 1) / T::BK;
@@ -445,11 +467,11 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
             lds_char *st = (lds_char *)lds;
             // leading bytes of chunk c of the K-step to clear (all from 16 on, none below 1)
             auto clear_of = [&](int c) {
-                if (GRAD || len >= T::BK) return ov * T::ES - 16 * c;
-                return 16 * (c + 1) - len * T::ES;  // what the chunk repeats, or more than all of it
+                if (GRAD || k_end >= T::BK) return ov * T::ES - 16 * c;
+                return 16 * (c + 1) - k_end * T::ES;  // what the chunk repeats, or more than all of it
             };
             auto zero = [&](int off, int rows, bool t) {
-                for (int e = threadIdx.x; e < rows * 8; e += T::NT) {
+                for (int e = 64 * w + lane; e < rows * 8; e += 64 * T::WAVES) {
                     lds_u32x4 *q = (lds_u32x4 *)(st + off + 16 * e);
                     if (t) {  // rows of k, rows / 8 chunks each
                         const int krow = e / (rows / 8);
@@ -509,6 +531,36 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                 if (kt + 1 < nk) k_step(kt + 1, S1(), std::false_type());
             }
         }
+    }
+
+    if constexpr (KG > 1) {
+        for (int i = 0; i < idle; ++i) bare_barrier();
+        // once every wave has read what it needs, the other groups' sums go through their panels' LDS
+        typedef __attribute__((address_space(3))) typename E::template Acc<T::MB> lds_acc;
+        static_assert(T::BM * T::BN * 4 <= 2 * T::STAGE, "a group's sums fit its LDS");
+        bare_barrier();
+        auto each = [&](const char *group, auto &&f) {
+            lds_acc *part = (lds_acc *)(lds_char *)group + 64 * w + lane;
+            int at = 0;
+#pragma unroll
+            for (int qa = 0; qa < HA; ++qa)
+#pragma unroll
+                for (int qb = 0; qb < 2; ++qb)
+#pragma unroll
+                    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < T::FN; ++j) f(acc[qa][qb][i][j], part + 64 * T::WAVES * at++);
+        };
+        if (kg > 0) {
+            each(lds, [](auto &mine, lds_acc *at) { *at = mine; });
+            wait_reads();
+            bare_barrier();
+            return;
+        }
+        bare_barrier();
+#pragma unroll
+        for (int group = 1; group < KG; ++group)
+            each(lds + group * 2 * T::STAGE, [](auto &mine, lds_acc *at) { mine += *at; });
     }
 
     // ---- epilogue: 16 bytes (32 of fp32) of a row per lane, 16 rows of 32 columns per instruction,
@@ -588,10 +640,10 @@ __device__ __forceinline__ bool tile_part(int64_t bid, int64_t tiles, unsigned &
     return half < 2;
 }
 
-template <class T, bool GRAD>
-__global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
+template <class T, bool GRAD, int KG>
+__global__ __launch_bounds__(T::NT * KG) void group_tile_kernel(GroupArgs p)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
+    __shared__ __attribute__((aligned(1024))) char lds[KG * 2 * T::STAGE];
 
     const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
     const int64_t bid = linear_block();
@@ -633,8 +685,8 @@ __global__ __launch_bounds__(T::NT) void group_tile_kernel(GroupArgs p)
     m_end = __builtin_amdgcn_readfirstlane(m_end);
     k_lo = __builtin_amdgcn_readfirstlane(k_lo);
     k_end = __builtin_amdgcn_readfirstlane(k_end);
-    if (m_end - m0 <= T::RH) tile_body<T, GRAD, true>(p, lds, g, m0, m_end, n0, k_lo, k_end);
-    else tile_body<T, GRAD, false>(p, lds, g, m0, m_end, n0, k_lo, k_end);
+    if (m_end - m0 <= T::RH) tile_body<T, GRAD, true, KG>(p, lds, g, m0, m_end, n0, k_lo, k_end);
+    else tile_body<T, GRAD, false, KG>(p, lds, g, m0, m_end, n0, k_lo, k_end);
 }
 
 // The tile takes the shape: rows of a D operand and of a T operand hold a chunk, and lane offsets fit
@@ -651,7 +703,7 @@ bool tile_ok(const GroupArgs &a)
     return ((a_rows - 1) * a.lda + T::BM) * T::ES + 128 < limit && ((b_rows - 1) * a.ldb + T::BN) * T::ES + 128 < limit;
 }
 
-template <class T, bool GRAD>
+template <class T, bool GRAD, int KG>
 hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
 {
     const int64_t tiles_n = ((int64_t)a.N + T::BN - 1) / T::BN;
@@ -661,19 +713,28 @@ hipError_t launch_tile(const GroupArgs &a, hipStream_t stream)
     if (!grid_for(tiles_m * tiles_n + (T::SPLIT ? kCUs / 2 : 0), gx, gy)) return hipErrorInvalidConfiguration;
     GroupArgs arg = a;
     void *args[] = {&arg};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&group_tile_kernel<T, GRAD>), dim3(gx, gy), dim3(T::NT), args,
+    return hipLaunchKernel(reinterpret_cast<const void *>(&group_tile_kernel<T, GRAD, KG>), dim3(gx, gy), dim3(T::NT * KG), args,
                            0, stream);
 }
 
-// Both tiles have the operands' requirements in common but for the size.
+// The tiles of an element type and layouts.
 template <class E, bool AT, bool BT>
 struct Tiles {
     using Large = GroupTile<E, AT, BT, 128, 128, 2, 4>;
     using Mid = GroupTile<E, AT, BT, 64, 64, 4, 2>;
-    static bool ok(const GroupArgs &a, bool large) { return large ? tile_ok<Large, AT>(a) : tile_ok<Mid, AT>(a); }
-    static hipError_t launch(const GroupArgs &a, bool large, hipStream_t stream)
+    using Small = GroupTile<E, AT, BT, 32, 32, 2, 1>;
+    static bool ok(const GroupArgs &a, GroupTileKind kind)
     {
-        return large ? launch_tile<Large, AT>(a, stream) : launch_tile<Mid, AT>(a, stream);
+        return kind == GroupTileKind::Large ? tile_ok<Large, AT>(a)
+               : kind == GroupTileKind::Mid ? tile_ok<Mid, AT>(a)
+                                            : tile_ok<Small, AT>(a);
+    }
+    static hipError_t launch(const GroupArgs &a, GroupTileKind kind, hipStream_t stream)
+    {
+        return kind == GroupTileKind::Large ? launch_tile<Large, AT, 1>(a, stream)
+               : kind == GroupTileKind::Mid  ? launch_tile<Mid, AT, 1>(a, stream)
+               : kind == GroupTileKind::Small ? launch_tile<Small, AT, 2>(a, stream)
+                                              : launch_tile<Small, AT, 4>(a, stream);
     }
 };
 
@@ -690,42 +751,56 @@ auto with_tiles(const GroupArgs &a, F &&f)
 
 }  // namespace
 
-// Fitted to some 300 shapes of all operators (the chosen kernel's time over the best one's: 1.03-1.05
+// Fitted to some 300 shapes of all operators (the chosen kernel's time over the best one's: 1.03-1.04
 // in the mean). 256 x 256: 5.5 us per round for a tile's first loads and its stores, 1.35 per K-step of
-// all CUs, 0.45-0.75 per K-step of a last round in halves. 128 x 128: 0.28 us of latency per K-step and
-// 0.75 of throughput at 512 tiles. So few tiles go to 128 x 128 (bf16 1024 x 4096 x 4096: 35 us, 43 in
-// 256 x 256), many to 256 x 256 (4608 x 8192 x 2048: 129 us, 145 in 128 x 128).
-double group_tile_time(const GroupArgs &a, bool large)
+// all CUs, 0.45-0.75 per K-step of a last round in halves. 128 x 128: 0.28 us per K-step, and 0.75 times
+// the share of 512 tiles. 64 x 64 in four parts: 0.13-0.19 us per K-step and round of 256 tiles, in two
+// 0.19-0.36 for up to 512, more with operands across k (64-byte rows). So many tiles go to 256 x 256
+// (bf16 4608 x 8192 x 2048: 129 us, 145 in 128 x 128), fewer to 128 x 128 (1024 x 4096 x 4096: 36 us, 41
+// in 256 x 256), few to 64 x 64 (256 x 4096 x 4096: 18 us, 27 in 128 x 128). Rows that start off 4-byte
+// boundaries weigh the more the less a tile reuses them.
+double group_tile_time(const GroupArgs &a, GroupTileKind kind)
 {
+    const bool large = kind == GroupTileKind::Large, small = kind <= GroupTileKind::Small;
     const double sum = a.grad ? (double)a.M / a.groups : (double)a.K;  // length of a tile's sums
-    const double steps = ceil(sum * (a.elem == GroupElem::I8 ? 1 : 2) / 128) * (aligned_words(a) ? 1.0 : 1.5);
-    const int t = large ? 256 : 128;
+    const double steps = ceil(sum * (a.elem == GroupElem::I8 ? 1 : 2) / 128) * (aligned_words(a) ? 1.0 : large ? 1.25 : small && a.trans_b ? 2.3 : 1.5);
+    const int t = large ? 256 : kind == GroupTileKind::Mid ? 128 : 64;
     const double tiles = (double)(((int64_t)a.N + t - 1) / t) *
                          (a.grad ? (double)(((int64_t)a.K + t - 1) / t) * a.groups : expected_row_tiles(a, t));
+    // the groups' sizes are not known here, so neither is the number of rounds: between whole ones
+    const bool known = a.grad || !a.offsets || a.groups == 1;
     double time;
     if (large) {
-        // the groups' sizes are not known here, so neither is the number of rounds: between whole ones
-        const bool known = a.grad || !a.offsets || a.groups == 1;
         const double round = 5.5 + 1.35 * steps, rest = known || tiles <= kCUs / 2 ? fmod(tiles, kCUs) : 0;
         const double full = known ? floor(tiles / kCUs) : fmax(1.0, tiles / kCUs + 0.1);
         if (rest == 0) time = full * round;
         else if (rest > kCUs / 2) time = (full + 1) * round;
         else time = (tiles <= kCUs / 2 ? 0 : full * round) + 5.5 + (0.45 + 0.3 * rest / (kCUs / 2)) * steps;
+    } else if (kind == GroupTileKind::Small4) {
+        const double rounds = known ? ceil(tiles / kCUs) : fmax(1.0, tiles / kCUs + 0.1);
+        const double step = (0.13 + 0.06 * fmin(1.0, tiles / kCUs)) * (a.trans_b ? 1 : 1.35);
+        time = rounds * (3 + step * steps);
+    } else if (kind == GroupTileKind::Small) {
+        const double full = floor(tiles / 512), rest = tiles / 512 - full, across = a.trans_b ? 1 : a.grad ? 1.35 : 1.15;
+        time = full * (3 + 0.36 * across * steps);
+        if (rest > 0) time += 2.7 + (0.185 + 0.35 * fmax(0.0, rest - 0.5)) * across * steps;
     } else {
         const double full = floor(tiles / 512), rest = tiles / 512 - full;
         time = full * (3 + 1.03 * steps) + (rest > 0 ? 2.5 + (0.28 + 0.75 * rest) * steps : 0);
     }
-    return 3 + fmax(time, a.grad ? 0.0 : expected_weight_bytes(a) / 4.8e6);
+    // the weights' stream overlaps the products, not wholly
+    const double stream = a.grad ? 0.0 : expected_weight_bytes(a) / 4.8e6;
+    return 3 + fmax(time, stream) + 0.1 * fmin(time, stream);
 }
 
-bool group_tile_ok(const GroupArgs &a, bool large)
+bool group_tile_ok(const GroupArgs &a, GroupTileKind kind)
 {
-    return with_tiles(a, [&](auto t) { return decltype(t)::ok(a, large); });
+    return with_tiles(a, [&](auto t) { return decltype(t)::ok(a, kind); });
 }
 
-hipError_t group_tile_launch(const GroupArgs &a, bool large, hipStream_t stream)
+hipError_t group_tile_launch(const GroupArgs &a, GroupTileKind kind, hipStream_t stream)
 {
-    return with_tiles(a, [&](auto t) { return decltype(t)::launch(a, large, stream); });
+    return with_tiles(a, [&](auto t) { return decltype(t)::launch(a, kind, stream); });
 }
 
 }  // namespace mm

@@ -163,11 +163,13 @@ struct GroupArgs {
 };
 // The kernel for the shape; M, N, groups >= 1 (gradient mode: K, N, groups >= 1).
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream);
-// Tiles of 256 x 256 (large) or 128 x 128 with panels loaded straight into LDS (mm_group_tile.hip):
+// Tiles of 256 x 256 (Large), 128 x 128 (Mid) or 64 x 64 with panels loaded straight into LDS
+// (mm_group_tile.hip), the last with each sum in two (Small) or four parts (Small4) in one workgroup:
 // whether they take the shape, their modelled time in microseconds, and the launch.
-bool group_tile_ok(const GroupArgs &a, bool large);
-double group_tile_time(const GroupArgs &a, bool large);
-hipError_t group_tile_launch(const GroupArgs &a, bool large, hipStream_t stream);
+enum class GroupTileKind { Small4, Small, Mid, Large };
+bool group_tile_ok(const GroupArgs &a, GroupTileKind kind);
+double group_tile_time(const GroupArgs &a, GroupTileKind kind);
+hipError_t group_tile_launch(const GroupArgs &a, GroupTileKind kind, hipStream_t stream);
 // Tiles of `rows` = 1, 16, 32 or 64 rows for few rows per group (mm_group_rows.hip), outside gradient
 // mode, with M, N and K at most 2^31 - 1 - 1024.
 bool group_rows_ok(const GroupArgs &a, int rows);
