@@ -313,6 +313,62 @@ def test_grad_b_many_tiles(dev, counts, N, K, dtype, out, dist):
         close(D[g], a @ b, a.abs() @ b.abs(), dist)
 
 
+# Sizes of about one tile of 128 x 128 for each CU, and of fewer tiles of 64 x 64 than CUs with sums of
+# few and many K-steps (parts of a sum in one workgroup that are empty, whole and partial).
+FEW_TILES = [
+    ([1500], 2000, 300), ([700, 0, 400], 4000, 136), ([2000, 0, 100], 2100, 333), ([1048, 1], 2048, 512),
+    ([100, 28], 4096, 520), ([200], 777, 1531), ([60, 0, 131], 1000, 2049), ([256], 2048, 4096), ([70], 520, 100),
+    ([33, 64], 1030, 190), ([300], 1024, 8192), ([65, 1, 190], 600, 257),
+]
+
+
+@pytest.mark.parametrize("dtype,out,dist", [("bf16", "bf16", "normal"), ("f16", "f32", "int")])
+@pytest.mark.parametrize("case", range(len(FEW_TILES)))
+def test_few_tiles(dev, case, dtype, out, dist):
+    counts, N, K = FEW_TILES[case]
+    off = ranges(counts)
+    offsets = torch.tensor(off, device=dev)
+    gen = torch.Generator(device=dev).manual_seed(100 + case)
+
+    def make(*shape):
+        if dist == "int":
+            return torch.randint(-2, 3, shape, generator=gen, device=dev).to(DT[dtype])
+        return torch.randn(shape, generator=gen, device=dev).to(DT[dtype])
+
+    A, B, G = make(off[-1], K), make(len(counts), K, N), make(off[-1], N)
+    Bt = B.transpose(1, 2).contiguous()
+    C = mm.gemm16_grouped(A, B, offsets, out_dtype=DT[out])
+    Ct = mm.gemm16_grouped(A, Bt, offsets, trans_b=True, out_dtype=DT[out])
+    D = mm.gemm16_grouped_grad_b(A, G, offsets, out_dtype=DT[out])
+    # the same numbers with the sum over K in the gradient: long sums for few tiles
+    turned = mm.gemm16_grouped_grad_b(A.t().contiguous(), B[0], torch.tensor([0, K], device=dev), out_dtype=DT[out])
+    a, w = A.double(), B[0].double()
+    close(turned[0], a @ w, a.abs() @ w.abs(), dist)
+    for g in range(len(counts)):
+        a, w, d = A[off[g]:off[g + 1]].double(), B[g].double(), G[off[g]:off[g + 1]].double()
+        if counts[g]:
+            close(C[off[g]:off[g + 1]], a @ w, a.abs() @ w.abs(), dist)
+            close(Ct[off[g]:off[g + 1]], a @ w, a.abs() @ w.abs(), dist)
+        at = a.t().contiguous()
+        close(D[g], at @ d, at.abs() @ d.abs(), dist)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("case", range(len(FEW_TILES)))
+def test_i8_few_tiles(dev, case, out):
+    counts, N, K = FEW_TILES[case]
+    M, off = sum(counts), ranges(counts)
+    a, b, sa, sb = int8(1, (M, K), dev), int8(2, (len(counts), N, K), dev), scales(3, M, dev), scales(4, (len(counts), N), dev)
+    got = mm.gemm_i8_grouped(a, b, torch.tensor(off, device=dev), sa, sb, out_dtype=DT[out])
+    one = mm.gemm_i8(a, b[0], sa, sb[0], out_dtype=DT[out])
+    torch.cuda.synchronize()
+    ha, hb, hsa, hsb = host64(a), host64(b), host64(sa), host64(sb)
+    check_i8(host64(one), (ha @ hb[0].T) * hsa[:, None] * hsb[0], DT[out])
+    for g in range(len(counts)):
+        lo, hi = off[g], off[g + 1]
+        check_i8(host64(got)[lo:hi], (ha[lo:hi] @ hb[g].T) * hsa[lo:hi, None] * hsb[g], DT[out])
+
+
 # Matrices of few columns, whole pieces of 8 and others, in each of a tile's quadrants.
 @pytest.mark.parametrize("dtype,out,dist", [("bf16", "bf16", "normal"), ("f16", "f32", "int")])
 @pytest.mark.parametrize("N,K", [(9, 8), (100, 17), (127, 200), (130, 64), (131, 255), (250, 2000), (4000, 241), (8, 3000),
