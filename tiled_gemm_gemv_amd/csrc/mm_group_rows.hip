@@ -477,7 +477,7 @@ bool group_rows_ok(const GroupArgs &a, int rows)
 
 // Fitted to some 200 shapes of all operators: a launch and one workgroup's start 4.5 us; the
 // right-hand matrices from memory at 5.4 TB/s; what is read again, through L2, at 9 TB/s (5 with B's
-// rows across k); 40 GB/s per workgroup where they are few; and rounds of workgroups, each at least
+// rows across k); 40 (24) GB/s per workgroup where they are few; and rounds of workgroups, each at least
 // its latency and its sums' join.
 double group_rows_time(const GroupArgs &a, int rows)
 {
@@ -489,7 +489,8 @@ double group_rows_time(const GroupArgs &a, int rows)
     const double mean = a.M / expected_groups(a), weights = expected_weight_bytes(a);
     const double bytes = tiles * (fmin(rows, mean) + cols) * (double)a.K * es;  // rows past a group's end are one row
     const double again = fmax(0.0, bytes - weights) / (a.trans_b ? 9e6 : 5e6);
-    const double stream = fmax(weights / 5.4e6 + again, bytes / (4e4 * tiles)) * unaligned;
+    const double rate = !a.trans_b && cols == 32 ? 2.4e4 : 4e4;  // of one workgroup; 64-byte rows of B: less
+    const double stream = fmax(weights / 5.4e6 + again, bytes / (rate * tiles)) * unaligned;
     const double rounds = a.trans_b ? ceil(tiles / 768) * (1.2 + 0.4 * rb) : ceil(tiles / 256) * (2 + 1.25 * rb);
     return 2.5 + fmax(2 + stream, rounds);
 }

@@ -778,7 +778,8 @@ double group_tile_time(const GroupArgs &a, GroupTileKind kind)
         else time = (tiles <= kCUs / 2 ? 0 : full * round) + 5.5 + (0.45 + 0.3 * rest / (kCUs / 2)) * steps;
     } else if (kind == GroupTileKind::Small4) {
         const double rounds = known ? ceil(tiles / kCUs) : fmax(1.0, tiles / kCUs + 0.1);
-        const double step = (0.13 + 0.06 * fmin(1.0, tiles / kCUs)) * (a.trans_b ? 1 : 1.35);
+        const bool halves = !a.grad && a.M <= 32 * expected_groups(a);  // tiles without a second half of rows
+        const double step = (0.13 + 0.06 * fmin(1.0, tiles / kCUs)) * (a.trans_b ? 1 : 1.35) * (halves ? 0.75 : 1);
         time = rounds * (3 + step * steps);
     } else if (kind == GroupTileKind::Small) {
         const double full = floor(tiles / 512), rest = tiles / 512 - full, across = a.trans_b ? 1 : a.grad ? 1.35 : 1.15;
