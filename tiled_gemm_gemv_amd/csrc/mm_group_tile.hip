@@ -1,18 +1,19 @@
 // mm_group_tile.hip -- large tiles of the grouped products and of the 8-bit integer product
 // (see mm_group.h for the sums), with panels moved HBM -> LDS by the LDS DMA.
 //
-// A group of waves computes a BM x BN tile of C (256 x 256 or 128 x 128 on 8 waves, 64 x 64 on 2; of
-// the last, 2 or 4 groups in a workgroup share one tile's sums) in K-steps of 128 bytes of k (64 16-bit or 128 8-bit elements; v_mfma_*_16x16x* takes 64 bytes of k at once, 2 steps of it).
-// The tile is four quadrants of RH x CH (halves lo, hi of its rows and columns); the waves stand in a
-// GM x GN grid over each quadrant (2 x 4, 4 x 2 and 2 x 1), so a wave owns a QM x QN part of all four. A
-// K-step is four phases, one quadrant each; every phase multiplies operands that are in registers
-// and reads the half panel that a phase after it needs from LDS, between its MFMAs:
+// A group of waves computes a BM x BN tile of C (256 x 256 or 128 x 128 on 8 waves, 64 x 64 on 2;
+// of the last, 2 or 4 groups in a workgroup share one tile's sums) in K-steps of 128 bytes of k (64
+// 16-bit or 128 8-bit elements; v_mfma_*_16x16x* takes 64 bytes of k at once, 2 steps of it). The
+// tile is four quadrants of RH x CH (halves lo, hi of its rows and columns); the waves stand in a
+// GM x GN grid over each quadrant (2 x 4, 4 x 2 and 2 x 1), so a wave owns a QM x QN part of all
+// four. A K-step is four phases, one quadrant each; every phase multiplies operands that are in
+// registers and reads the half panel that a phase after it needs from LDS, between its MFMAs:
 //   phase 0  A lo x B lo    reads B hi
 //   phase 1  A lo x B hi    reads A hi
 //   phase 2  A hi x B hi    reads A lo of the next K-step
 //   phase 3  A hi x B lo    reads B lo of the next K-step, into the registers of B hi
-// so each half panel is read from LDS once per K-step and wave, and the reads are spread evenly.
-// A tile whose second half of rows holds none of C (the last of a group, often) goes without A hi:
+// so each half panel is read from LDS once per K-step and wave, and the reads are spread evenly. A
+// tile whose second half of rows holds none of C (the last of a group, often) goes without A hi:
 //   phase 0  A lo x B lo    reads B hi
 //   phase 1  A lo x B hi    reads A lo and B lo of the next K-step, A lo into the registers of A hi
 //
@@ -30,15 +31,16 @@
 //
 // Edges. Rows of A past the group's end, and rows of a D operand B past N, are clamped to the last
 // one; they feed only elements that are not stored. The columns of a T operand that crosses the
-// matrix' edge start earlier instead (every 16-byte chunk inside its row; elements of C left of
-// the tile's origin belong to the tile before and are not stored again), or, with fewer columns
-// than the tile, clamp to the row's last 16 bytes: the last chunk is moved back by what it would have
-// crossed, and so are its elements of C, those that the chunk before holds too not being stored again. A partial K-step is run first and
-// ends at the last k: it shares its first `ov` k with the next step (or, in a group of fewer rows
-// than a K-step, reads rows before the group), and both panels are zeroed there once they have
-// landed, so that those k add 0 x 0 whatever the memory holds. Outside the gradient a K below one
-// K-step starts at k = 0, and its last, partial chunk ends at the last k instead: the k that it
-// shares with the chunk before are zeroed, and all chunks after it.
+// matrix' edge start earlier instead (every 16-byte chunk inside its row; elements of C left of the
+// tile's origin belong to the tile before and are not stored again), or, with fewer columns than
+// the tile, clamp to the row's last 16 bytes: the last chunk is moved back by what it would have
+// crossed, and so are its elements of C, those that the chunk before holds too not being stored
+// again. A partial K-step is run first and ends at the last k: it shares its first `ov` k with the
+// next step (or, in a group of fewer rows than a K-step, reads rows before the group), and both
+// panels are zeroed there once they have landed, so that those k add 0 x 0 whatever the memory
+// holds. Outside the gradient a K below one K-step starts at k = 0, and its last, partial chunk
+// ends at the last k instead: the k that it shares with the chunk before are zeroed, and all chunks
+// after it.
 //
 // Bound by the matrix cores at the clock the power limit leaves (1.64-1.7 GHz; MFMAs busy 67-75% of it,
 // no LDS bank conflicts). 256 x 256, one workgroup per CU: 1.35 us per K-step and round of 256 tiles;
