@@ -386,6 +386,29 @@ int mm_gemm_i8_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const in
                        void *C, int c_type, int64_t ldc, void *stream);
 
 /*
+ * Inspection of the grouped and the 8-bit products, which share one table of kernels:
+ *   mm_gemm_grouped_num_configs, mm_gemm_grouped_config_name(cfg): count and names (NULL for
+ *     an index outside the table).
+ *   ..._select: the kernel that the call with these arguments runs (mm_gemm_h16_...: the calls
+ *     of both 16-bit formats); -1 if the call is refused or enqueues nothing. It depends on the
+ *     sizes, the strides and the alignment of the addresses of the inputs, which are not read,
+ *     and not on the offsets.
+ */
+int mm_gemm_grouped_num_configs(void);
+const char *mm_gemm_grouped_config_name(int cfg);
+int mm_gemm_h16_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K,
+                               const uint16_t *A, int64_t lda,
+                               const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b);
+int mm_gemm_h16_grouped_grad_b_select(int64_t groups, int64_t M, int64_t N, int64_t K,
+                                      const uint16_t *A, int64_t lda,
+                                      const uint16_t *G, int64_t ldg);
+int mm_gemm_i8_select(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
+                      const int8_t *B, int64_t ldb);
+int mm_gemm_i8_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K,
+                              const int8_t *A, int64_t lda,
+                              const int8_t *B, int64_t ldb, int64_t stride_b);
+
+/*
  * mm_conv2d_f32: 2-D convolution (cross-correlation, as in neural networks) in fp32,
  * lowered to the GEMM by im2col ("Matrix Operations", Introduction: a convolutional
  * layer's core recast as a matrix product; "GPU Matrix Multiplication: Tiling and

@@ -124,6 +124,17 @@ def load():
     lib.mm_gemm_i8.restype = ci
     lib.mm_gemm_i8_grouped.argtypes = [i64] * 4 + [vp, vp, i64, vp, vp, i64, i64, vp, vp, ci, i64, vp]
     lib.mm_gemm_i8_grouped.restype = ci
+    lib.mm_gemm_grouped_num_configs.argtypes = []
+    lib.mm_gemm_grouped_num_configs.restype = ci
+    lib.mm_gemm_grouped_config_name.argtypes = [ci]
+    lib.mm_gemm_grouped_config_name.restype = ctypes.c_char_p
+    lib.mm_gemm_h16_grouped_select.argtypes = [i64] * 4 + [vp, i64, vp, i64, i64, ci]
+    lib.mm_gemm_h16_grouped_grad_b_select.argtypes = [i64] * 4 + [vp, i64, vp, i64]
+    lib.mm_gemm_i8_select.argtypes = [i64] * 3 + [vp, i64, vp, i64]
+    lib.mm_gemm_i8_grouped_select.argtypes = [i64] * 4 + [vp, i64, vp, i64, i64]
+    for name in ("mm_gemm_h16_grouped_select", "mm_gemm_h16_grouped_grad_b_select", "mm_gemm_i8_select",
+                 "mm_gemm_i8_grouped_select"):
+        getattr(lib, name).restype = ci
     lib.mm_status_string.argtypes = [ci]
     lib.mm_status_string.restype = ctypes.c_char_p
     lib.mm_last_error.argtypes = []
@@ -381,6 +392,37 @@ def mm_gemm_i8_grouped(groups, M, N, K, offsets, A, lda, a_scale, B, ldb, stride
     _check(lib.mm_gemm_i8_grouped(groups, M, N, K, _addr(offsets), _addr(A), lda, _addr(a_scale),
                                   _addr(B), ldb, stride_b, _addr(b_scale), _addr(C), c_type, ldc,
                                   _stream(stream)), "mm_gemm_i8_grouped")
+
+
+def mm_gemm_grouped_num_configs():
+    """Number of kernels of the grouped and the 8-bit products."""
+    return load().mm_gemm_grouped_num_configs()
+
+
+def mm_gemm_grouped_config_name(cfg):
+    """Name of kernel `cfg` of the grouped and the 8-bit products, None outside the table."""
+    name = load().mm_gemm_grouped_config_name(cfg)
+    return name.decode() if name is not None else None
+
+
+def mm_gemm_h16_grouped_select(groups, M, N, K, A, lda, B, ldb, stride_b, trans_b):
+    """Kernel that mm_gemm_bf16_grouped and mm_gemm_f16_grouped run (-1: none)."""
+    return load().mm_gemm_h16_grouped_select(groups, M, N, K, _addr(A), lda, _addr(B), ldb, stride_b, trans_b)
+
+
+def mm_gemm_h16_grouped_grad_b_select(groups, M, N, K, A, lda, G, ldg):
+    """Kernel that mm_gemm_bf16_grouped_grad_b and mm_gemm_f16_grouped_grad_b run (-1: none)."""
+    return load().mm_gemm_h16_grouped_grad_b_select(groups, M, N, K, _addr(A), lda, _addr(G), ldg)
+
+
+def mm_gemm_i8_select(M, N, K, A, lda, B, ldb):
+    """Kernel that mm_gemm_i8 runs (-1: none)."""
+    return load().mm_gemm_i8_select(M, N, K, _addr(A), lda, _addr(B), ldb)
+
+
+def mm_gemm_i8_grouped_select(groups, M, N, K, A, lda, B, ldb, stride_b):
+    """Kernel that mm_gemm_i8_grouped runs (-1: none)."""
+    return load().mm_gemm_i8_grouped_select(groups, M, N, K, _addr(A), lda, _addr(B), ldb, stride_b)
 
 
 def mm_status_string(status):

@@ -310,6 +310,26 @@ int run_group(mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, int64_t K,
                     mm::group_launch(a, static_cast<hipStream_t>(stream)));
 }
 
+// The kernel of the call that `a` describes but for its offsets, outputs and scales; -1 if it is refused
+// or launches nothing.
+int select_group(mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, int64_t K, bool dense)
+{
+    static const int64_t present = 0;  // its address stands for the pointers that the choice does not use
+    a.C = const_cast<int64_t *>(&present);
+    a.offsets = dense ? nullptr : &present;
+    a.sa = a.sb = reinterpret_cast<const float *>(&present);
+    a.ldc = N > 1 ? N : 1;
+    a.stride_c = 0;
+    a.c_type = MM_TYPE_F32;
+    if (check_group(a, groups, M, N, K, dense) != MM_OK) return -1;
+    if (groups == 0 || N == 0 || (a.grad ? K : M) == 0) return -1;
+    a.groups = (int)groups;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    return mm::group_select(a);
+}
+
 int run_grouped16(mm::GroupElem elem, int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
                   const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b,
                   void *C, int c_type, int64_t ldc, void *stream)
@@ -691,6 +711,64 @@ int mm_gemm_i8_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const in
     a.stride_sb = N;
     a.c_type = c_type;
     return run_group(a, groups, M, N, K, false, stream);
+}
+
+int mm_gemm_grouped_num_configs(void) { return mm::group_num_configs(); }
+const char *mm_gemm_grouped_config_name(int cfg) { return mm::group_config_name(cfg); }
+
+int mm_gemm_h16_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
+                               const uint16_t *B, int64_t ldb, int64_t stride_b, int trans_b)
+{
+    if (trans_b != 0 && trans_b != 1) return -1;
+    mm::GroupArgs a{};
+    a.elem = mm::GroupElem::Bf16;
+    a.A = A;
+    a.B = B;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.stride_b = stride_b;
+    a.trans_b = trans_b == 1;
+    return select_group(a, groups, M, N, K, false);
+}
+
+int mm_gemm_h16_grouped_grad_b_select(int64_t groups, int64_t M, int64_t N, int64_t K, const uint16_t *A, int64_t lda,
+                                      const uint16_t *G, int64_t ldg)
+{
+    mm::GroupArgs a{};
+    a.elem = mm::GroupElem::Bf16;
+    a.grad = true;
+    a.A = A;
+    a.B = G;
+    a.lda = lda;
+    a.ldb = ldg;
+    return select_group(a, groups, M, N, K, false);
+}
+
+int mm_gemm_i8_select(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const int8_t *B, int64_t ldb)
+{
+    mm::GroupArgs a{};
+    a.elem = mm::GroupElem::I8;
+    a.trans_b = true;
+    a.A = A;
+    a.B = B;
+    a.lda = lda;
+    a.ldb = ldb;
+    return select_group(a, 1, M, N, K, true);
+}
+
+int mm_gemm_i8_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
+                              const int8_t *B, int64_t ldb, int64_t stride_b)
+{
+    mm::GroupArgs a{};
+    a.elem = mm::GroupElem::I8;
+    a.trans_b = true;
+    a.A = A;
+    a.B = B;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.stride_b = stride_b;
+    a.stride_sb = N;
+    return select_group(a, groups, M, N, K, false);
 }
 
 const char *mm_status_string(int status)

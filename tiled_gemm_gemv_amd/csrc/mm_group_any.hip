@@ -131,30 +131,62 @@ hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream)
     return a.trans_b ? launch_any<ElemBf16, false, false>(a, stream) : launch_any<ElemBf16, false, true>(a, stream);
 }
 
-// The kernel whose modelled time is least among those that take the shape.
-hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
+// The kernels by number: one workgroup's rows and columns, and how many parts of k it sums side by side.
+// "Row": one row of a group, in columns of 8 or 4 to a wave.
+namespace {
+
+constexpr const char *kNames[] = {
+    "any 64x64",
+    "row x16", "row x32",
+    "rows 16x16", "rows 16x32", "rows 16x64", "rows 16x128",
+    "rows 32x16", "rows 32x32", "rows 32x64", "rows 32x128",
+    "rows 64x16", "rows 64x32", "rows 64x64", "rows 64x128",
+    "tile 64x64 in 4", "tile 64x64 in 2", "tile 128x128", "tile 256x256",
+};
+constexpr int kConfigs = sizeof kNames / sizeof kNames[0];
+constexpr int kAny = 0, kRow = 1, kRows = 3, kTiles = 15;
+
+int rows_config(int rows, int cols)
 {
-    enum { kAny, kRows, kTile };
-    int best = kAny, rows = 0;
-    GroupTileKind tile = GroupTileKind::Mid;
+    if (rows == 1) return kRow + (cols == 32);
+    const int r = rows == 16 ? 0 : rows == 32 ? 1 : 2, c = cols == 16 ? 0 : cols == 32 ? 1 : cols == 64 ? 2 : 3;
+    return kRows + 4 * r + c;
+}
+
+constexpr GroupTileKind kTileKinds[] = {GroupTileKind::Small4, GroupTileKind::Small, GroupTileKind::Mid, GroupTileKind::Large};
+
+}  // namespace
+
+int group_num_configs() { return kConfigs; }
+const char *group_config_name(int cfg) { return cfg >= 0 && cfg < kConfigs ? kNames[cfg] : nullptr; }
+
+// The kernel whose modelled time is least among those that take the shape.
+int group_select(const GroupArgs &a)
+{
+    int best = kAny;
     double time = 1e300;
     constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
-    if (a.M <= largest && a.N <= largest && a.K <= largest) {
-        if (!a.grad)
-            for (int r : {1, 16, 32, 64}) {
-                if (!group_rows_ok(a, r)) continue;
-                const double t = group_rows_time(a, r);
-                if (t < time) best = kRows, rows = r, time = t;
-            }
-        for (GroupTileKind k : {GroupTileKind::Small4, GroupTileKind::Small, GroupTileKind::Mid, GroupTileKind::Large}) {
-            if (!group_tile_ok(a, k)) continue;
-            const double t = group_tile_time(a, k);
-            if (t < time) best = kTile, tile = k, time = t;
+    if (a.M > largest || a.N > largest || a.K > largest) return kAny;
+    if (!a.grad)
+        for (int r : {1, 16, 32, 64}) {
+            if (!group_rows_ok(a, r)) continue;
+            const double t = group_rows_time(a, r);
+            if (t < time) best = rows_config(r, group_rows_columns(a, r)), time = t;
         }
+    for (int k = 0; k < 4; ++k) {
+        if (!group_tile_ok(a, kTileKinds[k])) continue;
+        const double t = group_tile_time(a, kTileKinds[k]);
+        if (t < time) best = kTiles + k, time = t;
     }
-    if (best == kRows) return group_rows_launch(a, rows, stream);
-    if (best == kTile) return group_tile_launch(a, tile, stream);
-    return group_any_launch(a, stream);
+    return best;
+}
+
+hipError_t group_launch(const GroupArgs &a, hipStream_t stream)
+{
+    const int cfg = group_select(a);
+    if (cfg == kAny) return group_any_launch(a, stream);
+    if (cfg >= kTiles) return group_tile_launch(a, kTileKinds[cfg - kTiles], stream);
+    return group_rows_launch(a, cfg < kRows ? 1 : 16 << (cfg - kRows) / 4, stream);
 }
 
 }  // namespace mm

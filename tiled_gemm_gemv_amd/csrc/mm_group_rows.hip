@@ -423,8 +423,10 @@ hipError_t launch_t(const GroupArgs &a, hipStream_t stream)
 // Columns per workgroup: with many workgroups wide strips, which read A's rows less often; with few
 // narrow ones, since one workgroup streams no more than about 40 GB/s. Measured at 16 rows: i8, 16
 // groups of 4096 x 2048 38 us in strips of 16, 31 in strips of 32; one of 4096 x 4096 7.1 and 9.0.
+// One row: 4 waves of 8 columns of 2 KB or 4 of 4 KB, 16 KB requested at once where k is that long.
 int strip_columns(const GroupArgs &a, int rows)
 {
+    if (rows == 1) return (int64_t)a.K * (a.elem == GroupElem::I8 ? 1 : 2) <= 2048 ? 32 : 16;
     const double tiles = expected_row_tiles(a, rows);
     if (a.trans_b) return tiles * ((a.N + 31) / 32) >= 768 ? 32 : 16;
     const double wide = tiles * ((a.N + 127) / 128);
@@ -432,11 +434,10 @@ int strip_columns(const GroupArgs &a, int rows)
     return a.N >= 8 && wide >= 192 ? 128 : 64;
 }
 
-// J columns of U KB each per wave: 16 KB requested at once where k is that long.
 template <class E>
 hipError_t rows_dot(const GroupArgs &a, hipStream_t stream)
 {
-    if ((int64_t)a.K * (int64_t)sizeof(typename E::T) <= 2048)
+    if (strip_columns(a, 1) == 32)
         return launch_rows<1>(reinterpret_cast<const void *>(&rows_kernel_dot<E, 8, 2>), a, 32, 4, stream);
     return launch_rows<1>(reinterpret_cast<const void *>(&rows_kernel_dot<E, 4, 4>), a, 16, 4, stream);
 }
@@ -494,6 +495,8 @@ double group_rows_time(const GroupArgs &a, int rows)
     const double rounds = a.trans_b ? ceil(tiles / 768) * (1.2 + 0.4 * rb) : ceil(tiles / 256) * (2 + 1.25 * rb);
     return 2.5 + fmax(2 + stream, rounds);
 }
+
+int group_rows_columns(const GroupArgs &a, int rows) { return strip_columns(a, rows); }
 
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream)
 {

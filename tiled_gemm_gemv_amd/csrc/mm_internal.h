@@ -161,7 +161,11 @@ struct GroupArgs {
     bool trans_b;              // B_g stored N x K (always so for I8)
     bool grad;                 // gradient mode
 };
-// The kernel for the shape; M, N, groups >= 1 (gradient mode: K, N, groups >= 1).
+// The kernel for the shape; M, N, groups >= 1 (gradient mode: K, N, groups >= 1). It depends on the
+// sizes, strides, types and addresses of A and B only.
+int group_num_configs();
+const char *group_config_name(int cfg);
+int group_select(const GroupArgs &a);
 hipError_t group_launch(const GroupArgs &a, hipStream_t stream);
 // Tiles of 256 x 256 (Large), 128 x 128 (Mid) or 64 x 64 with panels loaded straight into LDS
 // (mm_group_tile.hip), the last with each sum in two (Small) or four parts (Small4) in one workgroup:
@@ -174,6 +178,7 @@ hipError_t group_tile_launch(const GroupArgs &a, GroupTileKind kind, hipStream_t
 // mode, with M, N and K at most 2^31 - 1 - 1024.
 bool group_rows_ok(const GroupArgs &a, int rows);
 double group_rows_time(const GroupArgs &a, int rows);
+int group_rows_columns(const GroupArgs &a, int rows);  // columns of a workgroup's strip
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream);
 // Any shape and alignment (mm_group_any.hip).
 hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream);
