@@ -22,7 +22,7 @@ NARROW = [f"rows {r}x{c}" for r in (16, 32, 64) for c in (16, 32)]        # rows
 WIDE = ["rows 16x32", "rows 32x32"] + [f"rows {r}x{c}" for r in (16, 32, 64) for c in (64, 128)]  # across k
 TILES = ["tile 64x64 in 4", "tile 64x64 in 2", "tile 128x128", "tile 256x256"]
 # What calls can get. (Rows of B along k: "any" only within 1024 of 2^31, as in test_most_rows.)
-KERNELS = {"kn": ["any 64x64"] + WIDE + TILES, "nk": ROW + NARROW + TILES, "grad": ["any 64x64"] + TILES,
+KERNELS = {"kn": ["any 64x64"] + WIDE + TILES, "nk": ROW[:1] + NARROW + TILES, "grad": ["any 64x64"] + TILES,
            "i8": ROW + NARROW + TILES, "i8g": ROW + NARROW + TILES}
 
 # (call, kernel, groups, rows in groups, rows before and after them, N, K, rows at odd elements)
@@ -115,9 +115,9 @@ CASES = [
     ("nk", "row x16", 64, 10, 0, 3, 131, 2304, False),
     ("nk", "row x16", 32, 6, 1, 2, 53, 2049, True),
     ("nk", "row x16", 5, 2, 0, 0, 27, 2103, False),
-    ("nk", "row x32", 64, 8, 1, 2, 260, 1024, False),
-    ("nk", "row x32", 64, 12, 0, 0, 67, 777, True),
-    ("nk", "row x32", 7, 3, 0, 0, 35, 869, False),
+    ("nk", "rows 16x16", 64, 8, 1, 2, 260, 1024, False),
+    ("nk", "rows 16x16", 64, 12, 0, 0, 67, 777, True),
+    ("nk", "rows 16x16", 7, 3, 0, 0, 35, 869, False),
     ("nk", "rows 16x16", 3, 5, 1, 2, 17, 73, False),
     ("nk", "rows 16x16", 3, 3, 1, 2, 17, 70, True),
     ("nk", "rows 16x32", 3, 316, 1, 2, 1460, 117, False),
@@ -219,6 +219,34 @@ def test_choices_stay_in_the_table():
         cols, b_rows = (N, K) if op in ("kn", "grad") else (K, N)
         name = select(op, groups, M, N, K, FAKE, K + gap, FAKE, cols + gap, b_rows * (cols + gap))
         assert name in KERNELS[op], (op, groups, M, N, K, gap, name)
+
+
+def test_one_row_meets_one_group():
+    # one row in one group is the dense product of one row, whatever the sizes
+    for N in (1, 32, 777, 4096, 14336):
+        for K in (64, 1000, 1331, 2048, 4096, 7000):
+            dense = mm.mm_gemm_i8_select(1, N, K, FAKE, K, FAKE, K)
+            assert mm.mm_gemm_i8_grouped_select(1, 1, N, K, FAKE, K, FAKE, K, N * K) == dense, (N, K)
+    assert select("i8g", 1, 1, 14336, 4096, FAKE, 4096, FAKE, 4096, 0) == "row x16"
+    assert select("nk", 1, 1, 14336, 4096, FAKE, 4096, FAKE, 4096, 0) == "row x16"
+
+
+@pytest.mark.parametrize("groups,rows", [(2, 1), (3, 1), (3, 2), (4, 2), (8, 1), (8, 2), (64, 8)])
+def test_few_rows_among_few_groups(groups, rows):
+    # rows at random fall into G (1 - (1 - 1/G)^M) of G groups; with M little above that, about one row
+    # to a group is what the call is taken for
+    expected = groups * (1 - (1 - 1 / groups) ** rows)
+    assert rows <= 1.25 * expected
+    for op in ("nk", "i8g"):
+        name = select(op, groups, rows, 4096, 4096, FAKE, 4096, FAKE, 4096, 4096 * 4096)
+        assert name == "row x16", (op, name)
+
+
+@pytest.mark.parametrize("groups,rows", [(1, 2), (2, 2), (3, 3), (8, 5), (64, 40)])
+def test_more_rows_than_groups_they_fall_into(groups, rows):
+    assert rows > 1.25 * groups * (1 - (1 - 1 / groups) ** rows)
+    for op in ("nk", "i8g"):
+        assert select(op, groups, rows, 4096, 4096, FAKE, 4096, FAKE, 4096, 4096 * 4096) not in ROW
 
 
 def test_calls_without_a_kernel():

@@ -229,12 +229,13 @@ struct RowTiles {
 };
 
 // What the host expects of group sizes that it does not know, for the choice of a kernel: groups
-// with a row (rows spread at random), BM-row tiles (a group's last tile half full on average), and
-// the bytes of the right-hand matrices that are read.
+// with a row, BM-row tiles (a group's last tile half full on average), and the bytes of the
+// right-hand matrices that are read. Rows fall into the groups at random: one of G groups stays empty
+// with probability (1 - 1/G)^M, M >= 1 rows, so G (1 - (1 - 1/G)^M) have rows: 1 where M or G is 1.
 inline double expected_groups(const GroupArgs &a)
 {
-    if (!a.offsets) return 1;
-    return a.groups * (1 - exp(-(double)a.M / a.groups));
+    if (!a.offsets || a.groups == 1) return 1;
+    return a.groups * -expm1(a.M * log1p(-1.0 / a.groups));
 }
 inline double expected_row_tiles(const GroupArgs &a, int bm)
 {

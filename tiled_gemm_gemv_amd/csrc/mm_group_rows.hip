@@ -423,10 +423,10 @@ hipError_t launch_t(const GroupArgs &a, hipStream_t stream)
 // Columns per workgroup: with many workgroups wide strips, which read A's rows less often; with few
 // narrow ones, since one workgroup streams no more than about 40 GB/s. Measured at 16 rows: i8, 16
 // groups of 4096 x 2048 38 us in strips of 16, 31 in strips of 32; one of 4096 x 4096 7.1 and 9.0.
-// One row: 4 waves of 8 columns of 2 KB or 4 of 4 KB, 16 KB requested at once where k is that long.
+// One row: 4 waves of 4 columns of 4 KB, or 8 of 2 KB of short 8-bit rows: 16 KB requested at once.
 int strip_columns(const GroupArgs &a, int rows)
 {
-    if (rows == 1) return (int64_t)a.K * (a.elem == GroupElem::I8 ? 1 : 2) <= 2048 ? 32 : 16;
+    if (rows == 1) return a.elem == GroupElem::I8 && a.K <= 2048 ? 32 : 16;
     const double tiles = expected_row_tiles(a, rows);
     if (a.trans_b) return tiles * ((a.N + 31) / 32) >= 768 ? 32 : 16;
     const double wide = tiles * ((a.N + 127) / 128);
@@ -437,8 +437,9 @@ int strip_columns(const GroupArgs &a, int rows)
 template <class E>
 hipError_t rows_dot(const GroupArgs &a, hipStream_t stream)
 {
-    if (strip_columns(a, 1) == 32)
-        return launch_rows<1>(reinterpret_cast<const void *>(&rows_kernel_dot<E, 8, 2>), a, 32, 4, stream);
+    if constexpr (E::INT8)
+        if (strip_columns(a, 1) == 32)
+            return launch_rows<1>(reinterpret_cast<const void *>(&rows_kernel_dot<E, 8, 2>), a, 32, 4, stream);
     return launch_rows<1>(reinterpret_cast<const void *>(&rows_kernel_dot<E, 4, 4>), a, 16, 4, stream);
 }
 
@@ -471,8 +472,12 @@ hipError_t rows_t(const GroupArgs &a, int rows, hipStream_t stream)
 
 bool group_rows_ok(const GroupArgs &a, int rows)
 {
-    // one row at a time: about one row to a group, and 1 KB of it
-    if (rows == 1) return a.trans_b && a.M <= 1.25 * expected_groups(a) && (int64_t)a.K * (a.elem == GroupElem::I8 ? 1 : 2) >= 1024;
+    // One row at a time: about one row to a group, since each row reads its matrix (one that several
+    // rows share comes from L2 again), and of 8-bit elements 1 KB of it, of 16-bit ones more than 2.
+    // Against the other kernels, cold, rows at random: 8-bit 0.6-1.2 times their time (5 rows, 27 groups
+    // of 8496 x 6448: 45 us and 54); 16-bit 0.55-1.3 (one row of 6880 x 6064: 18 us and 32), up to 2 KB
+    // 0.8-1.6 (2 rows, 3 groups of 2173 x 900: 8.6 us and 5.4), most of it in partial loads.
+    if (rows == 1) return a.trans_b && a.M <= 1.25 * expected_groups(a) && a.K >= (a.elem == GroupElem::I8 ? 1024 : 1025);
     return a.trans_b || a.N >= (rows == 64 ? 4 : 2);  // a lane's columns of B rows across k
 }
 
