@@ -158,3 +158,18 @@ def test_front_ends_refuse_host_tensors_and_wrong_types():
         mm.quantize_i8(torch.zeros(4, 8))
     with pytest.raises(TypeError):
         mm.quantize_i8(torch.zeros(4, 8, dtype=torch.float64))
+
+
+def test_matrices_apart():
+    """The check of an output's strides against a count of the elements' addresses."""
+    for count in (2, 3, 5):
+        for rows in (1, 2, 3):
+            for cols in (1, 2, 4):
+                for stride in range(0, 14):
+                    for ld in range(cols, 25):
+                        at = {g * stride + i * ld + j for g in range(count) for i in range(rows) for j in range(cols)}
+                        if mm._apart(count, stride, rows, ld, cols):
+                            assert len(at) == count * rows * cols, (count, stride, rows, ld, cols)
+    assert mm._apart(3, 20, 4, 5, 5) and not mm._apart(3, 19, 4, 5, 5)    # one after the other
+    assert mm._apart(3, 5, 4, 15, 5) and not mm._apart(3, 5, 4, 14, 5)    # row by row in turn
+    assert not mm._apart(2, 0, 4, 100, 5)

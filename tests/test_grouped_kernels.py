@@ -349,3 +349,22 @@ def test_i8_on(dev, case, out):
     check_i8(host64(C), want, DT[out])
     C.fill_(nan)
     assert torch.isnan(buf).all().item(), "wrote outside C"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K,counts", [(5, 6, [3, 0, 4]), (72, 40, [3, 0, 40]), (333, 264, [100, 1, 0, 70]), (1030, 520, [300, 129])])
+def test_grad_b_into_matrices_row_by_row(dev, N, K, counts):
+    off, groups, nan = ranges(counts), len(counts), float("nan")
+    A, G = draw(1, (off[-1], K), "int", "bf16", dev), draw(2, (off[-1], N), "int", "bf16", dev)
+    want, S = reference_grad_b(A, G, off)
+    offsets = torch.tensor(off, device=dev)
+    for gap in (0, 3):
+        buf = torch.full((K, groups, N + gap), nan, device=dev)
+        D = buf[:, :, :N].transpose(0, 1)
+        assert mm.gemm16_grouped_grad_b(A, G, offsets, out=D) is D
+        torch.cuda.synchronize()
+        check(host64(D), want, S, "int", torch.float32)
+        D.fill_(nan)
+        assert torch.isnan(buf).all().item(), "wrote outside the matrices"
+    with pytest.raises(ValueError, match="overlap"):  # rows of two matrices share elements
+        mm.gemm16_grouped_grad_b(A, G, offsets, out=torch.as_strided(buf, (groups, K, N), (N - 1, groups * N, 1)))

@@ -717,6 +717,12 @@ def _stack(t, name, dtypes):
     return ld, stride_g
 
 
+def _apart(count, stride, rows, ld, cols):
+    """Whether `count` rows x cols matrices, `stride` elements apart, share no element: each ends before
+    the next begins, or all their rows i lie between one matrix' row i and its row i + 1."""
+    return stride >= (rows - 1) * ld + cols or (stride >= cols and ld >= (count - 1) * stride + cols)
+
+
 def _offsets(t, groups, device):
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int64:
@@ -788,7 +794,8 @@ def gemm16_grouped_grad_b(A, G, offsets, out=None, out_dtype=None, stream=None):
     """The gradient of gemm16_grouped(A, B, offsets) with respect to B from the gradient G of its
     output: out[g] = A[lo:hi].T @ G[lo:hi] over the rows lo = offsets[g] .. hi = offsets[g + 1]
     (zeros for an empty group), groups x K x N. For B stored groups x N x K (trans_b) exchange A
-    and G. A, G: bf16 or fp16 of the same dtype; out float32 (default), bfloat16 or float16."""
+    and G. A, G: bf16 or fp16 of the same dtype; out float32 (default), bfloat16 or float16, its
+    matrices one after the other or row by row in turn (a transposed K x groups x N)."""
     import torch
     lda = _matrix(A, "A", (torch.bfloat16, torch.float16))
     ldg = _matrix(G, "G", (A.dtype,))
@@ -803,8 +810,8 @@ def gemm16_grouped_grad_b(A, G, offsets, out=None, out_dtype=None, stream=None):
     groups = offsets.shape[0] - 1
     _offsets(offsets, groups, device)
     out, d_type, ldd, stride_d = _output(out, out_dtype, (groups, K, N), A)
-    if groups > 1 and K > 0 and N > 0 and stride_d < (K - 1) * ldd + N:
-        raise ValueError("the matrices of out overlap")
+    if groups > 1 and K > 0 and N > 0 and not _apart(groups, stride_d, K, ldd, N):
+        raise ValueError("the matrices of out overlap (neither one after the other nor row by row in turn)")
     name = "mm_gemm_bf16_grouped_grad_b" if A.dtype is torch.bfloat16 else "mm_gemm_f16_grouped_grad_b"
     _run(name, device, stream, groups, M, N, K, offsets.data_ptr(), A.data_ptr(), lda, G.data_ptr(), ldg,
          out.data_ptr(), d_type, ldd, stride_d)
