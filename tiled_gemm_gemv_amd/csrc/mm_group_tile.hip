@@ -244,8 +244,8 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     // ---- DMA. This lane's byte offsets from the panel's corner at a K-step; the host keeps them
     // below 2^32.
     unsigned a_voff[2][T::A_LD], b_voff[2][T::B_LD];
-    // first k of the partial step that is below row 0 of the matrix (groups near its start): those
-    // lanes read row 0
+    // first k of the partial step that is below row 0 of the matrix (groups near its start, whose only
+    // step it is): those lanes read row 0
     auto offsets_of = [&](int k_first) {
         const int below = k_first < 0 ? -k_first : 0;
         const int last16 = min(p.K, T::BK) * T::ES - 16;  // the last chunk of a row shorter than a K-step
@@ -458,7 +458,6 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         constexpr int panels = LO ? 3 : 4;  // half panels per K-step
         offsets_of(ov ? k_end - T::BK : 0);
         for (int i = 0; i < panels; ++i) issue(0, i);
-        if (GRAD && ov && k_end < T::BK) offsets_of(0);
         if (nk > 1)
             for (int i = 0; i < panels; ++i) issue(1, i);
         if (ov) {
