@@ -8,9 +8,9 @@ torch.cuda.Stream, or None for torch's current stream on the current device.
 
 gemm(A, B, out=None), gemv(A, x, out=None), conv2d(x, w, ...), gemm16_grouped(A, B, offsets),
 gemm_i8(A, B, a_scale, b_scale) etc. are conveniences for torch tensors:
-they check dtypes, devices and strides, allocate the output with torch when none
-is given, and call the C entry points. PyTorch only provides device memory and
-streams here.
+they check dtypes, devices and strides (not those of empty tensors, which are arbitrary),
+allocate the output with torch when none is given, and call the C entry points. PyTorch
+only provides device memory and streams here.
 
 There is no fallback: if libmm.so is missing or fails to load, every call raises.
 Build it with `python -m tiled_gemm_gemv_amd.build`.
