@@ -323,8 +323,8 @@ int mm_gemm_f16_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const i
  *             zeros. The D_g must not overlap (undefined, not checked).
  * With right-hand matrices stored N x K (trans_b = 1) exchange A and G (and N and K): the
  * result is then stored N x K too. Each element is one sum in a fixed order, so results are
- * deterministic. Values in rows of no group do not matter, NaN included. N == 0, K == 0 or groups == 0: nothing is
- * enqueued. Other arguments and errors as for mm_gemm_bf16_grouped.
+ * deterministic. Values in rows of no group do not matter, NaN included. N == 0, K == 0 or
+ * groups == 0: nothing is enqueued. Other arguments and errors as for mm_gemm_bf16_grouped.
  */
 int mm_gemm_bf16_grouped_grad_b(int64_t groups, int64_t M, int64_t N, int64_t K,
                                 const int64_t *offsets, const uint16_t *A, int64_t lda,

@@ -17,14 +17,17 @@
 // repeat its last row and are not stored.
 //
 // Bound by the stream of B from memory: 13 experts of 4096 x 2048 bf16 K x N, 16 rows, cold: 38 us,
-// 5.7 TB/s (through 128 x 128 tiles 43).
+// 5.7 TB/s (through 128 x 128 tiles 43). The same stored N x K 46 us, 4.7 TB/s: the MFMA's 16 pieces of
+// 64 bytes.
 //
 // With one row to a group and B's rows along k, whole rows of B (1 KB per wave and load) stream
 // faster than the MFMA's 16 pieces of 64 bytes, and the vector units keep up: each wave takes J
 // columns, multiplies its lanes' 16-byte pieces with A's by dot products (v_dot4_i32_i8, or fp32
 // multiply-adds of the 16-bit values) and adds the 64 lanes' sums at the end (fixed order). Cold, i8
 // 1 x 14336 x 4096: 15.6 us through the MFMA, 12.1 this way; 8 rows for 8 of 64 groups of 4096 x 2048:
-// 13.8 and 13.2; with 4 rows at a time 14.4 and 17.4 (registers for fewer waves), so only for one.
+// 13.8 and 13.2 (with 4 rows at a time, in registers for fewer waves, 14.4 and 17.4, so only for one);
+// the latter in bf16 23.5 us, 5.7 TB/s. Rows of one group each read its matrix, all but the first from
+// L2 where they run side by side, so the choice takes this kernel for about one row to a group only.
 #include "mm_group.h"
 
 namespace mm {

@@ -42,17 +42,19 @@
 // ends at the last k instead: the k that it shares with the chunk before are zeroed, and all chunks
 // after it.
 //
-// Bound by the matrix cores at the clock the power limit leaves (1.64-1.7 GHz; MFMAs busy 67-75% of it,
-// no LDS bank conflicts). 256 x 256, one workgroup per CU: 1.35 us per K-step and round of 256 tiles;
-// bf16 8192 x 14336 x 4096 682 us (1411 TFLOP/s), i8 362-386 us (2.5-2.65 POP/s). 128 x 128, two per
-// CU, for fewer tiles: i8 1000 x 1531 x 777 12 us. With fewer tiles than CUs a tile's panels bound it,
-// which one CU takes from L2 at about 100 GB/s: 64 x 64 tiles spread them over four times the CUs, and
-// the groups of a workgroup keep enough loads on their way (bf16 128 x 4096 x 4096 27.1 us in 128 x 128
-// tiles, 16.6 in 64 x 64; 256 x 2048 x 4096 26.9 and 14.8; two groups to a 128 x 128 tile no faster
-// than one). Against that, same shapes: 32 x 32 MFMAs instead of
-// 16 x 16 8-15% slower (they pass twice the accumulator bytes per product); 4 waves of 128 x 128 the
-// same with 32 x 32 MFMAs; a phase's reads in front of its MFMAs 5-8% slower; workgroups that stay
-// and load their next tile during the stores -1.7% to +8.6%.
+// Bound by the matrix cores at the clock the power limit leaves (1.64-1.7 GHz; MFMAs busy 67% of it in
+// i8 8192 x 14336 x 4096 and 75% in 8 bf16 experts of 14336 x 4096, 52-63% in a training batch's
+// gradients and 8-bit experts, whose last rounds are uneven; no LDS bank conflicts). 256 x 256, one
+// workgroup per CU: 1.35 us per K-step and round of 256 tiles; bf16 8192 x 14336 x 4096 682 us (1411
+// TFLOP/s), i8 368-371 us (2.6 POP/s; medians of calls in a row, single runs 362-410; 435-458 in short
+// runs under the profiler). 128 x 128, two per CU, for fewer tiles: i8 1000 x 1531 x 777 12 us. With
+// fewer tiles than CUs a tile's panels bound it, which one CU takes from L2 at about 100 GB/s: 64 x 64
+// tiles spread them over four times the CUs, and the groups of a workgroup keep enough loads on their
+// way (operands in the caches, bf16 128 x 4096 x 4096 27.1 us in 128 x 128 tiles, 16.6 in 64 x 64; 256 x
+// 2048 x 4096 26.9 and 14.8; two groups to a 128 x 128 tile no faster than one). Against that, same
+// shapes: 32 x 32 MFMAs instead of 16 x 16 8-15% slower (they pass twice the accumulator bytes per
+// product); 4 waves of 128 x 128 the same with 32 x 32 MFMAs; a phase's reads in front of its MFMAs 5-8%
+// slower; workgroups that stay and load their next tile during the stores -1.7% to +8.6%.
 #include "mm_group.h"
 
 namespace mm {
@@ -753,7 +755,8 @@ auto with_tiles(const GroupArgs &a, F &&f)
 }  // namespace
 
 // Fitted to some 300 shapes of all operators (the chosen kernel's time over the best one's: 1.03-1.04
-// in the mean). 256 x 256: 5.5 us per round for a tile's first loads and its stores, 1.35 per K-step of
+// in the mean, up to 1.4 for single shapes; neither the stored bytes nor the wait of a partial K-step
+// are terms of it). 256 x 256: 5.5 us per round for a tile's first loads and its stores, 1.35 per K-step of
 // all CUs, 0.45-0.75 per K-step of a last round in halves. 128 x 128: 0.28 us per K-step, and 0.75 times
 // the share of 512 tiles. 64 x 64 in four parts: 0.13-0.19 us per K-step and round of 256 tiles, in two
 // 0.19-0.36 for up to 512, more with operands across k (64-byte rows). So many tiles go to 256 x 256
