@@ -7,7 +7,8 @@
 // is one 16-byte LDS read. Single elements make no demand on alignment or sizes, and bound
 // the kernel (i8 8192 x 14336 x 4096 in 8.6 ms, 112 TOP/s): it is the one for what the others do not
 // take, a single column of matrices stored K x N, gradients of fewer than 8 rows or columns or with
-// strides that put a K-step's rows past 2^32 bytes, and sizes within 1024 of 2^31. The choice among all of them is at the end of this file.
+// strides that put a K-step's rows past 2^32 bytes, and sizes within 1024 of 2^31. The choice among all
+// of them is at the end of this file.
 #include "mm_group.h"
 
 namespace mm {
