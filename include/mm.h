@@ -19,7 +19,9 @@
  *   CONV  2-D convolution through the GEMM (mm_conv2d_f32 below).
  *
  *   Also: products with 16-bit inputs, products of rows grouped by expert with their
- *         gradients, and products of 8-bit integers with scales (below).
+ *         gradients, products of 8-bit integers with scales and of 4-bit floating point in
+ *         blocks with a scale each, the routing of tokens to experts, and the tokens' rows to
+ *         the experts' order and back (below).
  *
  * Conventions shared by every entry point:
  *   - Layout: row-major. Element (i, k) of A lives at A[i * lda + k], (k, j) of B
@@ -386,7 +388,170 @@ int mm_gemm_i8_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const in
                        void *C, int c_type, int64_t ldc, void *stream);
 
 /*
- * Inspection of the grouped and the 8-bit products, which share one table of kernels:
+ * mm_quantize_mx4: rows of a matrix to 4-bit floating point (1 sign, 2 exponent and 1 mantissa
+ * bit) in blocks of 32 elements along the row, a power of two for each block:
+ *
+ *   scale[i][b] = e + 127,  e = floor(log2 amax) - 2,  amax = max |X[i][j]| over block b,
+ *                 at least 0 (e >= -127), and 0 for a block of zeros
+ *   code of X[i][j]: X[i][j] / 2^e rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0
+ *                 to 7; halfway to the even code; above 6 to 6), plus 8 where X is negative
+ *   value       = (that number with its sign) * 2^(scale - 127); a scale of 255 stands for NaN
+ *
+ *   X, x_type, ldx   rows x cols of x_type (MM_TYPE_*), ldx >= max(1, cols).
+ *   Q, ldq    rows of 16 ceil(cols / 32) bytes, written: two codes to a byte, the even element in
+ *             its low half; the elements that a last block has beyond cols are zeros. ldq (bytes)
+ *             >= max(1, 16 ceil(cols / 32)).
+ *   scale, ld_scale  rows of ceil(cols / 32) bytes, written; ld_scale >= max(1, that).
+ * A block that holds an infinity or a NaN gets scale 255 and zeros, so that every product with it
+ * is NaN. rows == 0 or cols == 0: nothing is enqueued. Errors as for mm_gemm_f32;
+ * MM_ERR_INVALID_ARG also for an unknown type.
+ */
+int mm_quantize_mx4(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx,
+                    uint8_t *Q, int64_t ldq, uint8_t *scale, int64_t ld_scale, void *stream);
+
+/*
+ * mm_dequantize_mx4: the values that the codes stand for, rounded to x_type (exact in fp32 and
+ * bf16; infinities where a value is beyond the type's range, NaN where the scale is 255).
+ * Arguments as for mm_quantize_mx4; Q and scale are read, X (rows x cols) is written.
+ */
+int mm_dequantize_mx4(int64_t rows, int64_t cols, const uint8_t *Q, int64_t ldq,
+                      const uint8_t *scale, int64_t ld_scale,
+                      void *X, int x_type, int64_t ldx, void *stream);
+
+/*
+ * mm_gemm_mx4: product of two matrices in the format of mm_quantize_mx4, with k along their rows:
+ *
+ *   C[i][j] = sum over k in [0, K) of a[i][k] * b[j][k],  a and b the values of the codes
+ *
+ *   K         a multiple of 32 (rows quantised with other cols are filled up with zeros).
+ *   A, lda    M rows of K / 2 bytes; B, ldb: N rows of K / 2 bytes; lda, ldb (bytes) >= max(1,
+ *             K / 2). Any alignment; rows that start at 16-byte boundaries are fastest.
+ *   a_scale, ld_as   M rows of K / 32 bytes; b_scale, ld_bs: N rows of them; ld >= max(1, K / 32).
+ *             Any alignment; rows that start at 4-byte boundaries are fastest.
+ *   C, c_type, ldc   M x N of c_type (MM_TYPE_*), ldc >= max(1, N).
+ * Products are exact; sums are fp32 and rounded once, to nearest even. Where powers of two are so
+ * small that products lie below 2^-126 they may count as zeros. A scale of 255 makes every element
+ * NaN that its block is summed into. K == 0: C is zeros. M == 0 or N == 0: nothing is enqueued.
+ * Errors as for mm_gemm_f32; MM_ERR_INVALID_ARG also for an unknown type or missing scales.
+ */
+int mm_gemm_mx4(int64_t M, int64_t N, int64_t K,
+                const uint8_t *A, int64_t lda, const uint8_t *a_scale, int64_t ld_as,
+                const uint8_t *B, int64_t ldb, const uint8_t *b_scale, int64_t ld_bs,
+                void *C, int c_type, int64_t ldc, void *stream);
+
+/*
+ * mm_gemm_mx4_grouped: mm_gemm_mx4 with the rows of A in groups and a right-hand matrix for each
+ * group (groups and offsets as for mm_gemm_bf16_grouped):
+ *   B, ldb, stride_b   N rows of group g from B + g * stride_b on (bytes, >= 0).
+ *   b_scale, ld_bs, stride_bs   N rows of group g from b_scale + g * stride_bs on (>= 0).
+ * Errors as for mm_gemm_mx4 and mm_gemm_bf16_grouped.
+ */
+int mm_gemm_mx4_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets,
+                        const uint8_t *A, int64_t lda, const uint8_t *a_scale, int64_t ld_as,
+                        const uint8_t *B, int64_t ldb, int64_t stride_b,
+                        const uint8_t *b_scale, int64_t ld_bs, int64_t stride_bs,
+                        void *C, int c_type, int64_t ldc, void *stream);
+
+/*
+ * mm_route_topk: routing of T tokens to k of E experts each, with the order of their rows that
+ * the grouped products take.
+ *
+ *   scores    s_e = exp(l_e) / sum over e' of exp(l_e')  (MM_ROUTE_SOFTMAX), or
+ *             s_e = 1 / (1 + exp(-l_e))                  (MM_ROUTE_SIGMOID)
+ *   choice    experts are ranked by c_e = s_e + bias_e; without a bias by l_e (which ranks them
+ *             as s_e does). With groups > 1 the experts stand in groups of E / groups neighbours,
+ *             a group's value is the sum of its group_top largest c_e (without a bias: of l_e
+ *             for group_top 1, of s_e for 2), and only the top_groups best groups' experts can be
+ *             chosen. The k best experts are, in falling order. All of this is computed in 64
+ *             bits; equal values rank by the lower index, NaN above every number.
+ *   weights   w_j = scale * s_j for the expert of slot j; with renormalize scale * s_j / (the sum
+ *             of the token's chosen scores), 0 where that sum is 0
+ *   rows      slots (t, j) in the order of their expert, then t, then j: rows[t][j] is the number
+ *             of the slot in that order, from 0
+ *   offsets   expert e's rows are offsets[e] <= row < offsets[e + 1]; offsets[E] in all
+ *
+ * An expert whose logit or c_e is -infinity is not chosen (a padded token: all of its logits).
+ * Slots for which no expert is left have expert -1, row -1 and weight 0, and count nowhere.
+ *   T, E, k   0 <= T, 0 <= E <= 1024, 0 <= k <= 32, k <= E, T k <= 2^31 - 1.
+ *   logits, type, ld   T x E of type (MM_TYPE_*), ld >= max(1, E).
+ *   bias      E entries, fp32, or NULL.
+ *   groups    1 .. 64, a divisor of E; top_groups 1 .. groups; group_top 1 or 2; k at most
+ *             top_groups * E / groups.
+ *   weights   T x k, packed, fp32; experts, rows: T x k, packed, 32-bit; offsets: E + 1 entries;
+ *             all written.
+ *   workspace 16-byte aligned, at least mm_route_topk_workspace_bytes(T, E, k) bytes (0: NULL
+ *             will do; -1: the sizes are refused). Calls that may run at the same time need one
+ *             each.
+ * Results are deterministic. T == 0 or k == 0: offsets are zeros. Errors as for mm_gemm_f32.
+ */
+#define MM_ROUTE_SOFTMAX 0
+#define MM_ROUTE_SIGMOID 1
+int64_t mm_route_topk_workspace_bytes(int64_t T, int64_t E, int64_t k);
+int mm_route_topk(int64_t T, int64_t E, int64_t k, const void *logits, int type, int64_t ld,
+                  int scoring, const float *bias, int64_t groups, int64_t top_groups,
+                  int64_t group_top, int renormalize, float scale,
+                  float *weights, int32_t *experts, int32_t *rows, int64_t *offsets,
+                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * mm_route_topk_grad: the logits' gradient from that of the weights (dweights, T x k, packed,
+ * fp32), for the experts that were chosen (T x k, packed; entries outside [0, E) are no expert).
+ * The choice itself has no gradient, and neither has the bias. With g_e the gradient of s_e:
+ *   softmax   dlogits_e = s_e (g_e - sum over e' of s_e' g_e')
+ *   sigmoid   dlogits_e = s_e (1 - s_e) g_e
+ *   g_e       of the expert of slot j: scale dw_j; renormalised, with S the sum of the chosen
+ *             scores, scale (dw_j - sum over i of dw_i s_i / S) / S (0 where S is 0); else 0
+ * dlogits is T x E of the logits' type, ldd >= max(1, E), written. Computed in fp32, rounded once.
+ * Other arguments as for mm_route_topk. T == 0 or E == 0: nothing is enqueued.
+ */
+int mm_route_topk_grad(int64_t T, int64_t E, int64_t k, const void *logits, int type, int64_t ld,
+                       int scoring, int renormalize, float scale,
+                       const int32_t *experts, const float *dweights,
+                       void *dlogits, int64_t ldd, void *stream);
+
+/*
+ * mm_spread_rows: tokens' rows to the experts' order, Y[rows[t][j]] = X[t], as bytes (elements of
+ * any type, codes or scales).
+ *   T, k, total   0 <= T, k, T k, total <= 2^31 - 1.
+ *   row_bytes     bytes of a row, 0 .. 2^31 - 1.
+ *   X, ldx    T rows, ldx (bytes) >= max(1, row_bytes); Y, ldy: total rows, likewise.
+ *   rows      T x k, packed, device memory. Entries outside [0, total) are no row. Rows of Y that
+ *             no entry names are left untouched; of a row that several name the bytes are
+ *             unspecified.
+ * The gradient is mm_combine_rows without weights. Nothing to write: nothing is enqueued. Errors
+ * as for mm_gemm_f32.
+ */
+int mm_spread_rows(int64_t T, int64_t k, int64_t row_bytes, const void *X, int64_t ldx,
+                   const int32_t *rows, int64_t total, void *Y, int64_t ldy, void *stream);
+
+/*
+ * mm_combine_rows: C[t] = sum over j of weights[t][j] * Y[rows[t][j]] (weights NULL: the plain
+ * sum), the experts' outputs back to the tokens.
+ *   Y, y_type, ldy   total x D of y_type, ldy >= max(1, D).
+ *   rows, total, T, k   as for mm_spread_rows: slots that are no row add nothing.
+ *   weights   T x k, packed, fp32, or NULL.
+ *   C, c_type, ldc   T x D of c_type, ldc >= max(1, D), written (zeros for a token without rows).
+ * Sums are fp32, over j in rising order, and rounded once. T == 0 or D == 0: nothing is enqueued.
+ */
+int mm_combine_rows(int64_t T, int64_t k, int64_t D, const void *Y, int y_type, int64_t ldy,
+                    int64_t total, const int32_t *rows, const float *weights,
+                    void *C, int c_type, int64_t ldc, void *stream);
+
+/*
+ * mm_combine_rows_grad: the gradients of mm_combine_rows with weights from the gradient G of its
+ * output (T x D of g_type, ldg >= max(1, D)):
+ *   dY[rows[t][j]] = weights[t][j] * G[t]        (total x D of y_type, lddy >= max(1, D))
+ *   dweights[t][j] = sum over d of Y[rows[t][j]][d] * G[t][d]      (0 for a slot that is no row)
+ * Rows of dY that no entry of rows names are left untouched; of one that several name the values
+ * are unspecified. Sums are fp32 in a fixed order. T == 0 or k == 0: nothing is enqueued.
+ */
+int mm_combine_rows_grad(int64_t T, int64_t k, int64_t D, const void *G, int g_type, int64_t ldg,
+                         const void *Y, int y_type, int64_t ldy, int64_t total,
+                         const int32_t *rows, const float *weights,
+                         void *dY, int64_t lddy, float *dweights, void *stream);
+
+/*
+ * Inspection of the grouped, the 8-bit and the 4-bit products, which share one table of kernels:
  *   mm_gemm_grouped_num_configs, mm_gemm_grouped_config_name(cfg): count and names (NULL for
  *     an index outside the table).
  *   ..._select: the kernel that the call with these arguments runs (mm_gemm_h16_...: the calls
@@ -407,6 +572,13 @@ int mm_gemm_i8_select(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t 
 int mm_gemm_i8_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K,
                               const int8_t *A, int64_t lda,
                               const int8_t *B, int64_t ldb, int64_t stride_b);
+int mm_gemm_mx4_select(int64_t M, int64_t N, int64_t K,
+                       const uint8_t *A, int64_t lda, const uint8_t *a_scale, int64_t ld_as,
+                       const uint8_t *B, int64_t ldb, const uint8_t *b_scale, int64_t ld_bs);
+int mm_gemm_mx4_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K,
+                               const uint8_t *A, int64_t lda, const uint8_t *a_scale, int64_t ld_as,
+                               const uint8_t *B, int64_t ldb, int64_t stride_b,
+                               const uint8_t *b_scale, int64_t ld_bs, int64_t stride_bs);
 
 /*
  * mm_conv2d_f32: 2-D convolution (cross-correlation, as in neural networks) in fp32,

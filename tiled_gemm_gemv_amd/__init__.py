@@ -7,7 +7,7 @@ torch tensor on the GPU; `stream` accepts a hipStream_t address (int), a
 torch.cuda.Stream, or None for torch's current stream on the current device.
 
 gemm(A, B, out=None), gemv(A, x, out=None), conv2d(x, w, ...), gemm16_grouped(A, B, offsets),
-gemm_i8(A, B, a_scale, b_scale) etc. are conveniences for torch tensors:
+gemm_i8(A, B, a_scale, b_scale), gemm_mx4(A, B, a_scale, b_scale), route_topk(logits, k) etc. are conveniences for torch tensors:
 they check dtypes, devices and strides (not those of empty tensors, which are arbitrary),
 allocate the output with torch when none is given, and call the C entry points. PyTorch
 only provides device memory and streams here.
@@ -124,6 +124,24 @@ def load():
     lib.mm_gemm_i8.restype = ci
     lib.mm_gemm_i8_grouped.argtypes = [i64] * 4 + [vp, vp, i64, vp, vp, i64, i64, vp, vp, ci, i64, vp]
     lib.mm_gemm_i8_grouped.restype = ci
+    lib.mm_quantize_mx4.argtypes = [i64, i64, vp, ci, i64, vp, i64, vp, i64, vp]
+    lib.mm_dequantize_mx4.argtypes = [i64, i64, vp, i64, vp, i64, vp, ci, i64, vp]
+    lib.mm_gemm_mx4.argtypes = [i64] * 3 + [vp, i64, vp, i64, vp, i64, vp, i64, vp, ci, i64, vp]
+    lib.mm_gemm_mx4_grouped.argtypes = [i64] * 4 + [vp, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, ci, i64, vp]
+    lib.mm_gemm_mx4_select.argtypes = [i64] * 3 + [vp, i64, vp, i64, vp, i64, vp, i64]
+    lib.mm_gemm_mx4_grouped_select.argtypes = [i64] * 4 + [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64]
+    f32 = ctypes.c_float
+    lib.mm_route_topk_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.mm_route_topk_workspace_bytes.restype = i64
+    lib.mm_route_topk.argtypes = [i64] * 3 + [vp, ci, i64, ci, vp, i64, i64, i64, ci, f32, vp, vp, vp, vp, vp, i64, vp]
+    lib.mm_route_topk_grad.argtypes = [i64] * 3 + [vp, ci, i64, ci, ci, f32, vp, vp, vp, i64, vp]
+    lib.mm_spread_rows.argtypes = [i64] * 3 + [vp, i64, vp, i64, vp, i64, vp]
+    lib.mm_combine_rows.argtypes = [i64] * 3 + [vp, ci, i64, i64, vp, vp, vp, ci, i64, vp]
+    lib.mm_combine_rows_grad.argtypes = [i64] * 3 + [vp, ci, i64, vp, ci, i64, i64, vp, vp, vp, i64, vp, vp]
+    for name in ("mm_quantize_mx4", "mm_dequantize_mx4", "mm_gemm_mx4", "mm_gemm_mx4_grouped", "mm_gemm_mx4_select",
+                 "mm_gemm_mx4_grouped_select", "mm_route_topk", "mm_route_topk_grad", "mm_spread_rows",
+                 "mm_combine_rows", "mm_combine_rows_grad"):
+        getattr(lib, name).restype = ci
     lib.mm_gemm_grouped_num_configs.argtypes = []
     lib.mm_gemm_grouped_num_configs.restype = ci
     lib.mm_gemm_grouped_config_name.argtypes = [ci]
@@ -394,13 +412,93 @@ def mm_gemm_i8_grouped(groups, M, N, K, offsets, A, lda, a_scale, B, ldb, stride
                                   _stream(stream)), "mm_gemm_i8_grouped")
 
 
+def mm_quantize_mx4(rows, cols, X, x_type, ldx, Q, ldq, scale, ld_scale, stream=None):
+    """Rows of X to 4-bit codes Q with a scale for each block of 32. Raises MMError."""
+    lib = load()
+    _check(lib.mm_quantize_mx4(rows, cols, _addr(X), x_type, ldx, _addr(Q), ldq, _addr(scale), ld_scale,
+                               _stream(stream)), "mm_quantize_mx4")
+
+
+def mm_dequantize_mx4(rows, cols, Q, ldq, scale, ld_scale, X, x_type, ldx, stream=None):
+    """The values of 4-bit codes Q and their scales. Raises MMError."""
+    lib = load()
+    _check(lib.mm_dequantize_mx4(rows, cols, _addr(Q), ldq, _addr(scale), ld_scale, _addr(X), x_type, ldx,
+                                 _stream(stream)), "mm_dequantize_mx4")
+
+
+def mm_gemm_mx4(M, N, K, A, lda, a_scale, ld_as, B, ldb, b_scale, ld_bs, C, c_type, ldc, stream=None):
+    """C = A x B^T of 4-bit A (M x K) and B (N x K) with a scale for each block of 32. Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_mx4(M, N, K, _addr(A), lda, _addr(a_scale), ld_as, _addr(B), ldb, _addr(b_scale), ld_bs,
+                           _addr(C), c_type, ldc, _stream(stream)), "mm_gemm_mx4")
+
+
+def mm_gemm_mx4_grouped(groups, M, N, K, offsets, A, lda, a_scale, ld_as, B, ldb, stride_b, b_scale, ld_bs,
+                        stride_bs, C, c_type, ldc, stream=None):
+    """mm_gemm_mx4 with rows of A in groups, a B_g and scales for each group. Raises MMError."""
+    lib = load()
+    _check(lib.mm_gemm_mx4_grouped(groups, M, N, K, _addr(offsets), _addr(A), lda, _addr(a_scale), ld_as, _addr(B),
+                                   ldb, stride_b, _addr(b_scale), ld_bs, stride_bs, _addr(C), c_type, ldc,
+                                   _stream(stream)), "mm_gemm_mx4_grouped")
+
+
+MM_ROUTE_SOFTMAX = 0  # scorings, as include/mm.h defines them
+MM_ROUTE_SIGMOID = 1
+
+
+def mm_route_topk_workspace_bytes(T, E, k):
+    """Bytes of workspace mm_route_topk needs for (T, E, k); -1 for invalid sizes."""
+    return load().mm_route_topk_workspace_bytes(T, E, k)
+
+
+def mm_route_topk(T, E, k, logits, type, ld, scoring, bias, groups, top_groups, group_top, renormalize, scale,
+                  weights, experts, rows, offsets, workspace, workspace_bytes, stream=None):
+    """The k best of E experts for each of T tokens, their weights and the rows' order. Raises MMError."""
+    lib = load()
+    _check(lib.mm_route_topk(T, E, k, _addr(logits), type, ld, scoring, _addr(bias), groups, top_groups, group_top,
+                             renormalize, scale, _addr(weights), _addr(experts), _addr(rows), _addr(offsets),
+                             _addr(workspace), workspace_bytes, _stream(stream)), "mm_route_topk")
+
+
+def mm_route_topk_grad(T, E, k, logits, type, ld, scoring, renormalize, scale, experts, dweights, dlogits, ldd,
+                       stream=None):
+    """The logits' gradient from that of the weights. Raises MMError."""
+    lib = load()
+    _check(lib.mm_route_topk_grad(T, E, k, _addr(logits), type, ld, scoring, renormalize, scale, _addr(experts),
+                                  _addr(dweights), _addr(dlogits), ldd, _stream(stream)), "mm_route_topk_grad")
+
+
+def mm_spread_rows(T, k, row_bytes, X, ldx, rows, total, Y, ldy, stream=None):
+    """Y[rows[t][j]] = X[t], rows of bytes. Raises MMError."""
+    lib = load()
+    _check(lib.mm_spread_rows(T, k, row_bytes, _addr(X), ldx, _addr(rows), total, _addr(Y), ldy, _stream(stream)),
+           "mm_spread_rows")
+
+
+def mm_combine_rows(T, k, D, Y, y_type, ldy, total, rows, weights, C, c_type, ldc, stream=None):
+    """C[t] = sum over j of weights[t][j] Y[rows[t][j]]. Raises MMError."""
+    lib = load()
+    _check(lib.mm_combine_rows(T, k, D, _addr(Y), y_type, ldy, total, _addr(rows), _addr(weights), _addr(C), c_type,
+                               ldc, _stream(stream)), "mm_combine_rows")
+
+
+def mm_combine_rows_grad(T, k, D, G, g_type, ldg, Y, y_type, ldy, total, rows, weights, dY, lddy, dweights,
+                         stream=None):
+    """Gradients of mm_combine_rows with respect to Y and the weights. Raises MMError."""
+    lib = load()
+    _check(lib.mm_combine_rows_grad(T, k, D, _addr(G), g_type, ldg, _addr(Y), y_type, ldy, total, _addr(rows),
+                                    _addr(weights), _addr(dY), lddy, _addr(dweights), _stream(stream)),
+           "mm_combine_rows_grad")
+
+
 def mm_gemm_grouped_num_configs():
-    """Number of kernels of the grouped and the 8-bit products."""
+    """Number of kernels of the grouped, the 8-bit and the 4-bit products."""
     return load().mm_gemm_grouped_num_configs()
 
 
 def mm_gemm_grouped_config_name(cfg):
-    """Name of kernel `cfg` of the grouped and the 8-bit products, None outside the table."""
+    """Name of kernel `cfg` of the grouped, the 8-bit and the 4-bit products, None outside the
+    table."""
     name = load().mm_gemm_grouped_config_name(cfg)
     return name.decode() if name is not None else None
 
@@ -423,6 +521,17 @@ def mm_gemm_i8_select(M, N, K, A, lda, B, ldb):
 def mm_gemm_i8_grouped_select(groups, M, N, K, A, lda, B, ldb, stride_b):
     """Kernel that mm_gemm_i8_grouped runs (-1: none)."""
     return load().mm_gemm_i8_grouped_select(groups, M, N, K, _addr(A), lda, _addr(B), ldb, stride_b)
+
+
+def mm_gemm_mx4_select(M, N, K, A, lda, a_scale, ld_as, B, ldb, b_scale, ld_bs):
+    """Kernel that mm_gemm_mx4 runs (-1: none)."""
+    return load().mm_gemm_mx4_select(M, N, K, _addr(A), lda, _addr(a_scale), ld_as, _addr(B), ldb, _addr(b_scale), ld_bs)
+
+
+def mm_gemm_mx4_grouped_select(groups, M, N, K, A, lda, a_scale, ld_as, B, ldb, stride_b, b_scale, ld_bs, stride_bs):
+    """Kernel that mm_gemm_mx4_grouped runs (-1: none)."""
+    return load().mm_gemm_mx4_grouped_select(groups, M, N, K, _addr(A), lda, _addr(a_scale), ld_as, _addr(B), ldb,
+                                             stride_b, _addr(b_scale), ld_bs, stride_bs)
 
 
 def mm_status_string(status):
@@ -880,3 +989,284 @@ def gemm_i8_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, s
     _run("mm_gemm_i8_grouped", device, stream, groups, M, N, K, offsets.data_ptr(), A.data_ptr(), lda,
          a_scale.data_ptr(), B.data_ptr(), ldb, stride_b, b_scale.data_ptr(), out.data_ptr(), c_type, ldc)
     return out
+
+
+def _bytes_matrix(t, shape, name, device):
+    """Leading dimension of a uint8 matrix of the given shape."""
+    import torch
+    ld = _matrix(t, name, (torch.uint8,))
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    _same_device(t, name, device)
+    return ld
+
+
+def quantize_mx4(x, out=None, scale=None, stream=None):
+    """(q, scale): the rows of x (float32, bfloat16 or float16) in 4-bit floating point (values 0, 0.5,
+    1, 1.5, 2, 3, 4 and 6 with a sign) and blocks of 32 along the row with a power of two each. q is
+    uint8, rows x 16 ceil(cols / 32), two elements to a byte, the even one low (the last block filled
+    up with zeros); scale is uint8, rows x ceil(cols / 32), the exponent + 127. An element is x / 2^e
+    rounded to the nearest value, halves to the even code, e = floor(log2 max |x|) - 2 in its block."""
+    import torch
+    ldx = _matrix(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    device = x.get_device()
+    rows, cols = x.shape
+    blocks = (cols + 31) // 32
+    if out is None:
+        out, ldq = x.new_empty((rows, 16 * blocks), dtype=torch.uint8), max(16 * blocks, 1)
+    else:
+        ldq = _bytes_matrix(out, (rows, 16 * blocks), "out", device)
+    if scale is None:
+        scale, lds = x.new_empty((rows, blocks), dtype=torch.uint8), max(blocks, 1)
+    else:
+        lds = _bytes_matrix(scale, (rows, blocks), "scale", device)
+    _run("mm_quantize_mx4", device, stream, rows, cols, x.data_ptr(), _mm_type(x.dtype, "x"), ldx, out.data_ptr(), ldq,
+         scale.data_ptr(), lds)
+    return out, scale
+
+
+def dequantize_mx4(q, scale, cols=None, out=None, out_dtype=None, stream=None):
+    """The values that quantize_mx4's codes and scales stand for: rows x cols (all elements of the
+    blocks by default) of out_dtype, float32 (default), bfloat16 (both exact) or float16."""
+    import torch
+    ldq = _matrix(q, "q", (torch.uint8,))
+    device = q.get_device()
+    rows, width = q.shape
+    if width % 16:
+        raise ValueError(f"q has rows of {width} bytes, no multiple of 16")
+    if cols is None:
+        cols = 2 * width
+    if (cols + 31) // 32 * 16 != width:
+        raise ValueError(f"{cols} columns do not fit rows of {width // 16} blocks")
+    lds = _bytes_matrix(scale, (rows, width // 16), "scale", device)
+    out, x_type, ldx, _ = _output(out, out_dtype, (rows, cols), q)
+    _run("mm_dequantize_mx4", device, stream, rows, cols, q.data_ptr(), ldq, scale.data_ptr(), lds, out.data_ptr(),
+         x_type, ldx)
+    return out
+
+
+def gemm_mx4(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
+    """out[i][j] = sum_k a[i][k] b[j][k] of the values of quantize_mx4's codes A (M x K / 2 bytes) and B
+    (N x K / 2) with scales M x K / 32 and N x K / 32, all uint8, any row strides; out float32
+    (default), bfloat16 or float16."""
+    import torch
+    lda = _matrix(A, "A", (torch.uint8,))
+    ldb = _matrix(B, "B", (torch.uint8,))
+    device = A.get_device()
+    M, K = A.shape
+    N, K2 = B.shape
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
+    if K % 16:
+        raise ValueError(f"rows of {K} bytes, no multiple of 16")
+    _same_device(B, "B", device)
+    ld_as = _bytes_matrix(a_scale, (M, K // 16), "a_scale", device)
+    ld_bs = _bytes_matrix(b_scale, (N, K // 16), "b_scale", device)
+    out, c_type, ldc, _ = _output(out, out_dtype, (M, N), A)
+    _run("mm_gemm_mx4", device, stream, M, N, 2 * K, A.data_ptr(), lda, a_scale.data_ptr(), ld_as, B.data_ptr(), ldb,
+         b_scale.data_ptr(), ld_bs, out.data_ptr(), c_type, ldc)
+    return out
+
+
+def gemm_mx4_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, stream=None):
+    """gemm_mx4 with rows grouped by expert: B groups x N x K / 2, b_scale groups x N x K / 32, offsets as
+    for gemm16_grouped (and as route_topk returns them); rows of no group are left as they are."""
+    import torch
+    lda = _matrix(A, "A", (torch.uint8,))
+    ldb, stride_b = _stack(B, "B", (torch.uint8,))
+    device = A.get_device()
+    M, K = A.shape
+    groups, N, K2 = B.shape
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)} transposed")
+    if K % 16:
+        raise ValueError(f"rows of {K} bytes, no multiple of 16")
+    _same_device(B, "B", device)
+    _offsets(offsets, groups, device)
+    ld_as = _bytes_matrix(a_scale, (M, K // 16), "a_scale", device)
+    ld_bs, stride_bs = _stack(b_scale, "b_scale", (torch.uint8,))
+    if b_scale.shape != (groups, N, K // 16):
+        raise ValueError(f"b_scale has shape {tuple(b_scale.shape)}, expected {(groups, N, K // 16)}")
+    _same_device(b_scale, "b_scale", device)
+    out, c_type, ldc, _ = _output(out, out_dtype, (M, N), A)
+    _run("mm_gemm_mx4_grouped", device, stream, groups, M, N, 2 * K, offsets.data_ptr(), A.data_ptr(), lda,
+         a_scale.data_ptr(), ld_as, B.data_ptr(), ldb, stride_b, b_scale.data_ptr(), ld_bs, stride_bs, out.data_ptr(),
+         c_type, ldc)
+    return out
+
+
+def _scoring(name):
+    if name == "softmax":
+        return MM_ROUTE_SOFTMAX
+    if name == "sigmoid":
+        return MM_ROUTE_SIGMOID
+    raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {name!r}")
+
+
+def _slots(t, shape, dtype, name, device):
+    """Check a packed tensor with an entry for each slot of each token."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
+    _same_device(t, name, device)
+
+
+def _allocating_for(stream, device):
+    """A context whose allocations belong to `stream`, so that what is freed while work on that stream
+    still uses it is handed out again on that stream only."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        address = _stream(stream)
+        stream = torch.cuda.ExternalStream(address, device=device) if address else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def route_topk_workspace(T, E, k, device):
+    """A device buffer of the size mm_route_topk needs for (T, E, k) (None if none)."""
+    import torch
+    n = mm_route_topk_workspace_bytes(T, E, k)
+    if n < 0:
+        raise ValueError(f"invalid sizes: {T} tokens, {k} of {E} experts")
+    return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def route_topk(logits, k, scoring="softmax", bias=None, groups=1, top_groups=1, group_top=1, renormalize=False,
+               scale=1.0, workspace=None, stream=None):
+    """(weights, experts, rows, offsets): the k best of E experts for each row of logits (T x E; float32,
+    bfloat16 or float16), and the order of their rows. Scores are the softmax or the sigmoid of the
+    logits; experts are chosen by score + bias (float32, E entries), with groups > 1 among the
+    top_groups groups of E / groups neighbours whose group_top (1 or 2) best add up highest; equal ones
+    by the lower index. weights (T x k, float32) are the chosen scores times scale, with renormalize
+    divided by their sum. experts (T x k, int32) holds -1 where none is left (logits of -inf are never
+    chosen: give padded tokens only those). rows (T x k, int32) numbers the slots by expert, token and
+    slot, -1 without an expert, and offsets (E + 1, int64) says where each expert's rows begin, as the
+    grouped products take it. workspace: a device tensor of mm_route_topk_workspace_bytes bytes (e.g.
+    from route_topk_workspace); allocated for the call if not given."""
+    import torch
+    ld = _matrix(logits, "logits", (torch.float32, torch.bfloat16, torch.float16))
+    device = logits.get_device()
+    T, E = logits.shape
+    how = _scoring(scoring)
+    if bias is not None:
+        _scale(bias, (E,), "bias", device)
+    need = mm_route_topk_workspace_bytes(T, E, k)
+    if need < 0:
+        raise ValueError(f"invalid sizes: {T} tokens, {k} of {E} experts")
+    if workspace is not None:
+        size = _workspace_bytes(workspace, logits.device)
+    elif need > 0:
+        with _allocating_for(stream, logits.device):
+            workspace, size = logits.new_empty(need, dtype=torch.uint8), need
+    else:
+        size = 0
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    experts = logits.new_empty((T, k), dtype=torch.int32)
+    rows = logits.new_empty((T, k), dtype=torch.int32)
+    offsets = logits.new_empty(E + 1, dtype=torch.int64)
+    _run("mm_route_topk", device, stream, T, E, k, logits.data_ptr(), _mm_type(logits.dtype, "logits"), ld, how,
+         None if bias is None else bias.data_ptr(), groups, top_groups, group_top, 1 if renormalize else 0, scale,
+         weights.data_ptr(), experts.data_ptr(), rows.data_ptr(), offsets.data_ptr(),
+         None if workspace is None else workspace.data_ptr(), size)
+    return weights, experts, rows, offsets
+
+
+def route_topk_grad(logits, experts, dweights, scoring="softmax", renormalize=False, scale=1.0, out=None, stream=None):
+    """The gradient of route_topk's weights with respect to the logits, T x E of the logits' dtype, from
+    dweights (T x k, float32) and the experts that route_topk returned."""
+    import torch
+    ld = _matrix(logits, "logits", (torch.float32, torch.bfloat16, torch.float16))
+    device = logits.get_device()
+    T, E = logits.shape
+    how = _scoring(scoring)
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+        raise TypeError("experts must be a 2-D tensor")
+    k = experts.shape[1]
+    _slots(experts, (T, k), torch.int32, "experts", device)
+    _slots(dweights, (T, k), torch.float32, "dweights", device)
+    out, _, ldd, _ = _output(out, logits.dtype, (T, E), logits)
+    _run("mm_route_topk_grad", device, stream, T, E, k, logits.data_ptr(), _mm_type(logits.dtype, "logits"), ld, how,
+         1 if renormalize else 0, scale, experts.data_ptr(), dweights.data_ptr(), out.data_ptr(), ldd)
+    return out
+
+
+def _token_slots(rows):
+    """(T, k) of a router's rows."""
+    import torch
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
+        raise TypeError("rows must be a 2-D tensor")
+    return rows.shape
+
+
+def spread_rows(x, rows, out=None, stream=None):
+    """out[rows[t][j]] = x[t]: the tokens' rows in the experts' order. x is T x D of any of float32,
+    bfloat16, float16, int8 and uint8, rows T x k int32 as route_topk returns it; entries outside out's
+    rows are none. out has T k rows if it is not given; those that nothing names are left as they are
+    (uninitialised if out was not given). The gradient is combine_rows without weights."""
+    import torch
+    dtypes = (torch.float32, torch.bfloat16, torch.float16, torch.int8, torch.uint8)
+    ldx = _matrix(x, "x", dtypes)
+    device = x.get_device()
+    T, k = _token_slots(rows)
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows, rows {T}")
+    _slots(rows, (T, k), torch.int32, "rows", device)
+    D, size = x.shape[1], x.element_size()
+    if out is None:
+        out, ldo = x.new_empty((T * k, D)), max(D, 1)
+    else:
+        ldo = _matrix(out, "out", (x.dtype,))
+        if out.shape[1] != D:
+            raise ValueError(f"out has {out.shape[1]} columns, x {D}")
+        _same_device(out, "out", device)
+    _run("mm_spread_rows", device, stream, T, k, D * size, x.data_ptr(), ldx * size, rows.data_ptr(), out.shape[0],
+         out.data_ptr(), ldo * size)
+    return out
+
+
+def combine_rows(y, rows, weights=None, out=None, out_dtype=None, stream=None):
+    """out[t] = sum_j weights[t][j] y[rows[t][j]]: the experts' outputs y (float32, bfloat16 or float16)
+    back to the tokens. rows T x k int32 as route_topk returns it (entries outside y's rows add
+    nothing), weights T x k float32 or None for the plain sum; out T x D, float32 (default), bfloat16 or
+    float16."""
+    import torch
+    ldy = _matrix(y, "y", (torch.float32, torch.bfloat16, torch.float16))
+    device = y.get_device()
+    T, k = _token_slots(rows)
+    _slots(rows, (T, k), torch.int32, "rows", device)
+    if weights is not None:
+        _slots(weights, (T, k), torch.float32, "weights", device)
+    total, D = y.shape
+    out, c_type, ldc, _ = _output(out, out_dtype, (T, D), y)
+    _run("mm_combine_rows", device, stream, T, k, D, y.data_ptr(), _mm_type(y.dtype, "y"), ldy, total, rows.data_ptr(),
+         None if weights is None else weights.data_ptr(), out.data_ptr(), c_type, ldc)
+    return out
+
+
+def combine_rows_grad(dout, y, rows, weights, out=None, stream=None):
+    """(dy, dweights): the gradients of combine_rows(y, rows, weights) from that of its output (T x D,
+    float32, bfloat16 or float16): dy[rows[t][j]] = weights[t][j] dout[t], of y's shape and dtype (out
+    if given), rows that nothing names left as they are (uninitialised if out was not given);
+    dweights[t][j] = <y[rows[t][j]], dout[t]>, float32."""
+    import torch
+    types = (torch.float32, torch.bfloat16, torch.float16)
+    ldg = _matrix(dout, "dout", types)
+    ldy = _matrix(y, "y", types)
+    device = y.get_device()
+    _same_device(dout, "dout", device)
+    T, k = _token_slots(rows)
+    total, D = y.shape
+    if dout.shape != (T, D):
+        raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(T, D)}")
+    _slots(rows, (T, k), torch.int32, "rows", device)
+    _slots(weights, (T, k), torch.float32, "weights", device)
+    out, _, lddy, _ = _output(out, y.dtype, (total, D), y)
+    dweights = y.new_empty((T, k), dtype=torch.float32)
+    _run("mm_combine_rows_grad", device, stream, T, k, D, dout.data_ptr(), _mm_type(dout.dtype, "dout"), ldg,
+         y.data_ptr(), _mm_type(y.dtype, "y"), ldy, total, rows.data_ptr(), weights.data_ptr(), out.data_ptr(), lddy,
+         dweights.data_ptr())
+    return out, dweights

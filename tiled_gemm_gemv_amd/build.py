@@ -19,7 +19,7 @@ SOURCES = ["mm_api.hip", "mm_gemm.hip", "mm_gemm_direct.hip", "mm_gemm_skinny.hi
            "mm_conv.hip",
            "mm_gemv.hip", "mm_gemv_t.hip", "mm_static_ws.hip",
            "mm_group_any.hip", "mm_group_tile.hip", "mm_group_rows.hip",
-           "mm_quantize.hip"]
+           "mm_quantize.hip", "mm_mx4.hip", "mm_route.hip", "mm_expert_rows.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -269,9 +269,10 @@ int check_group(const mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, in
     // and C_g is K x N
     const int64_t b_rows = a.grad ? M : a.trans_b ? N : K, b_cols = a.grad ? N : a.trans_b ? K : N;
     const int64_t c_rows = a.grad ? K : M, b_count = a.grad ? 1 : groups, c_count = a.grad ? groups : 1;
-    if (a.lda < (K > 1 ? K : 1)) return invalid("lda < max(1, K)");
+    const bool mx4 = a.elem == mm::GroupElem::Mx4;  // K counts bytes
+    if (a.lda < (K > 1 ? K : 1)) return invalid(mx4 ? "lda < max(1, K / 2)" : "lda < max(1, K)");
     if (a.ldb < (b_cols > 1 ? b_cols : 1))
-        return invalid(a.grad ? "ldg < max(1, N)" : a.trans_b ? "ldb < max(1, K)" : "ldb < max(1, N)");
+        return invalid(mx4 ? "ldb < max(1, K / 2)" : a.grad ? "ldg < max(1, N)" : a.trans_b ? "ldb < max(1, K)" : "ldb < max(1, N)");
     if (a.ldc < (N > 1 ? N : 1)) return invalid(a.grad ? "ldd < max(1, N)" : "ldc < max(1, N)");
     if (a.stride_b < 0 || a.stride_c < 0) return invalid("negative group stride");
     if (groups == 0) return MM_OK;  // no rows belong to a group: pointers may be NULL
@@ -280,7 +281,7 @@ int check_group(const mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, in
     if (has_b && !a.B) return invalid(a.grad ? "G is NULL" : "B is NULL");
     if (has_c && !a.C) return invalid(a.grad ? "D is NULL" : "C is NULL");
     if (!dense && !a.offsets) return invalid("offsets is NULL");
-    const int elem = i8 ? 1 : 2;
+    const int elem = mm::group_elem_size(a);
     if ((uintptr_t)a.A % elem || (uintptr_t)a.B % elem || (uintptr_t)a.C % type_size(a.c_type))
         return invalid("pointer not aligned to its element size");
     if ((uintptr_t)a.offsets % 8) return invalid("offsets not 8-byte aligned");
@@ -306,7 +307,7 @@ int run_group(mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, int64_t K,
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
-    return from_hip(a.grad ? "grouped gradient launch" : dense ? "i8 gemm launch" : "grouped gemm launch",
+    return from_hip(a.grad ? "grouped gradient launch" : !dense ? "grouped gemm launch" : a.elem == mm::GroupElem::I8 ? "i8 gemm launch" : "mx4 gemm launch",
                     mm::group_launch(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -367,6 +368,107 @@ int run_grouped16_grad_b(mm::GroupElem elem, int64_t groups, int64_t M, int64_t 
     a.stride_c = stride_d;
     a.c_type = d_type;
     return run_group(a, groups, M, N, K, false, stream);
+}
+
+// The 4-bit products: the public K counts elements, the kernels' bytes of two of them.
+int check_mx4(mm::GroupArgs &a, int64_t groups, int64_t M, int64_t N, int64_t K)
+{
+    if (K % 32) return invalid("K is no multiple of 32");
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim || groups < 0 || groups > kMaxGroups)
+        return MM_OK;  // check_group names these
+    const int64_t blocks = K / 32, least = blocks > 1 ? blocks : 1;
+    if (a.ld_mxa < least) return invalid("ld of a_scale < max(1, K / 32)");
+    if (a.ld_mxb < least) return invalid("ld of b_scale < max(1, K / 32)");
+    if (a.stride_mxb < 0) return invalid("negative group stride");
+    if (groups == 0 || K == 0) return MM_OK;
+    if (M > 0 && !a.mxa) return invalid("a_scale is NULL");
+    if (N > 0 && !a.mxb) return invalid("b_scale is NULL");
+    if (M > 0 && !extent_fits(M, blocks, a.ld_mxa)) return invalid("a_scale extent overflows");
+    if (N > 0 && !strided_extent_fits(groups, a.stride_mxb, N, blocks, a.ld_mxb))
+        return invalid("b_scale extent overflows");
+    return MM_OK;
+}
+
+mm::GroupArgs mx4_args(const int64_t *offsets, const uint8_t *A, int64_t lda, const uint8_t *a_scale, int64_t ld_as,
+                       const uint8_t *B, int64_t ldb, int64_t stride_b, const uint8_t *b_scale, int64_t ld_bs,
+                       int64_t stride_bs, void *C, int c_type, int64_t ldc)
+{
+    mm::GroupArgs a{};
+    a.elem = mm::GroupElem::Mx4;
+    a.trans_b = true;
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.offsets = offsets;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.stride_b = stride_b;
+    a.c_type = c_type;
+    a.mxa = a_scale;
+    a.mxb = b_scale;
+    a.ld_mxa = ld_as;
+    a.ld_mxb = ld_bs;
+    a.stride_mxb = stride_bs;
+    return a;
+}
+
+// Rows of 4-bit blocks: the sizes and addresses that both directions check.
+int check_mx4_rows(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx, const uint8_t *Q, int64_t ldq,
+                   const uint8_t *scale, int64_t ld_scale)
+{
+    if (rows < 0 || cols < 0) return invalid("negative size");
+    if (rows > kMaxDim || cols > kMaxDim) return invalid("size above 2^31 - 1");
+    if (!type_ok(x_type)) return invalid("unknown type of X");
+    const int64_t blocks = (cols + 31) / 32;
+    if (ldx < (cols > 1 ? cols : 1)) return invalid("ldx < max(1, cols)");
+    if (ldq < (blocks > 0 ? 16 * blocks : 1)) return invalid("ldq < max(1, 16 ceil(cols / 32))");
+    if (ld_scale < (blocks > 0 ? blocks : 1)) return invalid("ld_scale < max(1, ceil(cols / 32))");
+    if (rows == 0 || cols == 0) return MM_OK;
+    if (!X) return invalid("X is NULL");
+    if (!Q) return invalid("Q is NULL");
+    if (!scale) return invalid("scale is NULL");
+    if ((uintptr_t)X % type_size(x_type)) return invalid("pointer not aligned to its element size");
+    if (!extent_fits(rows, cols, ldx) || !extent_fits(rows, 16 * blocks, ldq) || !extent_fits(rows, blocks, ld_scale))
+        return invalid("extent overflows");
+    return MM_OK;
+}
+
+int check_route(int64_t T, int64_t E, int64_t k, const void *logits, int type, int64_t ld, int scoring, int renormalize)
+{
+    if (T < 0 || E < 0 || k < 0) return invalid("negative size");
+    if (E > mm::kRouteMaxExperts) return invalid("more than 1024 experts");
+    if (k > mm::kRouteMaxTop) return invalid("more than 32 experts to a token");
+    if (k > E) return invalid("more experts to a token than there are");
+    if (T > kMaxDim || (k > 0 && T > kMaxDim / k)) return invalid("T k above 2^31 - 1");
+    if (!type_ok(type)) return invalid("unknown type of the logits");
+    if (scoring != MM_ROUTE_SOFTMAX && scoring != MM_ROUTE_SIGMOID) return invalid("unknown scoring");
+    if (renormalize != 0 && renormalize != 1) return invalid("renormalize is neither 0 nor 1");
+    if (ld < (E > 1 ? E : 1)) return invalid("ld < max(1, E)");
+    if (T > 0 && E > 0 && !logits) return invalid("logits is NULL");
+    if ((uintptr_t)logits % type_size(type)) return invalid("pointer not aligned to its element size");
+    if (T > 0 && E > 0 && !extent_fits(T, E, ld)) return invalid("logits extent overflows");
+    return MM_OK;
+}
+
+// A matrix of `rows` x `cols` elements of `size` bytes that is used where it has elements.
+int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int size, const char *null, const char *extent)
+{
+    if (rows == 0 || cols == 0) return MM_OK;
+    if (!p) return invalid(null);
+    if ((uintptr_t)p % size) return invalid("pointer not aligned to its element size");
+    if (!extent_fits(rows, cols, ld)) return invalid(extent);
+    return MM_OK;
+}
+
+int check_rows(int64_t T, int64_t k, int64_t D, int64_t total, const int32_t *rows)
+{
+    if (T < 0 || k < 0 || D < 0 || total < 0) return invalid("negative size");
+    if (T > kMaxDim || D > kMaxDim || total > kMaxDim) return invalid("size above 2^31 - 1");
+    if (k > kMaxDim || (k > 0 && T > kMaxDim / k)) return invalid("T k above 2^31 - 1");
+    if (T > 0 && k > 0 && !rows) return invalid("rows is NULL");
+    if ((uintptr_t)rows % 4) return invalid("rows not 4-byte aligned");
+    return MM_OK;
 }
 
 }  // namespace
@@ -713,6 +815,225 @@ int mm_gemm_i8_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const in
     return run_group(a, groups, M, N, K, false, stream);
 }
 
+int mm_quantize_mx4(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx, uint8_t *Q, int64_t ldq,
+                    uint8_t *scale, int64_t ld_scale, void *stream)
+{
+    const int st = check_mx4_rows(rows, cols, X, x_type, ldx, Q, ldq, scale, ld_scale);
+    if (st != MM_OK || rows == 0 || cols == 0) return st;
+    const mm::Mx4Args a{const_cast<void *>(X), Q, scale, rows, cols, ldx, ldq, ld_scale, x_type};
+    return from_hip("quantize launch", mm::mx4_quantize_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int mm_dequantize_mx4(int64_t rows, int64_t cols, const uint8_t *Q, int64_t ldq, const uint8_t *scale,
+                      int64_t ld_scale, void *X, int x_type, int64_t ldx, void *stream)
+{
+    const int st = check_mx4_rows(rows, cols, X, x_type, ldx, Q, ldq, scale, ld_scale);
+    if (st != MM_OK || rows == 0 || cols == 0) return st;
+    const mm::Mx4Args a{X, const_cast<uint8_t *>(Q), const_cast<uint8_t *>(scale), rows, cols, ldx, ldq, ld_scale, x_type};
+    return from_hip("dequantize launch", mm::mx4_dequantize_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int mm_gemm_mx4(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *a_scale, int64_t ld_as,
+                const uint8_t *B, int64_t ldb, const uint8_t *b_scale, int64_t ld_bs, void *C, int c_type, int64_t ldc,
+                void *stream)
+{
+    mm::GroupArgs a = mx4_args(nullptr, A, lda, a_scale, ld_as, B, ldb, 0, b_scale, ld_bs, 0, C, c_type, ldc);
+    const int st = check_mx4(a, 1, M, N, K);
+    return st != MM_OK ? st : run_group(a, 1, M, N, K / 2, true, stream);
+}
+
+int mm_gemm_mx4_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const int64_t *offsets, const uint8_t *A,
+                        int64_t lda, const uint8_t *a_scale, int64_t ld_as, const uint8_t *B, int64_t ldb,
+                        int64_t stride_b, const uint8_t *b_scale, int64_t ld_bs, int64_t stride_bs, void *C, int c_type,
+                        int64_t ldc, void *stream)
+{
+    mm::GroupArgs a =
+        mx4_args(offsets, A, lda, a_scale, ld_as, B, ldb, stride_b, b_scale, ld_bs, stride_bs, C, c_type, ldc);
+    const int st = check_mx4(a, groups, M, N, K);
+    return st != MM_OK ? st : run_group(a, groups, M, N, K / 2, false, stream);
+}
+
+int64_t mm_route_topk_workspace_bytes(int64_t T, int64_t E, int64_t k)
+{
+    if (T < 0 || E < 0 || k < 0 || E > mm::kRouteMaxExperts || k > mm::kRouteMaxTop || k > E || T > kMaxDim ||
+        (k > 0 && T > kMaxDim / k))
+        return -1;
+    return T == 0 || k == 0 ? 0 : 4 * mm::route_ws_ints(T, (int)E, (int)k);
+}
+
+int mm_route_topk(int64_t T, int64_t E, int64_t k, const void *logits, int type, int64_t ld, int scoring,
+                  const float *bias, int64_t groups, int64_t top_groups, int64_t group_top, int renormalize,
+                  float scale, float *weights, int32_t *experts, int32_t *rows, int64_t *offsets, void *workspace,
+                  int64_t workspace_bytes, void *stream)
+{
+    const int st = check_route(T, E, k, logits, type, ld, scoring, renormalize);
+    if (st != MM_OK) return st;
+    if (groups < 1 || groups > 64) return invalid("groups outside 1 .. 64");
+    if (E % groups) return invalid("E is no multiple of groups");
+    if (top_groups < 1 || top_groups > groups) return invalid("top_groups outside 1 .. groups");
+    if (group_top != 1 && group_top != 2) return invalid("group_top is neither 1 nor 2");
+    if (k > E / groups * top_groups) return invalid("more experts to a token than the kept groups have");
+    const bool any = T > 0 && k > 0;
+    if (any && !weights) return invalid("weights is NULL");
+    if (any && !experts) return invalid("experts is NULL");
+    if (any && !rows) return invalid("rows is NULL");
+    if (!offsets) return invalid("offsets is NULL");
+    if ((uintptr_t)offsets % 8) return invalid("offsets not 8-byte aligned");
+    if ((uintptr_t)bias % 4 || (uintptr_t)weights % 4 || (uintptr_t)experts % 4 || (uintptr_t)rows % 4)
+        return invalid("pointer not aligned to its element size");
+    const int64_t need = mm_route_topk_workspace_bytes(T, E, k);
+    if (need > 0) {
+        if (!workspace) return invalid("workspace is NULL");
+        if ((uintptr_t)workspace % 16) return invalid("workspace not 16-byte aligned");
+        if (workspace_bytes < need) return invalid("workspace smaller than mm_route_topk_workspace_bytes");
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    // no rows: every expert's begin at 0 (the fill counts words)
+    if (!any) return from_hip("zero fill launch", mm::zero_fill_launch(reinterpret_cast<float *>(offsets), 1, 2 * (E + 1), 2 * (E + 1), s));
+    mm::RouteArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.weights = weights;
+    a.experts = experts;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.ws = static_cast<int *>(workspace);
+    a.ld = ld;
+    a.T = (int)T;
+    a.E = (int)E;
+    a.k = (int)k;
+    a.groups = (int)groups;
+    a.top_groups = (int)top_groups;
+    a.group_top = (int)group_top;
+    a.type = type;
+    a.sigmoid = scoring == MM_ROUTE_SIGMOID;
+    a.renormalize = renormalize == 1;
+    a.scale = scale;
+    return from_hip("route launch", mm::route_launch(a, s));
+}
+
+int mm_route_topk_grad(int64_t T, int64_t E, int64_t k, const void *logits, int type, int64_t ld, int scoring,
+                       int renormalize, float scale, const int32_t *experts, const float *dweights, void *dlogits,
+                       int64_t ldd, void *stream)
+{
+    const int st = check_route(T, E, k, logits, type, ld, scoring, renormalize);
+    if (st != MM_OK) return st;
+    if (ldd < (E > 1 ? E : 1)) return invalid("ldd < max(1, E)");
+    const bool any = T > 0 && k > 0;
+    if (any && !experts) return invalid("experts is NULL");
+    if (any && !dweights) return invalid("dweights is NULL");
+    if ((uintptr_t)experts % 4 || (uintptr_t)dweights % 4) return invalid("pointer not aligned to its element size");
+    const int d = check_matrix(dlogits, T, E, ldd, type_size(type), "dlogits is NULL", "dlogits extent overflows");
+    if (d != MM_OK || T == 0 || E == 0) return d;
+    mm::RouteGradArgs a;
+    a.logits = logits;
+    a.experts = experts;
+    a.dweights = dweights;
+    a.dlogits = dlogits;
+    a.ld = ld;
+    a.ldd = ldd;
+    a.T = (int)T;
+    a.E = (int)E;
+    a.k = (int)k;
+    a.type = type;
+    a.sigmoid = scoring == MM_ROUTE_SIGMOID;
+    a.renormalize = renormalize == 1;
+    a.scale = scale;
+    return from_hip("route gradient launch", mm::route_grad_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int mm_spread_rows(int64_t T, int64_t k, int64_t row_bytes, const void *X, int64_t ldx, const int32_t *rows,
+                   int64_t total, void *Y, int64_t ldy, void *stream)
+{
+    int st = check_rows(T, k, row_bytes, total, rows);
+    if (st != MM_OK) return st;
+    if (ldx < (row_bytes > 1 ? row_bytes : 1)) return invalid("ldx < max(1, row_bytes)");
+    if (ldy < (row_bytes > 1 ? row_bytes : 1)) return invalid("ldy < max(1, row_bytes)");
+    const int64_t used = k > 0 && total > 0 ? T : 0;
+    if ((st = check_matrix(X, used, row_bytes, ldx, 1, "X is NULL", "X extent overflows")) != MM_OK) return st;
+    if ((st = check_matrix(Y, used > 0 ? total : 0, row_bytes, ldy, 1, "Y is NULL", "Y extent overflows")) != MM_OK) return st;
+    if (used == 0 || row_bytes == 0) return MM_OK;
+    mm::RowsArgs a{};
+    a.x = X;
+    a.out = Y;
+    a.rows = rows;
+    a.total = total;
+    a.ldx = ldx;
+    a.ldo = ldy;
+    a.T = (int)T;
+    a.k = (int)k;
+    a.D = (int)row_bytes;
+    return from_hip("spread rows launch", mm::spread_rows_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int mm_combine_rows(int64_t T, int64_t k, int64_t D, const void *Y, int y_type, int64_t ldy, int64_t total,
+                    const int32_t *rows, const float *weights, void *C, int c_type, int64_t ldc, void *stream)
+{
+    int st = check_rows(T, k, D, total, rows);
+    if (st != MM_OK) return st;
+    if (!type_ok(y_type)) return invalid("unknown input type");
+    if (!type_ok(c_type)) return invalid("unknown output type");
+    if (ldy < (D > 1 ? D : 1)) return invalid("ldy < max(1, D)");
+    if (ldc < (D > 1 ? D : 1)) return invalid("ldc < max(1, D)");
+    if ((uintptr_t)weights % 4) return invalid("pointer not aligned to its element size");
+    const int64_t used = T > 0 && k > 0 ? total : 0;
+    if ((st = check_matrix(Y, used, D, ldy, type_size(y_type), "Y is NULL", "Y extent overflows")) != MM_OK) return st;
+    if ((st = check_matrix(C, T, D, ldc, type_size(c_type), "C is NULL", "C extent overflows")) != MM_OK) return st;
+    if (T == 0 || D == 0) return MM_OK;
+    mm::RowsArgs a{};
+    a.x = Y;
+    a.out = C;
+    a.rows = rows;
+    a.weights = weights;
+    a.total = total;
+    a.ldx = ldy;
+    a.ldo = ldc;
+    a.T = (int)T;
+    a.k = (int)k;
+    a.D = (int)D;
+    a.x_type = y_type;
+    a.o_type = c_type;
+    return from_hip("combine rows launch", mm::combine_rows_launch(a, static_cast<hipStream_t>(stream)));
+}
+
+int mm_combine_rows_grad(int64_t T, int64_t k, int64_t D, const void *G, int g_type, int64_t ldg, const void *Y,
+                         int y_type, int64_t ldy, int64_t total, const int32_t *rows, const float *weights, void *dY,
+                         int64_t lddy, float *dweights, void *stream)
+{
+    int st = check_rows(T, k, D, total, rows);
+    if (st != MM_OK) return st;
+    if (!type_ok(g_type) || !type_ok(y_type)) return invalid("unknown input type");
+    if (ldg < (D > 1 ? D : 1)) return invalid("ldg < max(1, D)");
+    if (ldy < (D > 1 ? D : 1)) return invalid("ldy < max(1, D)");
+    if (lddy < (D > 1 ? D : 1)) return invalid("lddy < max(1, D)");
+    const bool any = T > 0 && k > 0;
+    if (any && !weights) return invalid("weights is NULL");
+    if (any && !dweights) return invalid("dweights is NULL");
+    if ((uintptr_t)weights % 4 || (uintptr_t)dweights % 4) return invalid("pointer not aligned to its element size");
+    const int ys = type_size(y_type);
+    if ((st = check_matrix(G, any ? T : 0, D, ldg, type_size(g_type), "G is NULL", "G extent overflows")) != MM_OK) return st;
+    if ((st = check_matrix(Y, any ? total : 0, D, ldy, ys, "Y is NULL", "Y extent overflows")) != MM_OK) return st;
+    if ((st = check_matrix(dY, any ? total : 0, D, lddy, ys, "dY is NULL", "dY extent overflows")) != MM_OK) return st;
+    if (!any) return MM_OK;
+    mm::RowsArgs a{};
+    a.x = G;
+    a.out = dY;
+    a.y = Y;
+    a.rows = rows;
+    a.weights = weights;
+    a.dweights = dweights;
+    a.total = total;
+    a.ldx = ldg;
+    a.ldo = lddy;
+    a.ldy = ldy;
+    a.T = (int)T;
+    a.k = (int)k;
+    a.D = (int)D;
+    a.x_type = g_type;
+    a.y_type = y_type;
+    return from_hip("combine rows gradient launch", mm::combine_rows_grad_launch(a, static_cast<hipStream_t>(stream)));
+}
+
 int mm_gemm_grouped_num_configs(void) { return mm::group_num_configs(); }
 const char *mm_gemm_grouped_config_name(int cfg) { return mm::group_config_name(cfg); }
 
@@ -769,6 +1090,22 @@ int mm_gemm_i8_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K, c
     a.stride_b = stride_b;
     a.stride_sb = N;
     return select_group(a, groups, M, N, K, false);
+}
+
+int mm_gemm_mx4_select(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *a_scale,
+                       int64_t ld_as, const uint8_t *B, int64_t ldb, const uint8_t *b_scale, int64_t ld_bs)
+{
+    mm::GroupArgs a = mx4_args(nullptr, A, lda, a_scale, ld_as, B, ldb, 0, b_scale, ld_bs, 0, nullptr, 0, 0);
+    return check_mx4(a, 1, M, N, K) != MM_OK ? -1 : select_group(a, 1, M, N, K / 2, true);
+}
+
+int mm_gemm_mx4_grouped_select(int64_t groups, int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda,
+                               const uint8_t *a_scale, int64_t ld_as, const uint8_t *B, int64_t ldb, int64_t stride_b,
+                               const uint8_t *b_scale, int64_t ld_bs, int64_t stride_bs)
+{
+    mm::GroupArgs a =
+        mx4_args(nullptr, A, lda, a_scale, ld_as, B, ldb, stride_b, b_scale, ld_bs, stride_bs, nullptr, 0, 0);
+    return check_mx4(a, groups, M, N, K) != MM_OK ? -1 : select_group(a, groups, M, N, K / 2, false);
 }
 
 const char *mm_status_string(int status)

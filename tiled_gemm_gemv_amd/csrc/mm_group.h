@@ -1,5 +1,5 @@
-// mm_group.h -- shared by the kernels of the grouped products and of the 8-bit integer
-// product (mm_group_tile.hip, mm_group_rows.hip, mm_group_any.hip): element types, loads of any
+// mm_group.h -- shared by the kernels of the grouped products and of the 8-bit integer and
+// 4-bit products (mm_group_tile.hip, mm_group_rows.hip, mm_group_any.hip): element types, loads of any
 // alignment, the map from a workgroup to a tile of a group, and what the host expects of group
 // sizes that it does not know.
 //
@@ -8,7 +8,8 @@
 //   rows mode      C[i][j] = s(i, j) sum over k < K of A[i][k] B_g(k, j)
 //                  s = 1 for 16-bit elements, sa[i] sb_g[j] for 8-bit integers;
 //                  B_g(k, j) = B[g stride_b + k ldb + j] or, "transposed",
-//                  B[g stride_b + j ldb + k]
+//                  B[g stride_b + j ldb + k]; 4-bit elements come in blocks of 32 along k
+//                  with a scale each, for A and B
 //   gradient mode  C_g[p][j] = sum over lo_g <= i < hi_g of A[i][p] B[i][j]
 //
 // The offsets live in device memory and no host code reads them: the grid covers the most
@@ -83,6 +84,31 @@ struct ElemI8 {
         else return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
     }
 };
+
+// 4-bit floating point in blocks of 32 along k with a power of two each: K counts bytes here, two
+// elements to a byte, so that a block is 16 bytes of k, one lane's part of an MFMA operand, and
+// everything that moves bytes is the 8-bit product's. The MFMA multiplies lane l's products by
+// 2^(x - 127) 2^(y - 127), x and y the scale bytes number SA and SB of that lane's words sa and sb
+// (255: NaN). Products are exact in fp32.
+struct ElemMx4 {
+    typedef unsigned char T;
+    static constexpr bool INT8 = false;
+    template <int B>
+    using Acc = BlockAcc<B, f32x4, f32x16>;
+    template <int B, int SA, int SB>
+    static __device__ __forceinline__ Acc<B> mma(u32x4 a, unsigned sa, u32x4 b, unsigned sb, Acc<B> c)
+    {
+        typedef int i32x8 __attribute__((ext_vector_type(8)));  // the builtin's operand; 4-bit formats take half of it
+        const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+        const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+        constexpr int fp4 = 4;  // the format's number
+        if constexpr (B == 32)
+            return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, fp4, fp4, SA, (int)sa, SB, (int)sb);
+        else return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, fp4, fp4, SA, (int)sa, SB, (int)sb);
+    }
+};
+template <class E>
+constexpr bool is_mx = std::is_same_v<E, ElemMx4>;
 
 // Output types (the public MM_TYPE_* values). fp32 sums are rounded once, to nearest even.
 template <int OUT>
@@ -245,14 +271,14 @@ inline double expected_row_tiles(const GroupArgs &a, int bm)
 }
 inline double expected_weight_bytes(const GroupArgs &a)
 {
-    return expected_groups(a) * a.N * (double)a.K * (a.elem == GroupElem::I8 ? 1 : 2);
+    return expected_groups(a) * a.N * (double)a.K * group_elem_size(a);
 }
 
 // Rows that start at 4-byte boundaries. Loads of others take about twice as long (measured on one
 // shape with K = 1531 and 1536: 50 and 22 us through the rows kernel, 25 and 17 in 128 x 128 tiles).
 inline bool aligned_words(const GroupArgs &a)
 {
-    const int es = a.elem == GroupElem::I8 ? 1 : 2;
+    const int es = group_elem_size(a);
     return (a.lda * es | a.ldb * es | a.stride_b * es | (int64_t)(uintptr_t)a.A | (int64_t)(uintptr_t)a.B) % 4 == 0;
 }
 

@@ -1,4 +1,4 @@
-// mm_group_any.hip -- the grouped products and the 8-bit integer product for any shape,
+// mm_group_any.hip -- the grouped products and the 8-bit integer and 4-bit products for any shape,
 // stride and alignment (see mm_group.h for the sums).
 //
 // One workgroup of 4 waves per 64 x 64 tile of C, each wave a 32 x 32 block. Per step the
@@ -81,7 +81,17 @@ __global__ __launch_bounds__(256) void group_any_kernel(GroupArgs p)
         for (int s = 0; s < kStepBytes / 32; ++s) {
             const char *a = lds + (wm + (lane & 31)) * kPitch + 32 * s + 16 * (lane >> 5);
             const char *b = lds + (kTile + wn + (lane & 31)) * kPitch + 32 * s + 16 * (lane >> 5);
-            acc = E::template mma<32>(*reinterpret_cast<const u32x4 *>(a), *reinterpret_cast<const u32x4 *>(b), acc);
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(a), y = *reinterpret_cast<const u32x4 *>(b);
+            if constexpr (is_mx<E>) {
+                const int64_t m = (int64_t)m0 + wm + (lane & 31), n = (int64_t)n0 + wn + (lane & 31);
+                const int64_t block = k0 / 16 + 2 * s + (lane >> 5);  // of zeros from K on: scale 1
+                const bool inside = 16 * block < k_end;
+                const unsigned sa = inside && m < m_end ? p.mxa[m * p.ld_mxa + block] : 127u;
+                const unsigned sb = inside && n < p.N ? p.mxb[g * p.stride_mxb + n * p.ld_mxb + block] : 127u;
+                acc = E::template mma<32, 0, 0>(x, sa, y, sb, acc);
+            } else {
+                acc = E::template mma<32>(x, y, acc);
+            }
         }
         __syncthreads();
     }
@@ -127,6 +137,7 @@ hipError_t group_any_launch(const GroupArgs &a, hipStream_t stream)
         return a.elem == GroupElem::F16 ? launch_any<ElemF16, true, true>(a, stream)
                                         : launch_any<ElemBf16, true, true>(a, stream);
     if (a.elem == GroupElem::I8) return launch_any<ElemI8, false, false>(a, stream);
+    if (a.elem == GroupElem::Mx4) return launch_any<ElemMx4, false, false>(a, stream);
     if (a.elem == GroupElem::F16)
         return a.trans_b ? launch_any<ElemF16, false, false>(a, stream) : launch_any<ElemF16, false, true>(a, stream);
     return a.trans_b ? launch_any<ElemBf16, false, false>(a, stream) : launch_any<ElemBf16, false, true>(a, stream);
@@ -166,6 +177,7 @@ int group_select(const GroupArgs &a)
 {
     int best = kAny;
     double time = 1e300;
+    if (a.elem == GroupElem::Mx4) return kAny;
     constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
     if (a.M > largest || a.N > largest || a.K > largest) return kAny;
     if (!a.grad)

@@ -144,9 +144,9 @@ int gemm16_select_config(int64_t M, int64_t N, int64_t K);
 hipError_t gemm16_launch(int cfg, bool bf16, const void *A, int64_t lda, const void *B, int64_t ldb,
                          float *C, int64_t ldc, int M, int N, int K, hipStream_t stream);
 
-// Grouped products and the 8-bit integer product (mm_group.h has the sums). Sizes and
+// Grouped products and the 8-bit integer and 4-bit products (mm_group.h has the sums). Sizes and
 // pointers are validated on the host; offsets (device memory) are not.
-enum class GroupElem { Bf16, F16, I8 };
+enum class GroupElem { Bf16, F16, I8, Mx4 };
 struct GroupArgs {
     const void *A;
     const void *B;
@@ -158,9 +158,17 @@ struct GroupArgs {
     int groups, M, N, K;       // gradient mode: C_g is K x N, the sum runs over the rows
     int c_type;                // MM_TYPE_*
     GroupElem elem;
-    bool trans_b;              // B_g stored N x K (always so for I8)
+    bool trans_b;              // B_g stored N x K (always so for I8 and Mx4)
     bool grad;                 // gradient mode
+    // Mx4: K, lda, ldb and stride_b count bytes of two elements, K a multiple of 16; the scales of
+    // A's and B's blocks of 16 bytes, K / 16 to a row
+    const unsigned char *mxa, *mxb;
+    int64_t ld_mxa, ld_mxb, stride_mxb;
 };
+inline int group_elem_size(const GroupArgs &a)
+{
+    return a.elem == GroupElem::I8 || a.elem == GroupElem::Mx4 ? 1 : 2;
+}
 // The kernel for the shape; M, N, groups >= 1 (gradient mode: K, N, groups >= 1). It depends on the
 // sizes, strides, types and addresses of A and B only.
 int group_num_configs();
@@ -192,6 +200,62 @@ struct QuantArgs {
     int x_type;                // MM_TYPE_*
 };
 hipError_t quantize_launch(const QuantArgs &a, hipStream_t stream);
+
+// Rows to 4-bit elements in blocks of 32 with a scale each, and back (mm_mx4.hip); rows, cols >= 1.
+struct Mx4Args {
+    void *X;                   // read by mx4_quantize_launch, written by mx4_dequantize_launch
+    unsigned char *Q, *scale;
+    int64_t rows, cols, ldx, ldq, lds;
+    int x_type;                // MM_TYPE_*
+};
+hipError_t mx4_quantize_launch(const Mx4Args &a, hipStream_t stream);
+hipError_t mx4_dequantize_launch(const Mx4Args &a, hipStream_t stream);
+
+// Routing of tokens to experts and its gradient (mm_route.hip); T, E >= 1, k in 1 .. kRouteMaxTop.
+constexpr int kRouteMaxExperts = 1024, kRouteMaxTop = 32;
+struct RouteArgs {
+    const void *logits;        // T x E of type, leading dimension ld
+    const float *bias;         // E, or nullptr
+    float *weights;            // T x k
+    int *experts, *rows;       // T x k
+    int64_t *offsets;          // E + 1
+    int *ws;                   // route_ws_ints(T, E, k) ints
+    int64_t ld;
+    int T, E, k, groups, top_groups, group_top;
+    int type;                  // MM_TYPE_*
+    bool sigmoid, renormalize;
+    float scale;
+};
+int64_t route_ws_ints(int64_t T, int E, int k);
+hipError_t route_launch(const RouteArgs &a, hipStream_t stream);
+struct RouteGradArgs {
+    const void *logits;        // T x E of type, leading dimension ld
+    const int *experts;        // T x k
+    const float *dweights;     // T x k
+    void *dlogits;             // T x E of type, leading dimension ldd
+    int64_t ld, ldd;
+    int T, E, k;
+    int type;
+    bool sigmoid, renormalize;
+    float scale;
+};
+hipError_t route_grad_launch(const RouteGradArgs &a, hipStream_t stream);
+
+// Tokens' rows to the experts' order and back (mm_expert_rows.hip); T, k, D >= 1.
+struct RowsArgs {
+    const void *x;             // spread: T x D; combine: total x D; gradient: T x D (of the output)
+    void *out;                 // spread: total x D; combine: T x D; gradient: total x D
+    const void *y;             // gradient: total x D
+    const int *rows;           // T x k
+    const float *weights;      // T x k, or nullptr
+    float *dweights;           // gradient: T x k
+    int64_t total, ldx, ldo, ldy;
+    int T, k, D;               // spread: D in bytes
+    int x_type, o_type, y_type;
+};
+hipError_t spread_rows_launch(const RowsArgs &a, hipStream_t stream);
+hipError_t combine_rows_launch(const RowsArgs &a, hipStream_t stream);
+hipError_t combine_rows_grad_launch(const RowsArgs &a, hipStream_t stream);
 
 // A 2-D convolution (mm_conv.hip): x is N x C x H x W, w is K x C x R x S, y is
 // N x K x P x Q, all packed; strides sh, sw, padding ph, pw, dilation dh, dw.
