@@ -76,12 +76,21 @@ struct GroupTile {
     static constexpr int ES = sizeof(typename E::T), BK = 128 / ES;
     static constexpr int A_HALF = RH * 128, B_HALF = CH * 128;  // bytes of a half panel
     static constexpr int STAGE = 2 * (A_HALF + B_HALF);
+    // Mx4: the scales of two K-steps, 16 bytes of every row of B and A, come in one load per wave and lane,
+    // with the first half panel of the even one. (8 bytes for each K-step: every 128-byte line of them
+    // read twice as often, which took i8's 233 us for the same bytes of k to 373.)
+    static constexpr bool MX = is_mx<E>;
+    static constexpr int SC_PAIR = MX ? 16 * (BN + BM) : 0;  // bytes of LDS, two of them
+    static constexpr int SC_SEGMENTS = (BN + BM) / 64;       // 64 rows each
+    static_assert(!MX || SC_SEGMENTS <= WAVES, "one load brings all rows' scales");
+    static constexpr int SAW = FM > 2 ? 2 : 1;  // words of the scales of a half's blocks of A; of B: one
+    static constexpr int GROUP_LDS = 2 * (STAGE + SC_PAIR);  // of a group of waves
     static constexpr int A_LD = A_HALF / 1024 / WAVES, B_LD = B_HALF / 1024 / WAVES;  // 1 KB loads per wave
     // offsets of the half panels in a stage
     static constexpr int A_OFF[2] = {0, A_HALF}, B_OFF[2] = {2 * A_HALF, 2 * A_HALF + B_HALF};
     static_assert(A_LD >= 1 && B_LD >= 1 && A_HALF % (1024 * WAVES) == 0 && B_HALF % (1024 * WAVES) == 0, "whole loads");
     static_assert(QM % MB == 0 && QN % MB == 0, "whole blocks");
-    static_assert(2 * STAGE <= 160 * 1024, "two stages in LDS");
+    static_assert(GROUP_LDS <= 160 * 1024, "two stages in LDS");
     static constexpr bool SPLIT = RH == 128;  // one workgroup per CU: the last round's tiles may be split
     static_assert(FN == 2, "the epilogue exchanges two 16 x 16 blocks side by side");
     static_assert(!(AT || BT) || ES == 2, "transposed reads of 16-bit elements");
@@ -117,26 +126,70 @@ __device__ __forceinline__ void wait_vm()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Loads per wave of the S half panels after number n (n % 4 == N4) of the order A lo, B lo, B hi,
+// A lane's scale bytes as the MFMA takes them. `raw`: the 8 scale bytes (chunk c of the K-step in byte
+// c) of the row that lane 16 s + r reads its operands' row r from in block s, s < 4. The operand of
+// block i and MFMA step ks in lane 16 g + r is chunk 4 ks + g of row r; its scale becomes byte
+// 2 (i / 2) + ks of word i % 2 (of two blocks: byte 2 i + ks of one word). Bytes change places with 16-lane rows in two steps: the 16-bit halves
+// between the halves of the wave, then the bytes between neighbouring rows.
+template <int W>
+__device__ __forceinline__ void scales_of_lane(u32x2 raw, unsigned (&out)[W])
+{
+    const unsigned x = __builtin_amdgcn_perm(raw[1], raw[0], 0x05040100u);  // chunks 0 1 4 5
+    const unsigned y = __builtin_amdgcn_perm(raw[1], raw[0], 0x07060302u);  // chunks 2 3 6 7
+    const auto h = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    const unsigned p = __builtin_amdgcn_perm(h[1], h[0], 0x06040200u), q = __builtin_amdgcn_perm(h[1], h[0], 0x07050301u);
+    const auto w = __builtin_amdgcn_permlane16_swap(p, q, false, false);
+    if constexpr (W == 2) {
+        out[0] = w[0];
+        out[1] = w[1];
+    } else {
+        out[0] = __builtin_amdgcn_perm(w[1], w[0], 0x05040100u);
+    }
+}
+
+// The MFMA of A's block i and B's block j in step ks (constants once unrolled), the operands exchanged.
+template <class T, class Acc>
+__device__ __forceinline__ Acc mma_scaled(u32x4 b, unsigned sb, int j, u32x4 a, const unsigned (&sa)[T::SAW], int i, int ks,
+                                          Acc c)
+{
+    typedef typename T::E E;
+    const unsigned y = T::SAW == 2 ? sa[i & (T::SAW - 1)] : sa[0];
+    const int x_byte = 2 * j + ks, y_byte = T::SAW == 2 ? 2 * (i >> 1) + ks : 2 * i + ks;
+    switch (4 * x_byte + y_byte) {  // the same step ks on both sides
+    case 0: return E::template mma<16, 0, 0>(b, sb, a, y, c);
+    case 2: return E::template mma<16, 0, 2>(b, sb, a, y, c);
+    case 5: return E::template mma<16, 1, 1>(b, sb, a, y, c);
+    case 7: return E::template mma<16, 1, 3>(b, sb, a, y, c);
+    case 8: return E::template mma<16, 2, 0>(b, sb, a, y, c);
+    case 10: return E::template mma<16, 2, 2>(b, sb, a, y, c);
+    case 13: return E::template mma<16, 3, 1>(b, sb, a, y, c);
+    default: return E::template mma<16, 3, 3>(b, sb, a, y, c);
+    }
+}
+
+// Loads per wave of the S half panels after number n (n % 2P == N) of the order A lo, B lo, B hi,
 // A hi, ...
-// (P = 4; without A hi, P = 3).
-template <class T, int N4, int S, int P = 4>
+// (P = 4; without A hi, P = 3). The first of an even K-step comes with scales.
+template <class T, int N, int S, int P = 4>
 constexpr int loads_after()
 {
     int sum = 0;
-    for (int i = 1; i <= S; ++i) sum += ((N4 + i) % P == 0 || (N4 + i) % P == 3) ? T::A_LD : T::B_LD;
+    for (int i = 1; i <= S; ++i) {
+        sum += ((N + i) % P == 0 || (N + i) % P == 3) ? T::A_LD : T::B_LD;
+        if (T::MX && (N + i) % (2 * P) == 0) ++sum;
+    }
     return sum;
 }
 
 // Wait until at most the min(later, S) half panels issued after number n are outstanding.
-template <class T, int N4, int S, int P = 4>
+template <class T, int N, int S, int P = 4>
 __device__ __forceinline__ void wait_halves(int later)
 {
     if constexpr (S == 0) {
         wait_vm<0>();
     } else {
-        if (later >= S) wait_vm<loads_after<T, N4, S, P>()>();
-        else wait_halves<T, N4, S - 1, P>(later);
+        if (later >= S) wait_vm<loads_after<T, N, S, P>()>();
+        else wait_halves<T, N, S - 1, P>(later);
     }
 }
 
@@ -231,7 +284,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         if (kg < KG - 1) k_end = k_lo + first_step(kg + 1) * T::BK;
         k_lo = lo;
         idle -= barriers(k_end - k_lo);
-        lds += kg * 2 * T::STAGE;
+        lds += kg * T::GROUP_LDS;
     }
     const int len = k_end - k_lo;
     const int ov = (T::BK - len % T::BK) % T::BK;
@@ -248,7 +301,29 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     unsigned a_voff[2][T::A_LD], b_voff[2][T::B_LD];
     // first k of the partial step that is below row 0 of the matrix (groups near its start, whose only
     // step it is): those lanes read row 0
+    // Mx4, whose scales take registers, keeps less: load l of half h is of rows h RH + 8 WAVES l + this
+    // wave's and lane's, its offset that row's, at most the last row's (offsets grow with rows).
+    unsigned a_row = 0, b_row = 0, mx_chunk = 0;
+    // Mx4: 64 rows' scales for each wave (some twice): of B, then of A
+    const int sc_row = 64 * (w % T::SC_SEGMENTS);
+    const bool sc_of_b = sc_row < T::BN;
+    const unsigned char *sc_base = nullptr;
+    unsigned sc_voff = 0;
+    if constexpr (T::MX) {
+        const int row = sc_row + lane - (sc_of_b ? 0 : T::BN), last = sc_of_b ? p.N - 1 - nb0 : m_end - 1 - mb0;
+        sc_base = sc_of_b ? p.mxb + g * p.stride_mxb + (int64_t)nb0 * p.ld_mxb : p.mxa + (int64_t)mb0 * p.ld_mxa;
+        sc_voff = (unsigned)(min(row, last) * (sc_of_b ? p.ld_mxb : p.ld_mxa));
+    }
+    const unsigned a_last = (unsigned)((m_end - 1 - mb0) * p.lda), b_last = (unsigned)((p.N - 1 - nb0) * p.ldb);
     auto offsets_of = [&](int k_first) {
+        if constexpr (T::MX) {
+            const int r8 = 8 * w + lane / 8;
+            a_row = (unsigned)(r8 * p.lda);
+            b_row = (unsigned)(r8 * p.ldb);
+            mx_chunk = 16u * ((lane % 8) ^ swz_d(r8));
+            static_assert(8 * T::WAVES % 16 == 0, "a wave's loads share their rows' swizzle");
+            return;
+        }
         const int below = k_first < 0 ? -k_first : 0;
         const int last16 = min(p.K, T::BK) * T::ES - 16;  // the last chunk of a row shorter than a K-step
 #pragma unroll
@@ -285,10 +360,28 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         }
     };
     const unsigned lds0 = (unsigned)(uintptr_t)(lds_char *)lds;
+    auto first_k = [&](int kt) { return ov ? (kt == 0 ? k_partial : k_lo + (kt - 1) * T::BK) : k_lo + kt * T::BK; };
+    // Mx4: the scales of K-steps kt and kt + 1, kt even and not 0: a K-step's 8 follow each other. Of a
+    // last K-step alone those of the one before it come too, and its own are the second 8.
+    auto issue_scales = [&](int kt) {
+        const int at = first_k(kt) / 16 - (kt + 1 < nk ? 0 : 8);
+        dma16(lds0 + 2 * T::STAGE + (kt / 2 & 1) * T::SC_PAIR + 16 * sc_row, sc_base + at, sc_voff);
+    };
     // half panel number 4 kt + i of the reading order (0: A lo, 1: B lo, 2: B hi, 3: A hi)
     auto issue_one = [&](int kt, int i, int l) {  // load l of it
-        const int k0 = ov ? (kt == 0 ? k_partial : k_lo + (kt - 1) * T::BK) : k_lo + kt * T::BK;
+        const int k0 = first_k(kt);
         const unsigned st = lds0 + (kt & 1) * T::STAGE;
+        if constexpr (T::MX) {
+            const unsigned at = (w + T::WAVES * l) * 1024;
+            if (i == 0 || i == 3) {
+                const unsigned down = (unsigned)(((i == 3) * T::RH + 8 * T::WAVES * l) * p.lda);
+                dma16(st + T::A_OFF[i == 3] + at, A + (int64_t)mb0 * p.lda + k0, min(a_row + down, a_last) + mx_chunk);
+            } else {
+                const unsigned down = (unsigned)(((i - 1) * T::CH + 8 * T::WAVES * l) * p.ldb);
+                dma16(st + T::B_OFF[i - 1] + at, B + (int64_t)nb0 * p.ldb + k0, min(b_row + down, b_last) + mx_chunk);
+            }
+            return;
+        }
         if (i == 0 || i == 3) {
             const int h = i == 3;
             const Elem *base = T::AT ? A + (int64_t)k0 * p.lda + mb0 : A + (int64_t)mb0 * p.lda + k0;
@@ -346,6 +439,35 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         else dst[ks][j] = read_d(half, wn * T::FN + j, ks);
     };
 
+    // Mx4: a half panel's scales as read, and as the MFMAs take them (like a and b)
+    u32x2 raw_a = {}, raw_b = {};
+    unsigned sa[2][T::SAW] = {}, sb4[2][1] = {};
+    typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+    auto read_scales = [&](int kt, bool of_b, int half, u32x2 &raw) {
+        const lds_char *sc = (const lds_char *)lds + 2 * T::STAGE + (kt / 2 & 1) * T::SC_PAIR;
+        const int second = (kt & 1) != 0 || (kt == nk - 1 && kt > 0) ? 8 : 0;
+        // B's, of at most two blocks, come from the first 32 lanes; the rows that the others read lie in A's
+        const int row = of_b ? half * T::CH + wn * T::QN + lane : T::BN + half * T::RH + wm * T::QM + lane % T::QM;
+        raw = *(const lds_u32x2 *)(sc + second + 16 * row);
+    };
+    // of the first two K-steps, through registers
+    auto first_scales = [&] {
+        struct __attribute__((packed)) Eight {
+            u32x2 v;
+        };
+        const unsigned char *q = sc_base + sc_voff;
+        u32x4 v = {};
+        const u32x2 x = reinterpret_cast<const Eight *>(q + first_k(0) / 16)->v;
+        v[0] = x[0];
+        v[1] = x[1];
+        if (nk > 1) {
+            const u32x2 y = reinterpret_cast<const Eight *>(q + first_k(1) / 16)->v;
+            v[2] = y[0];
+            v[3] = y[1];
+        }
+        *(lds_u32x4 *)((lds_char *)lds + 2 * T::STAGE + 16 * (sc_row + lane)) = v;
+    };
+
     constexpr int HA = LO ? 1 : 2;  // halves of rows
     // blocks of C transposed (the MFMA's operands exchanged): lane l holds row l % 16 of C and the
     // columns 4 (l / 16) + r, r < 4
@@ -381,7 +503,8 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                                (reads_a ? T::A_OFF[I == 1] : T::B_OFF[I == 0]);
         auto mfma = [&](int m) {
             const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
-            acc[qa][qb][i][j] = E::template mma<T::MB>(b[S ^ qb][ks][j], a[qa][ks][i], acc[qa][qb][i][j]);
+            if constexpr (!T::MX)  // phase_mx
+                acc[qa][qb][i][j] = E::template mma<T::MB>(b[S ^ qb][ks][j], a[qa][ks][i], acc[qa][qb][i][j]);
         };
         auto read = [&](int r) {
             if constexpr (reads_a) read_a(half, r, a[I == 1]);
@@ -406,6 +529,74 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    // The same for Mx4, whose scales' registers leave none for both halves of A: a half replaces the
+    // other operand by operand, each read behind the last MFMA of the one before it, B lo of the next
+    // K-step likewise B hi. Phase 0: A lo x B lo, reads B hi; 1: A lo x B hi, reads A hi; 2: A hi x
+    // B hi, reads B lo of the next K-step; 3: A hi x B lo, reads A lo of the next. So half panels are
+    // numbered 4 kt + (0: B lo, 1: A lo, 2: B hi, 3: A hi), and the DMA goes out a phase later, so that a
+    // phase waits for the reads of the phase before the last one only. Five half panels are on their way.
+    // LEFT: K-steps that follow, 2 if there are more. (One body for all but the last two and no branches
+    // in them: with bodies for even and odd K-steps, or branches around the loads, some of the sums went
+    // through memory on the way.) B lo is in b[0], B hi in b[1], and so B lo of the next K-step, until its
+    // first phase moves it.
+    auto phase_mx = [&](int kt, auto I_, auto LEFT_) {
+        constexpr int I = decltype(I_)::value, LEFT = decltype(LEFT_)::value;
+        constexpr int qa = I >= 2, qb = I == 1 || I == 2;
+        constexpr bool reads_a = I == 1 || I == 3;
+        constexpr int NM = T::KS * T::FM * T::FN, NR = T::KS * (reads_a ? T::FM : T::FN), each = NM / NR;
+        constexpr int issues = I == 0 ? 1 : I == 1 ? 0 : I;  // as issue_one counts
+        constexpr int NL = issues == 0 || issues == 3 ? T::A_LD : T::B_LD;
+        constexpr int pre = NM / 8;
+        const lds_char *half = (const lds_char *)lds + ((kt + (I >= 2)) & 1) * T::STAGE +
+                               (reads_a ? T::A_OFF[I == 1] : T::B_OFF[I == 0]);
+        auto mfma = [&](int m) {  // operands in the order in which the next half replaces them
+            const int ks = m / (T::FM * T::FN);
+            const int i = I == 2 ? m % T::FM : m / T::FN % T::FM, j = I == 2 ? m / T::FM % T::FN : m % T::FN;
+            acc[qa][qb][i][j] = mma_scaled<T>(b[qb][ks][j], sb4[qb][0], j, a[0][ks][i], sa[0], i, ks, acc[qa][qb][i][j]);
+        };
+        // the offsets of the loads and reads anew for each K-step: kept, they would take some 20 registers
+        if constexpr (I == 0) asm volatile("" : "+v"(a_row), "+v"(b_row), "+v"(d_off[0]), "+v"(d_off[1]));
+        // the scales that the phase before read
+        if constexpr (reads_a) scales_of_lane(raw_b, sb4[1]);
+        else scales_of_lane(raw_a, sa[0]);
+#pragma unroll
+        for (int m = 0; m < pre; ++m) mfma(m);
+        // half panels issued after number 4 kt + 2 + I, which is read next
+        constexpr int later = LEFT == 2 ? 5 : 4 * LEFT + 1 - I;
+        if constexpr (later >= 0) wait_vm<later * T::A_LD>();  // scales among them: one more than need be
+        // at most the reads of the phase before are left: those before it are done
+        asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(T::KS * (reads_a ? T::FN : T::FM)) : "memory");
+        bare_barrier();
+        if constexpr (later >= 0) read_scales(kt + (I >= 2), !reads_a, I < 2, reads_a ? raw_a : raw_b);
+        auto read = [&](int r) {
+            if constexpr (later < 0) return;
+            else if constexpr (reads_a) read_a(half, r, a[0]);
+            else read_b(half, r, b[1]);
+        };
+#pragma unroll
+        for (int m = pre; m < NM; ++m) {
+            if (m > 0 && m % each == 0) read(m / each - 1);
+#pragma unroll
+            for (int l = 0; l < NL; ++l)
+                if (LEFT == 2 && m == pre + (l + 1) * (NM - pre) / (NL + 1)) issue_one(kt + 2, issues, l);
+            mfma(m);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        read(NR - 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto k_step_mx = [&](int kt, auto LEFT) {
+        static_assert(!T::MX || T::A_LD == T::B_LD, "half panels of as many loads");
+#pragma unroll
+        for (int ks = 0; ks < T::KS; ++ks)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j) b[0][ks][j] = b[1][ks][j];
+        sb4[0][0] = sb4[1][0];
+        phase_mx(kt, std::integral_constant<int, 0>(), LEFT);
+        phase_mx(kt, std::integral_constant<int, 1>(), LEFT);
+        phase_mx(kt, std::integral_constant<int, 2>(), LEFT);
+        phase_mx(kt, std::integral_constant<int, 3>(), LEFT);
+    };
     auto k_step = [&](int kt, auto S, auto FULL) {
         phase(kt, std::integral_constant<int, 0>(), S, FULL);
         phase(kt, std::integral_constant<int, 1>(), S, FULL);
@@ -424,15 +615,27 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         const lds_char *stage = (const lds_char *)lds + ((kt + I) & 1) * T::STAGE;
         auto mfma = [&](int m) {
             const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
-            acc[0][I][i][j] = E::template mma<T::MB>(b[I][ks][j], a[S][ks][i], acc[0][I][i][j]);
+            if constexpr (T::MX)
+                acc[0][I][i][j] = mma_scaled<T>(b[I][ks][j], sb4[I][0], j, a[S][ks][i], sa[S], i, ks, acc[0][I][i][j]);
+            else acc[0][I][i][j] = E::template mma<T::MB>(b[I][ks][j], a[S][ks][i], acc[0][I][i][j]);
         };
+        if constexpr (T::MX) {
+            scales_of_lane(raw_b, sb4[I]);
+            if constexpr (I == 0) scales_of_lane(raw_a, sa[S]);
+        }
 #pragma unroll
         for (int m = 0; m < pre; ++m) mfma(m);
         const int n = 3 * kt + (I == 0 ? 2 : 4), issued = 3 * kt + (I == 0 ? 6 : 8);
-        if (FULL) wait_vm<T::A_LD + 2 * T::B_LD>();
-        else if (n < halves) wait_halves<T, (I == 0 ? 2 : 1), 3, 3>(min(issued, halves) - 1 - n);
+        if (FULL) wait_vm<loads_after<T, (3 * S + (I == 0 ? 2 : 4)) % 6, 3, 3>()>();
+        else if (n < halves) wait_halves<T, (3 * S + (I == 0 ? 2 : 4)) % 6, 3, 3>(min(issued, halves) - 1 - n);
         wait_reads();
         bare_barrier();
+        if constexpr (T::MX) {
+            read_scales(kt + I, true, I == 0, raw_b);
+            if constexpr (I == 1) read_scales(kt + 1, false, 0, raw_a);
+            if constexpr (I == 0 && S == 0)
+                if (FULL || kt + 2 < nk) issue_scales(kt + 2);
+        }
 #pragma unroll
         for (int m = pre; m < NM; ++m) {
 #pragma unroll
@@ -459,9 +662,11 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     if (nk > 0) {
         constexpr int panels = LO ? 3 : 4;  // half panels per K-step
         offsets_of(ov ? k_end - T::BK : 0);
-        for (int i = 0; i < panels; ++i) issue(0, i);
+        if constexpr (T::MX) first_scales();
+        constexpr int swapped = T::MX && !LO;  // B lo first, as it is read
+        for (int i = 0; i < panels; ++i) issue(0, i < 2 ? i ^ swapped : i);
         if (nk > 1)
-            for (int i = 0; i < panels; ++i) issue(1, i);
+            for (int i = 0; i < panels; ++i) issue(1, i < 2 ? i ^ swapped : i);
         if (ov) {
             // zeros over the first ov k of both panels, once the whole step has landed everywhere
             if (nk > 1) wait_vm<(LO ? 1 : 2) * T::A_LD + 2 * T::B_LD>();
@@ -503,12 +708,18 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
             wait_reads();
         } else {
             wait_halves<T, 1, 6, panels>(min(halves, 2 * panels) - 2);
+            if constexpr (T::MX) wait_reads();  // the first scales' write
         }
         bare_barrier();
 #pragma unroll
         for (int r = 0; r < T::KS * T::FM; ++r) read_a((const lds_char *)lds + T::A_OFF[0], r, a[0]);
 #pragma unroll
-        for (int r = 0; r < T::KS * T::FN; ++r) read_b((const lds_char *)lds + T::B_OFF[0], r, b[0]);
+        for (int r = 0; r < T::KS * T::FN; ++r) read_b((const lds_char *)lds + T::B_OFF[0], r, b[T::MX && !LO]);
+        if constexpr (T::MX) {
+            read_scales(0, false, 0, raw_a);
+            read_scales(0, true, 0, raw_b);
+            if constexpr (!LO) scales_of_lane(raw_b, sb4[1]);
+        }
         wait_reads();
         bare_barrier();
         using S0 = std::integral_constant<int, 0>;
@@ -523,6 +734,13 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
                 k_step_lo(kt, S0(), std::false_type());
                 if (kt + 1 < nk) k_step_lo(kt + 1, S1(), std::false_type());
             }
+        } else if constexpr (T::MX) {
+            for (; kt + 2 < nk; ++kt) {
+                if (!(kt & 1)) issue_scales(kt + 2);
+                k_step_mx(kt, std::integral_constant<int, 2>());
+            }
+            if (kt + 1 < nk) k_step_mx(kt++, std::integral_constant<int, 1>());
+            k_step_mx(kt, std::integral_constant<int, 0>());
         } else {
             if (nk > 2) issue(2, 0);
             for (; kt + 4 < nk; kt += 2) {
@@ -540,7 +758,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         for (int i = 0; i < idle; ++i) bare_barrier();
         // once every wave has read what it needs, the other groups' sums go through their panels' LDS
         typedef __attribute__((address_space(3))) typename E::template Acc<T::MB> lds_acc;
-        static_assert(T::BM * T::BN * 4 <= 2 * T::STAGE, "a group's sums fit its LDS");
+        static_assert(T::BM * T::BN * 4 <= T::GROUP_LDS, "a group's sums fit its LDS");
         bare_barrier();
         auto each = [&](const char *group, auto &&f) {
             lds_acc *part = (lds_acc *)(lds_char *)group + 64 * w + lane;
@@ -563,7 +781,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         bare_barrier();
 #pragma unroll
         for (int group = 1; group < KG; ++group)
-            each(lds + group * 2 * T::STAGE, [](auto &mine, lds_acc *at) { mine += *at; });
+            each(lds + group * T::GROUP_LDS, [](auto &mine, lds_acc *at) { mine += *at; });
     }
 
     // ---- epilogue: 16 bytes (32 of fp32) of a row per lane, 16 rows of 32 columns per instruction,
@@ -646,7 +864,7 @@ __device__ __forceinline__ bool tile_part(int64_t bid, int64_t tiles, unsigned &
 template <class T, bool GRAD, int KG>
 __global__ __launch_bounds__(T::NT * KG) void group_tile_kernel(GroupArgs p)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[KG * 2 * T::STAGE];
+    __shared__ __attribute__((aligned(1024))) char lds[KG * T::GROUP_LDS];
 
     const unsigned tiles_n = (unsigned)((p.N + T::BN - 1) / T::BN);
     const int64_t bid = linear_block();
@@ -701,6 +919,8 @@ bool tile_ok(const GroupArgs &a)
     constexpr int largest = 0x7fffffff - 1024;  // a tile's row and column numbers fit an int
     if (a.M > largest || a.N > largest || a.K > largest) return false;
     if (!GRAD && a.K * T::ES < 16) return false;  // a chunk
+    // a row has a K-step's scales, and their lane offsets fit 32 bits
+    if (T::MX && (a.K < T::BK || (T::BM - 1) * a.ld_mxa >= limit || (T::BN - 1) * a.ld_mxb >= limit)) return false;
     if ((T::AT && a.K < 8) || (T::BT && a.N < 8)) return false;  // a chunk of a T operand's columns
     const int64_t a_rows = T::AT ? T::BK : T::BM, b_rows = T::BT ? T::BK : T::BN;
     return ((a_rows - 1) * a.lda + T::BM) * T::ES + 128 < limit && ((b_rows - 1) * a.ldb + T::BN) * T::ES + 128 < limit;
@@ -746,6 +966,7 @@ template <class F>
 auto with_tiles(const GroupArgs &a, F &&f)
 {
     if (a.elem == GroupElem::I8) return f(Tiles<ElemI8, false, false>());
+    if (a.elem == GroupElem::Mx4) return f(Tiles<ElemMx4, false, false>());
     const bool f16 = a.elem == GroupElem::F16;
     if (a.grad) return f16 ? f(Tiles<ElemF16, true, true>()) : f(Tiles<ElemBf16, true, true>());
     if (a.trans_b) return f16 ? f(Tiles<ElemF16, false, false>()) : f(Tiles<ElemBf16, false, false>());
@@ -767,7 +988,7 @@ double group_tile_time(const GroupArgs &a, GroupTileKind kind)
 {
     const bool large = kind == GroupTileKind::Large, small = kind <= GroupTileKind::Small;
     const double sum = a.grad ? (double)a.M / a.groups : (double)a.K;  // length of a tile's sums
-    const double steps = ceil(sum * (a.elem == GroupElem::I8 ? 1 : 2) / 128) * (aligned_words(a) ? 1.0 : large ? 1.25 : small && a.trans_b ? 2.3 : 1.5);
+    const double steps = ceil(sum * group_elem_size(a) / 128) * (aligned_words(a) ? 1.0 : large ? 1.25 : small && a.trans_b ? 2.3 : 1.5);
     const int t = large ? 256 : kind == GroupTileKind::Mid ? 128 : 64;
     const double tiles = (double)(((int64_t)a.N + t - 1) / t) *
                          (a.grad ? (double)(((int64_t)a.K + t - 1) / t) * a.groups : expected_row_tiles(a, t));
