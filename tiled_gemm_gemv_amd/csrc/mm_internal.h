@@ -222,6 +222,7 @@ struct RouteArgs {
     int *ws;                   // route_ws_ints(T, E, k) ints
     int64_t ld;
     int T, E, k, groups, top_groups, group_top;
+    int tokens;                // of a workgroup, set by route_launch
     int type;                  // MM_TYPE_*
     bool sigmoid, renormalize;
     float scale;

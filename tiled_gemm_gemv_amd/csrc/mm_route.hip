@@ -8,19 +8,31 @@
 // chosen; slots left over get expert -1 and weight 0. w_j = scale s_j, or scale s_j / sum of the chosen s
 // (0 where that is 0).
 //
-// The ranks are taken in 64 bits: with 16384 tokens and 256 experts some pair of neighbouring scores
-// lies closer than 32-bit rounding, and the choice would go by it.
+// The ranks are those of 64-bit values: with 16384 tokens and 256 experts some pair of neighbouring
+// scores lies closer than 32-bit rounding, and the choice would go by it. A wave takes a token. It
+// computes c in 32 bits, off by at most `slack`, and picks the best one after the other by a 32-bit key
+// of 22 leading bits and the index: k of them, and all others that could be above the k-th by slack and
+// truncation. Those few, one to a lane, get their values in 64 bits and are put in that order. Where
+// groups lie closer than the slack, values are NaN or infinite, or more than 64 experts are that close,
+// the token is done in 64 bits throughout.
 //
-// The rows' order: slots by (expert, token, slot). Each workgroup routes 64 tokens, counts their slots
-// for each expert and numbers them there; a scan over the workgroups' counts gives each expert's first
-// row and each workgroup's first of it; the last kernel adds that to the slots' numbers. No atomics: the
+// The rows' order: slots by (expert, token, slot). A workgroup routes 16 or 64 tokens; a token takes an expert
+// once, so a 64-bit mask for each expert says which of them have it, and counts of its bits number the
+// workgroup's slots. The workgroups' counts are added up over workgroups and experts (in the last
+// kernel itself for up to 16 workgroups, else by one in between). No atomics but the masks' bits: the
 // order is fixed.
+//
+// Many tokens are bound by instructions (some 650 for a token of 256 experts, 8 of them chosen: 16384
+// tokens 19 us, with groups and a bias 32, of 8 MB that could be read in 2), few by the launches: 3 to 5 us
+// each, three of them (8 tokens of 64 experts: one, 5 us).
 #include "mm_group.h"
 
 namespace mm {
 namespace {
 
-constexpr int kWaves = 16, kTokens = 64;  // of a workgroup of the first kernel
+constexpr int kWaves = 16;                // of a workgroup of the first kernel
+constexpr int kTokens = 64;               // most tokens of a workgroup
+constexpr int kFewBlocks = 16;            // workgroups whose counts the last kernel adds up by itself
 
 template <class X>
 __device__ __forceinline__ float load_logit(const void *p, int64_t at)
@@ -52,15 +64,25 @@ __device__ __forceinline__ uint64_t ordered(double v)
 }
 constexpr uint64_t kLowest = 0x000fffffffffffffull;  // ordered(-inf)
 
+// Largest value of the wave, in every lane.
+__device__ __forceinline__ unsigned wave_max_u32(unsigned v)
+{
+    v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));  // row_shr 1, 2, 4, 8
+    v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));
+    v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));
+    v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));
+    v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));  // row_bcast 15
+    v = max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));  // row_bcast 31
+    return (unsigned)__builtin_amdgcn_readlane((int)v, 63);
+}
 // The largest key of the wave and the lowest index that has it.
 __device__ __forceinline__ void wave_best(uint64_t &key, int &index)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const uint64_t k = __shfl_xor(key, d);
-        const int i = __shfl_xor(index, d);
-        if (k > key || (k == key && i < index)) key = k, index = i;
-    }
+    const unsigned hi = wave_max_u32((unsigned)(key >> 32));
+    const bool top = (unsigned)(key >> 32) == hi;
+    const unsigned lo = wave_max_u32(top ? (unsigned)key : 0u);
+    index = (int)~wave_max_u32(top && (unsigned)key == lo ? ~(unsigned)index : 0u);
+    key = (uint64_t)hi << 32 | lo;
 }
 
 // Scores of this lane's experts lane + 64 r of one token.
@@ -94,9 +116,10 @@ __device__ __forceinline__ void token_scores(const RouteArgs &p, const float (&l
     for (int r = 0; r < R; ++r) s[r] = sum == 0 ? 0.0 : s[r] / sum;
 }
 
-// Scores, choice and weights of token t by one wave; lane j < k returns the expert of slot j (-1: none).
+// Scores, choice and weights of token t by one wave, all of it in 64 bits; lane j < k returns the expert
+// of slot j (-1: none).
 template <class X, int R>
-__device__ __forceinline__ int route_token(const RouteArgs &p, int64_t t)
+__device__ __forceinline__ int route_token_exact(const RouteArgs &p, int64_t t)
 {
     const int lane = threadIdx.x & 63;
     float l[R];
@@ -190,6 +213,303 @@ __device__ __forceinline__ int route_token(const RouteArgs &p, int64_t t)
     return chosen;
 }
 
+// The same for fp32, and back.
+__device__ __forceinline__ unsigned ordered32(float v)
+{
+    if (v != v) return ~0u;
+    const unsigned b = __builtin_bit_cast(unsigned, v + 0.f);  // -0 and 0 are equal
+    return b >> 31 ? ~b : b | 1u << 31;
+}
+__device__ __forceinline__ float from_ordered32(unsigned u)
+{
+    return __builtin_bit_cast(float, u >> 31 ? u & 0x7fffffffu : ~u);
+}
+
+// Sum over the wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v)
+{
+    auto step = [&](auto ctrl, auto rows) {
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value,
+                                                                   decltype(rows)::value, 0xf, false));
+    };
+    step(std::integral_constant<int, 0x111>(), std::integral_constant<int, 0xf>());  // row_shr 1, 2, 4, 8
+    step(std::integral_constant<int, 0x112>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x114>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x118>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>());  // row_bcast 15
+    step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>());  // row_bcast 31
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ float readlane_f(float v, int lane)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int lane)
+{
+    return (uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+           (unsigned)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// How far c in 32 bits may be from c in 64. Sigmoid: the exponential is off by 2^-23 of itself and, from
+// its argument times log2 e, by 1.5 |l| 2^-24, which makes 2^-25 and (s (1 - s) |l| <= 0.224) 2^-25.5 of s;
+// 1 + exp and its reciprocal 3 2^-24 s: less than 2^-22. Softmax: the exponential 2^-23 of itself and
+// |l - m| 2^-24 (0.37 at most of p |l - m|), sum and quotient 2^-24 each: less than 2^-22 too. The sum with
+// the bias 2^-24 |c|.
+__device__ __forceinline__ float slack(float c) { return 0x1p-22f + 0x1p-23f * fabsf(c); }
+
+// v of the lane that differs in the bit d (a lane of the other half of 2 d lanes, where those of a half
+// are equal).
+template <class V>
+__device__ __forceinline__ V other_half(V v, int d)
+{
+    if constexpr (sizeof(V) == 8) {
+        return __shfl_xor(v, d);
+    } else {
+        const int x = __builtin_bit_cast(int, v);
+        int y;
+        if (d == 1) y = __builtin_amdgcn_update_dpp(0, x, 0xb1, 0xf, 0xf, false);         // quad_perm 1 0 3 2
+        else if (d == 2) y = __builtin_amdgcn_update_dpp(0, x, 0x4e, 0xf, 0xf, false);    // quad_perm 2 3 0 1
+        else if (d == 4) y = __builtin_amdgcn_update_dpp(0, x, 0x141, 0xf, 0xf, false);   // row_half_mirror
+        else if (d == 8) y = __builtin_amdgcn_update_dpp(0, x, 0x140, 0xf, 0xf, false);   // row_mirror
+        else y = __shfl_xor(x, d);
+        return __builtin_bit_cast(float, y);
+    }
+}
+__device__ __forceinline__ float readlane(float v, int lane) { return readlane_f(v, lane); }
+__device__ __forceinline__ double readlane(double v, int lane)
+{
+    return __builtin_bit_cast(double, readlane_u64(__builtin_bit_cast(uint64_t, v), lane));
+}
+
+// The kept groups, 2^shift lanes to a group, the bit of a group that of its first lane; at(e) is the
+// value of expert e, no NaN. low, next: the last kept group's value and the first other's.
+template <class V, class F>
+__device__ __forceinline__ unsigned long long keep_groups(const RouteArgs &p, int per, int shift, F &&at, V &low, V &next)
+{
+    const int lane = threadIdx.x & 63, g = lane >> shift, e0 = min(g, p.groups - 1) * per;
+    const V none = -__builtin_inff();
+    V first = none, second = none;
+    for (int i = lane & ((1 << shift) - 1); i < per; i += 4 << shift) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int x = i + (u << shift);
+            const V v = x < per ? at(e0 + x) : none;
+            second = fmax(second, fmin(first, v));
+            first = fmax(first, v);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        if (d < 1 << shift) {
+            const V f = other_half(first, d), h = other_half(second, d);
+            second = fmax(fmin(first, f), fmax(second, h));
+            first = fmax(first, f);
+        }
+    const V value = p.group_top == 1 ? first : second == none ? none : first + second;
+    int rank = 0;
+    for (int i = 0; i < p.groups; ++i) {
+        const V v = readlane(value, i << shift);
+        rank += v > value || (v == value && i < g);
+    }
+    const unsigned long long a = __ballot(rank == p.top_groups - 1 && g < p.groups);
+    const unsigned long long b = __ballot(rank == p.top_groups && g < p.groups);
+    low = a ? readlane(value, __ffsll(a) - 1) : none;
+    next = b ? readlane(value, __ffsll(b) - 1) : none;
+    return __ballot(g < p.groups && rank < p.top_groups);
+}
+
+// Sum of 64-bit values over the wave, in lane 63.
+__device__ __forceinline__ double wave_sum64(double v)
+{
+    auto step = [&](auto ctrl, auto rows) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)b, decltype(ctrl)::value, decltype(rows)::value,
+                                                                  0xf, false);
+        const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), decltype(ctrl)::value,
+                                                                  decltype(rows)::value, 0xf, false);
+        v += __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    };
+    step(std::integral_constant<int, 0x111>(), std::integral_constant<int, 0xf>());  // row_shr 1, 2, 4, 8
+    step(std::integral_constant<int, 0x112>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x114>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x118>(), std::integral_constant<int, 0xf>());
+    step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>());  // row_bcast 15
+    step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>());  // row_bcast 31
+    return v;
+}
+
+constexpr int kExact = -2;  // the token has to be done in 64 bits throughout
+
+// Token t by one wave, `row` its LDS for E values, `bias` in LDS; lane j < k returns the expert of slot
+// j (-1: none), or every lane kExact.
+template <class X, int R>
+__device__ __forceinline__ int route_token(const RouteArgs &p, int64_t t, const float (&l)[R], const int (&group)[R],
+                                           int per, int shift, float *row, const float *bias)
+{
+    const int lane = threadIdx.x & 63;
+    const float inf = __builtin_inff();
+    const bool by_score = p.bias, sums = p.groups > 1 && p.group_top == 2;
+    // scores in 32 bits (softmax: without the quotient) where the choice or the sum needs them
+    float m = 0.f, total32 = 1.f;
+    float s[R];
+    if (!p.sigmoid) {
+        unsigned top = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) top = max(top, ordered32(l[r]));
+        m = from_ordered32(wave_max_u32(top));
+        if (m == -inf) m = 0.f;
+        if (!(m < inf)) m = __builtin_nanf("");  // an infinite logit makes all scores NaN, as NaN does
+    }
+    const bool all_scores = !p.sigmoid && (by_score || !p.renormalize);
+    double total = 1.0;
+    if (by_score || sums || all_scores) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            s[r] = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-l[r])) : expf(l[r] - m);
+    }
+    if (all_scores) {
+        if (by_score) {  // the quotient decides ranks: the sum in 64 bits
+            double sum = 0;
+#pragma unroll
+            for (int r = 0; r < R; ++r) sum += exp((double)l[r] - (double)m);
+            total = wave_add(sum);
+            total32 = (float)total;
+        } else {
+            float sum = s[0];
+#pragma unroll
+            for (int r = 1; r < R; ++r) sum += s[r];
+            total = total32 = wave_sum(sum);
+        }
+    }
+    bool exact = false;  // the token has to be done in 64 bits throughout
+    float c[R];
+    if (by_score) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float q = p.sigmoid ? s[r] : total32 == 0.f ? 0.f : s[r] / total32;
+            const int e = lane + 64 * r;
+            c[r] = l[r] == -inf || e >= p.E ? -inf : q + bias[e];
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) c[r] = l[r];
+    }
+    unsigned long long kept = ~0ull;  // the bit of a group: of its first lane, 2^shift lanes to a group
+    if (p.groups > 1) {
+        bool odd = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float v = by_score || !sums ? c[r] : l[r] == -inf ? -inf : s[r];
+            odd |= !(v < inf);
+            if (lane + 64 * r < p.E) row[lane + 64 * r] = v;
+        }
+        exact = __any(odd);
+        __builtin_amdgcn_wave_barrier();
+        float low, next;
+        kept = keep_groups<float>(p, per, shift, [&](int e) { return row[e]; }, low, next);
+        __builtin_amdgcn_wave_barrier();
+        if (!exact && p.top_groups < p.groups && (by_score || sums) && next > -inf && !(low - next > 4 * slack(low))) {
+            // too close to tell: the same in 64 bits (softmax without a bias: without the quotient)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (lane + 64 * r < p.E) row[lane + 64 * r] = c[r] == -inf ? -inf : l[r];
+            __builtin_amdgcn_wave_barrier();
+            auto wide = [&](int e) {
+                const double x = row[e];
+                if (x == -__builtin_inf()) return x;
+                double v = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)m);
+                if (by_score) v = (all_scores ? total == 0 ? 0.0 : v / total : v) + (double)bias[e];
+                return v;
+            };
+            double low64, next64;
+            kept = keep_groups<double>(p, per, shift, wide, low64, next64);
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+    // the picks' keys: 22 bits of c, then the lower index first; 0: not to be picked
+    unsigned key[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = lane + 64 * r;
+        const bool live = c[r] != -inf && (p.groups == 1 || (kept >> group[r] & 1));
+        key[r] = live ? (ordered32(c[r]) & ~1023u) | (unsigned)(1023 - e) : 0u;
+        if (e < p.E) row[e] = l[r];
+    }
+    unsigned mine = 0, least = 0;
+    int n = 0;
+    for (; !exact; ++n) {
+        unsigned best = key[0];
+#pragma unroll
+        for (int r = 1; r < R; ++r) best = max(best, key[r]);
+        best = wave_max_u32(best);
+        if (best <= least) break;  // none left, or none that could be above the k-th
+        if (n == 64) {
+            exact = true;
+            break;
+        }
+        if (lane == n) mine = best;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (key[r] == best) key[r] = 0;
+        if (n == p.k - 1) {
+            if (by_score) {
+                const float v = from_ordered32(best & ~1023u);
+                exact = !(fabsf(v) < inf);
+                least = (ordered32(v - 2 * slack(v)) & ~1023u) - 1;
+            } else if (sizeof(X) == 2) {  // 16-bit logits are in the key whole
+                ++n;
+                break;
+            } else {
+                least = (best & ~1023u) - 1;
+            }
+        }
+    }
+    if (exact) return kExact;
+    __builtin_amdgcn_wave_barrier();
+    int index = lane < n ? 1023 - (int)(mine & 1023u) : -1;
+    double score = 0;
+    uint64_t rank_value = 0;
+    if (lane < n) {
+        const float x = row[index];
+        score = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)m);
+        if (all_scores) score = total == 0 ? 0.0 : score / total;
+        rank_value = by_score ? ordered(score + (double)bias[index]) : (uint64_t)ordered32(x);
+    }
+    if (by_score || sizeof(X) == 4) {
+        // in order? (32 bits almost always tell it)
+        const uint64_t next = __shfl_down(rank_value, 1);
+        const int next_index = __shfl_down(index, 1);
+        if (__any(lane + 1 < n && (next > rank_value || (next == rank_value && next_index < index)))) {
+            int place = 0;
+            for (int i = 0; i < n; ++i) {
+                const uint64_t v = readlane_u64(rank_value, i);
+                const int e = __builtin_amdgcn_readlane(index, i);
+                place += v > rank_value || (v == rank_value && e < index);
+            }
+            // lane `place` takes this lane's: push
+            const uint64_t bits = __builtin_bit_cast(uint64_t, score);
+            const int to = 4 * (lane < n ? place : lane);
+            index = __builtin_amdgcn_ds_permute(to, index);
+            const unsigned lo = (unsigned)__builtin_amdgcn_ds_permute(to, (int)bits);
+            const unsigned hi = (unsigned)__builtin_amdgcn_ds_permute(to, (int)(bits >> 32));
+            score = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+        }
+    }
+    if (lane >= p.k || lane >= n) {
+        index = -1;
+        score = 0;
+    }
+    if (p.renormalize) {
+        const double sum = __builtin_bit_cast(double, readlane_u64(__builtin_bit_cast(uint64_t, wave_sum64(score)), 63));
+        score = sum == 0 || index < 0 ? 0.0 : score / sum;
+    }
+    if (lane < p.k) {
+        p.weights[t * p.k + lane] = (float)(score * (double)p.scale);
+        p.experts[t * p.k + lane] = index;
+    }
+    return index;
+}
+
 // Exclusive sum over the workgroup's threads, in thread order, and the total.
 template <int W>
 __device__ __forceinline__ unsigned block_scan(unsigned v, unsigned *part, unsigned &total)
@@ -209,118 +529,159 @@ __device__ __forceinline__ unsigned block_scan(unsigned v, unsigned *part, unsig
     return before + incl - v;
 }
 
-// 64 tokens: weights and experts; rows: each slot's number among the workgroup's of its expert; the
+// p.tokens tokens: weights and experts; rows: each slot's number among the workgroup's of its expert; the
 // experts' counts. ALL: the only workgroup, which finishes rows and offsets.
 template <class X, int R, bool ALL>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p)
 {
-    // a wave's tokens choose an expert once each at most
-    __shared__ unsigned char count[kWaves][64 * R];
+    __shared__ unsigned mask[64 * R][2];  // the tokens that take an expert
     __shared__ short slot[kTokens * kRouteMaxTop];
+    __shared__ float rows[kWaves][64 * R], bias[64 * R];
     __shared__ unsigned first[64 * R], part[kWaves];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t bid = linear_block(), t0 = bid * kTokens;
-    constexpr int per_wave = kTokens / kWaves;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, e = threadIdx.x;
+    const int64_t t0 = linear_block() * p.tokens;
     if (t0 >= p.T) return;  // the whole workgroup
-    for (int i = lane; i < 64 * R; i += 64) count[w][i] = 0;
-    for (int i = 0; i < per_wave; ++i) {
-        const int t = w * per_wave + i;
-        const int chosen = t0 + t < p.T ? route_token<X, R>(p, t0 + t) : -1;
-        if (lane < p.k) slot[t * p.k + lane] = (short)chosen;
+    if (e < 64 * R) {
+        mask[e][0] = mask[e][1] = 0;
+        bias[e] = p.bias && e < p.E ? p.bias[e] : 0.f;
     }
     __syncthreads();
-    // numbers within the wave: a token's experts differ, so those of the tokens before
-    const int slots = per_wave * p.k, base = w * slots;
-    for (int c = 0; c < slots; c += 64) {
-        const int i = c + lane, e = i < slots ? slot[base + i] : -1;
-        unsigned long long same = __ballot(e >= 0);
-        for (int b = 0; b < 10; ++b) {
-            const unsigned long long set = __ballot(e >> b & 1);
-            same &= e >> b & 1 ? set : ~set;
+    int group[R], shift = 0;  // the bit of an expert's group
+    const int per = __builtin_amdgcn_readfirstlane(p.E / p.groups);
+    while (2 * p.groups << shift <= 64) ++shift;
+#pragma unroll
+    for (int r = 0; r < R; ++r) group[r] = p.groups == 1 ? 0 : min((lane + 64 * r) / per, p.groups - 1) << shift;
+    float l[R], ahead[R];
+    auto load = [&](int t, float (&x)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = lane + 64 * r;
+            x[r] = t < p.tokens && t0 + t < p.T && i < p.E ? load_logit<X>(p.logits, (t0 + t) * p.ld + i) : -__builtin_inff();
         }
-        if (e >= 0) {
-            const int before = __popcll(same & ((1ull << lane) - 1)), n = count[w][e];
-            __builtin_amdgcn_wave_barrier();
-            if (before == __popcll(same) - 1) count[w][e] = (unsigned char)(n + before + 1);
-            p.rows[t0 * p.k + base + i] = n + before;  // of the slots in range: e >= 0
+    };
+    auto keep = [&](int t, int chosen) {
+        if (lane < p.k) {
+            slot[t * p.k + lane] = (short)chosen;
+            if (chosen >= 0) atomicOr(&mask[chosen][t >> 5], 1u << (t & 31));
         }
-        __builtin_amdgcn_wave_barrier();
+    };
+    unsigned again = 0;  // of this wave's tokens, those to be done in 64 bits
+    load(w, ahead);
+    for (int i = 0; i < p.tokens / kWaves; ++i) {
+        const int t = w + kWaves * i;
+        if (t0 + t >= p.T) break;
+#pragma unroll
+        for (int r = 0; r < R; ++r) l[r] = ahead[r];
+        load(t + kWaves, ahead);
+        const int chosen = route_token<X, R>(p, t0 + t, l, group, per, shift, rows[w], bias);
+        if (__builtin_amdgcn_readfirstlane(chosen) == kExact) again |= 1u << i;
+        else keep(t, chosen);
     }
+    for (int i = 0; again >> i; ++i)
+        if (again >> i & 1) keep(w + kWaves * i, route_token_exact<X, R>(p, t0 + w + kWaves * i));
     __syncthreads();
-    // of the waves before; this workgroup's count of expert e
-    unsigned total_e = 0;
-    const int e = threadIdx.x;
-    if (e < 64 * R)
-        for (int i = 0; i < kWaves; ++i) {
-            const unsigned n = count[i][e];
-            count[i][e] = (unsigned char)total_e;  // at most 64 - 4
-            total_e += n;
-        }
+    const unsigned count = e < p.E ? __popc(mask[e][0]) + __popc(mask[e][1]) : 0;
     if constexpr (ALL) {
         unsigned total;
-        const unsigned at = block_scan<kWaves>(e < p.E ? total_e : 0, part, total);
+        const unsigned at = block_scan<kWaves>(count, part, total);
         if (e < p.E) {
             first[e] = at;
             p.offsets[e] = at;
         }
         if (e == 0) p.offsets[p.E] = total;
+        __syncthreads();
     } else if (e < p.E) {
-        p.ws[bid * p.E + e] = (int)total_e;
+        p.ws[linear_block() * p.E + e] = (int)count;
     }
-    __syncthreads();
-    for (int c = 0; c < slots; c += 64) {
-        const int i = c + lane;
-        if (i >= slots || t0 * p.k + base + i >= (int64_t)p.T * p.k) continue;
-        const int x = slot[base + i];
-        int *row = p.rows + t0 * p.k + base + i;
-        *row = x < 0 ? -1 : *row + count[w][x] + (ALL ? (int)first[x] : 0);
+    const int slots = (int)min((int64_t)p.tokens, p.T - t0) * p.k;
+    for (int i = threadIdx.x; i < slots; i += 64 * kWaves) {
+        const int x = slot[i], t = i / p.k;
+        int row = -1;
+        if (x >= 0) {
+            row = t < 32 ? __popc(mask[x][0] & ((1u << t) - 1))
+                         : __popc(mask[x][0]) + __popc(mask[x][1] & ((1u << (t - 32)) - 1));
+            if (ALL) row += (int)first[x];
+        }
+        p.rows[t0 * p.k + i] = row;
     }
 }
 
-// The workgroups' counts -> their first rows; offsets. One workgroup; `blocks` of the kernel before.
+// The workgroups' counts of an expert -> those of the workgroups before; the experts' totals behind them.
+// A workgroup takes 64 experts, 16 threads each.
 __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs p, int blocks)
 {
-    __shared__ unsigned sums[1024], part[16];
-    // 1024 / W threads to an expert, W = E rounded up to a power of two
-    int W = 1;
-    while (W < p.E) W *= 2;
-    const int parts = 1024 / W, e = threadIdx.x % W, q = threadIdx.x / W;
-    const int lo = (int)((int64_t)blocks * q / parts), hi = (int)((int64_t)blocks * (q + 1) / parts);
+    __shared__ unsigned sums[16][64];
+    const int x = threadIdx.x & 63, q = threadIdx.x >> 6, e = blockIdx.x * 64 + x;
+    const bool live = e < p.E;
+    constexpr int U = 16;
+    const int each = (blocks + 15) / 16, lo = min(q * each, blocks), hi = min(lo + each, blocks);
     unsigned sum = 0;
-    if (e < p.E)
-        for (int b = lo; b < hi; ++b) sum += (unsigned)p.ws[(int64_t)b * p.E + e];
-    sums[threadIdx.x] = sum;
-    __syncthreads();
-    unsigned before = 0, all = 0;
-    for (int i = 0; i < parts; ++i) {
-        const unsigned v = sums[i * W + e];
-        before += i < q ? v : 0;
-        all += v;
+    for (int b = lo; b < hi; b += U) {
+        unsigned v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = live && b + i < hi ? (unsigned)p.ws[(int64_t)(b + i) * p.E + e] : 0u;
+#pragma unroll
+        for (int i = 0; i < U; ++i) sum += v[i];
     }
+    sums[q][x] = sum;
     __syncthreads();
-    unsigned total;
-    const unsigned first = block_scan<16>(q == 0 ? all : 0, part, total);  // of thread e: expert e
-    if (q == 0) sums[e] = first;
-    __syncthreads();
-    unsigned at = sums[e] + before;
-    if (e < p.E) {
-        if (q == 0) p.offsets[e] = first;
-        for (int b = lo; b < hi; ++b) {
-            int *c = p.ws + (int64_t)b * p.E + e;
-            const unsigned n = (unsigned)*c;
-            *c = (int)at;
-            at += n;
+    unsigned at = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        at += i < q ? sums[i][x] : 0;
+        all += sums[i][x];
+    }
+    if (!live) return;
+    if (q == 0) p.ws[(int64_t)blocks * p.E + e] = (int)all;
+    for (int b = lo; b < hi; b += U) {
+        unsigned v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = b + i < hi ? (unsigned)p.ws[(int64_t)(b + i) * p.E + e] : 0u;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (b + i < hi) p.ws[(int64_t)(b + i) * p.E + e] = (int)at;
+            at += v[i];
         }
     }
-    if (threadIdx.x == 0) p.offsets[p.E] = total;
 }
 
-__global__ __launch_bounds__(256) void route_rows_kernel(RouteArgs p)
+// A workgroup's tokens: rows from their numbers in it; offsets. FEW: the counts as route_kernel left
+// them, else as the scan did.
+template <bool FEW>
+__global__ __launch_bounds__(1024) void route_rows_kernel(RouteArgs p, int blocks)
 {
-    const int64_t i = linear_block() * 256 + threadIdx.x;
-    if (i >= (int64_t)p.T * p.k) return;
-    const int e = p.experts[i];
-    if (e >= 0) p.rows[i] += p.ws[i / (kTokens * p.k) * p.E + e];
+    __shared__ unsigned first[kRouteMaxExperts], part[16];
+    const int64_t bid = linear_block();
+    if (bid >= blocks) return;
+    const int e = threadIdx.x;
+    unsigned all = 0, before = 0;
+    if (e < p.E) {
+        if constexpr (FEW) {
+#pragma unroll
+            for (int b = 0; b < kFewBlocks; ++b) {
+                const unsigned v = b < blocks ? (unsigned)p.ws[b * p.E + e] : 0u;
+                before += b < bid ? v : 0u;
+                all += v;
+            }
+        } else {
+            before = (unsigned)p.ws[bid * p.E + e];
+            all = (unsigned)p.ws[(int64_t)blocks * p.E + e];
+        }
+    }
+    unsigned total;
+    const unsigned at = block_scan<16>(all, part, total);
+    if (e < p.E) {
+        first[e] = at + before;
+        if (bid == 0) p.offsets[e] = at;
+    }
+    if (bid == 0 && e == 0) p.offsets[p.E] = total;
+    __syncthreads();
+    const int64_t t0 = bid * p.tokens;
+    const int slots = (int)min((int64_t)p.tokens, p.T - t0) * p.k;
+    for (int i = threadIdx.x; i < slots; i += 1024) {
+        const int x = p.experts[t0 * p.k + i];
+        if (x >= 0) p.rows[t0 * p.k + i] += (int)first[x];
+    }
 }
 
 // dl_e of one token by one wave: with g_e the gradient of s_e (0 where e was not chosen),
@@ -421,21 +782,26 @@ hipError_t with_route(int type, int E, F &&f)
 
 }  // namespace
 
+// Tokens of a workgroup: one to a wave, so that more CUs take part, or four where all of them have work
+// (4001 tokens of 60 experts: 15 us with 64, 5 with 16).
+static int tokens_of(int64_t T) { return T <= 32 || T > 8192 ? kTokens : kWaves; }
+
 int64_t route_ws_ints(int64_t T, int E, int k)
 {
     (void)k;
-    const int64_t blocks = (T + kTokens - 1) / kTokens;
-    return blocks > 1 ? blocks * E : 0;
+    const int64_t tokens = tokens_of(T), blocks = (T + tokens - 1) / tokens;
+    return blocks > 1 ? (blocks + 1) * E : 0;
 }
 
 hipError_t route_launch(const RouteArgs &a, hipStream_t stream)
 {
     RouteArgs arg = a;
-    const int64_t blocks = ((int64_t)a.T + kTokens - 1) / kTokens;
+    arg.tokens = tokens_of(a.T);
+    int blocks = (int)(((int64_t)a.T + arg.tokens - 1) / arg.tokens);
     unsigned gx, gy;
     if (!grid_for(blocks, gx, gy)) return hipErrorInvalidConfiguration;
     void *args[] = {&arg};
-    const hipError_t e = with_route(a.type, a.E, [&](auto x, auto r) {
+    hipError_t e = with_route(a.type, a.E, [&](auto x, auto r) {
         typedef decltype(x) X;
         constexpr int R = decltype(r)::value;
         const void *fn = blocks == 1 ? reinterpret_cast<const void *>(&route_kernel<X, R, true>)
@@ -443,13 +809,16 @@ hipError_t route_launch(const RouteArgs &a, hipStream_t stream)
         return hipLaunchKernel(fn, dim3(gx, gy), dim3(64 * kWaves), args, 0, stream);
     });
     if (e != hipSuccess || blocks == 1) return e;
-    int n = (int)blocks;
-    void *scan_args[] = {&arg, &n};
-    const hipError_t s = hipLaunchKernel(reinterpret_cast<const void *>(&route_scan_kernel), dim3(1), dim3(1024), scan_args,
-                                         0, stream);
-    if (s != hipSuccess) return s;
-    if (!grid_for(((int64_t)a.T * a.k + 255) / 256, gx, gy)) return hipErrorInvalidConfiguration;
-    return hipLaunchKernel(reinterpret_cast<const void *>(&route_rows_kernel), dim3(gx, gy), dim3(256), args, 0, stream);
+    void *more[] = {&arg, &blocks};
+    const bool few = blocks <= kFewBlocks;
+    if (!few) {
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&route_scan_kernel), dim3((a.E + 63) / 64), dim3(1024), more, 0,
+                            stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipLaunchKernel(few ? reinterpret_cast<const void *>(&route_rows_kernel<true>)
+                               : reinterpret_cast<const void *>(&route_rows_kernel<false>),
+                           dim3(gx, gy), dim3(1024), more, 0, stream);
 }
 
 hipError_t route_grad_launch(const RouteGradArgs &a, hipStream_t stream)
