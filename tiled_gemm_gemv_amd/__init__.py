@@ -572,15 +572,18 @@ def _matrix(t, name, dtypes=None):
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    rows, cols = t.shape
-    if t.numel() == 0:  # the strides of an empty tensor are arbitrary, and nothing uses them
+    rows, cols = shape
+    if rows == 0 or cols == 0:  # the strides of an empty tensor are arbitrary, and nothing uses them
         return max(cols, 1)
-    if cols > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    if ld < max(cols, 1):
+    if rows == 1:
+        return cols
+    if ld < cols:
         raise ValueError(f"{name} row stride {ld} is below its width {cols}")
     return ld
 
@@ -772,10 +775,10 @@ def conv2d(x, w, stride=(1, 1), pad=(0, 0), dilation=(1, 1), out=None, config=No
 def _run(name, device, stream, *args):
     """Call the C entry point `name` with `args` and the stream, `device` (an index) current."""
     import torch
-    fn = getattr(load(), name)
+    fn = getattr(_lib or load(), name)
     # the current stream's address without a Stream object around it (2.9 us of a 12 us call)
     s = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:  # as torch.cuda.current_device(), initialised with the tensors
         status = fn(*args, s)
     else:
         with torch.cuda.device(device):
@@ -1154,7 +1157,7 @@ def route_topk(logits, k, scoring="softmax", bias=None, groups=1, top_groups=1, 
     how = _scoring(scoring)
     if bias is not None:
         _scale(bias, (E,), "bias", device)
-    need = mm_route_topk_workspace_bytes(T, E, k)
+    need = (_lib or load()).mm_route_topk_workspace_bytes(T, E, k)
     if need < 0:
         raise ValueError(f"invalid sizes: {T} tokens, {k} of {E} experts")
     if workspace is not None:
@@ -1264,9 +1267,10 @@ def combine_rows_grad(dout, y, rows, weights, out=None, stream=None):
         raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(T, D)}")
     _slots(rows, (T, k), torch.int32, "rows", device)
     _slots(weights, (T, k), torch.float32, "weights", device)
+    y_type = _mm_type(y.dtype, "y")
     out, _, lddy, _ = _output(out, y.dtype, (total, D), y)
     dweights = y.new_empty((T, k), dtype=torch.float32)
     _run("mm_combine_rows_grad", device, stream, T, k, D, dout.data_ptr(), _mm_type(dout.dtype, "dout"), ldg,
-         y.data_ptr(), _mm_type(y.dtype, "y"), ldy, total, rows.data_ptr(), weights.data_ptr(), out.data_ptr(), lddy,
+         y.data_ptr(), y_type, ldy, total, rows.data_ptr(), weights.data_ptr(), out.data_ptr(), lddy,
          dweights.data_ptr())
     return out, dweights

@@ -18,6 +18,8 @@
 namespace mm {
 namespace {
 
+typedef unsigned int AnyWords __attribute__((ext_vector_type(4), aligned(1)));  // at any address
+
 constexpr int kUnit = 8;      // elements of a lane
 constexpr int kUnits = 4;     // units of a lane, 256 apart
 constexpr int kThreads = 256;
@@ -71,6 +73,12 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(Mx4Args p)
         int64_t row;
         unsigned unit;
         const bool live = units.at(i, row, unit);
+        if (live && (int64_t)(unit + 1) * kUnit <= p.cols) {
+            const AnyWords *x = reinterpret_cast<const AnyWords *>(static_cast<const X *>(p.X) + row * p.ldx + (int64_t)unit * kUnit);
+#pragma unroll
+            for (int c = 0; c < V; ++c) v[i][c] = __builtin_nontemporal_load(x + c);
+            continue;
+        }
         const char *x = static_cast<const char *>(p.X) + (row * p.ldx + (int64_t)unit * kUnit) * (int)sizeof(X);
         const int64_t left = live ? row_bytes - (int64_t)unit * kUnit * (int)sizeof(X) : 0;
 #pragma unroll
@@ -144,12 +152,18 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(Mx4Args p)
         const int64_t col = (int64_t)unit * kUnit;
         X *out = static_cast<X *>(p.X) + row * p.ldx + col;
         if (col + kUnit <= p.cols) {
-            struct __attribute__((packed)) Eight {
+            struct Eight {
                 X v[kUnit];
             } o;
 #pragma unroll
             for (int e = 0; e < kUnit; ++e) o.v[e] = (X)x[e];
-            *reinterpret_cast<Eight *>(out) = o;
+            struct Words {
+                u32x4 w[sizeof(X) / 2];
+            };
+            const Words words = __builtin_bit_cast(Words, o);
+#pragma unroll
+            for (int c = 0; c < (int)sizeof(X) / 2; ++c)
+                __builtin_nontemporal_store(words.w[c], reinterpret_cast<AnyWords *>(out) + c);
         } else {
 #pragma unroll
             for (int e = 0; e < kUnit; ++e)
