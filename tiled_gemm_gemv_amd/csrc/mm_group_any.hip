@@ -179,7 +179,7 @@ int group_select(const GroupArgs &a)
     double time = 1e300;
     constexpr int largest = 0x7fffffff - 1024;  // row and column numbers of a tile fit an int
     if (a.M > largest || a.N > largest || a.K > largest) return kAny;
-    if (!a.grad && a.elem != GroupElem::Mx4)
+    if (!a.grad)
         for (int r : {1, 16, 32, 64}) {
             if (!group_rows_ok(a, r)) continue;
             const double t = group_rows_time(a, r);

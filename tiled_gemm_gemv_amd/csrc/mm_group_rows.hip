@@ -91,6 +91,15 @@ __device__ __forceinline__ bool rows_tile(const GroupArgs &p, int cols, RowTile 
     return true;
 }
 
+// 8 scale bytes from any address.
+__device__ __forceinline__ u32x2 load8(const unsigned char *p)
+{
+    struct __attribute__((packed)) Bytes {
+        u32x2 v;
+    };
+    return reinterpret_cast<const Bytes *>(p)->v;
+}
+
 // B rows along k. W waves, 16 NB columns, slices of 128 bytes of k, J of them in flight.
 template <class E, int RB, int NB, int W, int J>
 __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
@@ -117,11 +126,35 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
     for (int i = 0; i < RB; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = typename E::template Acc<16>{0, 0, 0, 0};
+    // Mx4: a slice's 8 scale bytes of the same rows and columns; this lane's are number lane / 16 and 4 on
+    const unsigned char *sa[RB], *sb[NB];
+    const unsigned pick = (unsigned)(lane >> 4) * 0x0101u | 0x0c0c0400u;
+    if constexpr (is_mx<E>) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i) sa[i] = p.mxa + (int64_t)min(t.row0 + 16 * i + (lane & 15), t.hi - 1) * p.ld_mxa;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            sb[j] = p.mxb + t.g * p.stride_mxb + min((int64_t)n0 + 16 * j + (lane & 15), (int64_t)p.N - 1) * p.ld_mxb;
+    }
+    // MFMA step h of a slice
+    auto mma = [&](auto h, u32x4 x, unsigned sx, u32x4 y, unsigned sy, typename E::template Acc<16> c) {
+        if constexpr (is_mx<E>) return E::template mma<16, decltype(h)::value, decltype(h)::value>(x, sx, y, sy, c);
+        else return E::template mma<16>(x, y, c);
+    };
+    using H0 = std::integral_constant<int, 0>;
+    using H1 = std::integral_constant<int, 1>;
 
     const int64_t whole = kb / 128;  // whole slices; wave w takes w, w + W, ...
     u32x4 av[J][2][RB], bv[J][2][NB];
+    u32x2 as[J][RB] = {}, bs[J][NB] = {};
     int64_t s = w;
     auto load = [&](int x, int64_t slice) {
+        if constexpr (is_mx<E>) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) bs[x][j] = load8(sb[j] + slice * 8);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) as[x][i] = load8(sa[i] + slice * 8);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -131,12 +164,21 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
         }
     };
     auto multiply = [&](int x) {
+        unsigned p[RB] = {}, q[NB] = {};
+        if constexpr (is_mx<E>) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < RB; ++i) p[i] = __builtin_amdgcn_perm(as[x][i][1], as[x][i][0], pick);
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
+            for (int j = 0; j < NB; ++j) q[j] = __builtin_amdgcn_perm(bs[x][j][1], bs[x][j][0], pick);
+        }
 #pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] = E::template mma<16>(av[x][h][i], bv[x][h][j], acc[i][j]);
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) acc[i][j] = mma(H0(), av[x][0][i], p[i], bv[x][0][j], q[j], acc[i][j]);
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) acc[i][j] = mma(H1(), av[x][1][i], p[i], bv[x][1][j], q[j], acc[i][j]);
     };
     // J slices loaded ahead; a slice is multiplied, then its registers take the slice J further on
     if (whole > 0) {
@@ -157,13 +199,19 @@ __global__ __launch_bounds__(64 * W) void rows_kernel_d(GroupArgs p)
         for (int h = 0; h < 2; ++h) {
             const int valid = (int)(kb - at) - 64 * h - 16 * (lane >> 4);
             u32x4 aa[RB];
+            unsigned p[RB] = {}, q = 0;  // Mx4: of a block, 16 bytes; past the last zeros of scale 1
+            const int64_t block = whole * 8 + 4 * h + (lane >> 4);
 #pragma unroll
-            for (int i = 0; i < RB; ++i) aa[i] = load16_upto<T>(a[i] + at + 64 * h, valid, kb);
+            for (int i = 0; i < RB; ++i) {
+                aa[i] = load16_upto<T>(a[i] + at + 64 * h, valid, kb);
+                if constexpr (is_mx<E>) p[i] = valid > 0 ? sa[i][block] : 127u;
+            }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const u32x4 bb = load16_upto<T>(b[j] + at + 64 * h, valid, kb);
+                if constexpr (is_mx<E>) q = valid > 0 ? sb[j][block] : 127u;
 #pragma unroll
-                for (int i = 0; i < RB; ++i) acc[i][j] = E::template mma<16>(aa[i], bb, acc[i][j]);
+                for (int i = 0; i < RB; ++i) acc[i][j] = mma(H0(), aa[i], p[i], bb, q, acc[i][j]);
             }
         }
     }
@@ -449,7 +497,8 @@ hipError_t rows_dot(const GroupArgs &a, hipStream_t stream)
 template <class E>
 hipError_t rows_d(const GroupArgs &a, int rows, hipStream_t stream)
 {
-    if (rows == 1) return rows_dot<E>(a, stream);
+    if constexpr (!is_mx<E>)
+        if (rows == 1) return rows_dot<E>(a, stream);
     const bool wide = strip_columns(a, rows) == 32;
     if (rows == 16) return wide ? launch_d<E, 1, 2, 4, 2>(a, stream) : launch_d<E, 1, 1, 4, 4>(a, stream);
     if (rows == 32) return wide ? launch_d<E, 2, 2, 4, 2>(a, stream) : launch_d<E, 2, 1, 4, 4>(a, stream);
@@ -479,8 +528,12 @@ bool group_rows_ok(const GroupArgs &a, int rows)
     // rows share comes from L2 again), and of 8-bit elements 1 KB of it, of 16-bit ones more than 2.
     // Against the other kernels, cold, rows at random: 8-bit 0.6-1.2 times their time (5 rows, 27 groups
     // of 8496 x 6448: 45 us and 54); 16-bit 0.55-1.3 (one row of 6880 x 6064: 18 us and 32), up to 2 KB
-    // 0.8-1.6 (2 rows, 3 groups of 2173 x 900: 8.6 us and 5.4), most of it in partial loads.
-    if (rows == 1) return a.trans_b && a.M <= 1.25 * expected_groups(a) && a.K >= (a.elem == GroupElem::I8 ? 1024 : 1025);
+    // 0.8-1.6 (2 rows, 3 groups of 2173 x 900: 8.6 us and 5.4), most of it in partial loads. 4-bit rows
+    // never: unpacking and scaling them by vector instructions (8 rows for 8 of 64 groups of 4096 x 2048: 17
+    // us, 10 through the MFMA).
+    if (rows == 1)
+        return a.trans_b && a.elem != GroupElem::Mx4 && a.M <= 1.25 * expected_groups(a) &&
+               a.K >= (a.elem == GroupElem::I8 ? 1024 : 1025);
     return a.trans_b || a.N >= (rows == 64 ? 4 : 2);  // a lane's columns of B rows across k
 }
 
@@ -490,7 +543,7 @@ bool group_rows_ok(const GroupArgs &a, int rows)
 // its latency and its sums' join.
 double group_rows_time(const GroupArgs &a, int rows)
 {
-    const int es = a.elem == GroupElem::I8 ? 1 : 2;
+    const int es = group_elem_size(a);
     const double unaligned = aligned_words(a) ? 1.0 : 2.2;
     if (rows == 1) return 3.5 + a.M * (double)a.N * a.K * es / 5.8e6 * unaligned;
     const int cols = strip_columns(a, rows), rb = rows / 16;
@@ -509,6 +562,7 @@ int group_rows_columns(const GroupArgs &a, int rows) { return strip_columns(a, r
 hipError_t group_rows_launch(const GroupArgs &a, int rows, hipStream_t stream)
 {
     if (a.elem == GroupElem::I8) return rows_d<ElemI8>(a, rows, stream);
+    if (a.elem == GroupElem::Mx4) return rows_d<ElemMx4>(a, rows, stream);
     if (a.trans_b)
         return a.elem == GroupElem::F16 ? rows_d<ElemF16>(a, rows, stream) : rows_d<ElemBf16>(a, rows, stream);
     return a.elem == GroupElem::F16 ? rows_t<ElemF16>(a, rows, stream) : rows_t<ElemBf16>(a, rows, stream);
