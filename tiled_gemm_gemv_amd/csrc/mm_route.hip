@@ -606,6 +606,331 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p)
     }
 }
 
+// ------------------------------------------------------------ four tokens to a wave
+//
+// Up to 256 experts, 12 of them chosen and 16 groups: a token takes a row of 16 lanes, lane q its experts
+// q + 16 r, so that what is done for a token with one instruction is done for four, and maxima need four
+// steps. The same steps as route_token; up to 16 candidates.
+constexpr int kRowExperts = 256, kRowTop = 12, kRowGroups = 16;
+
+// v of the lane I before this one in the row, in a circle.
+template <int I>
+__device__ __forceinline__ unsigned rotate(unsigned v)
+{
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + I, 0xf, 0xf, false);  // row_ror
+}
+template <int I>
+__device__ __forceinline__ float rotate(float v)
+{
+    return __builtin_bit_cast(float, rotate<I>(__builtin_bit_cast(unsigned, v)));
+}
+template <int I>
+__device__ __forceinline__ uint64_t rotate(uint64_t v)
+{
+    return (uint64_t)rotate<I>((unsigned)(v >> 32)) << 32 | rotate<I>((unsigned)v);
+}
+template <int I>
+__device__ __forceinline__ double rotate(double v)
+{
+    return __builtin_bit_cast(double, rotate<I>(__builtin_bit_cast(uint64_t, v)));
+}
+// f(I) for I = 1 .. 15.
+template <int I = 1, class F>
+__device__ __forceinline__ void each_other(F &&f)
+{
+    f(std::integral_constant<int, I>());
+    if constexpr (I < 15) each_other<I + 1>(f);
+}
+// Maximum and sum of the row, in all its lanes.
+__device__ __forceinline__ unsigned row_max(unsigned v)
+{
+    v = max(v, rotate<8>(v));
+    v = max(v, rotate<4>(v));
+    v = max(v, rotate<2>(v));
+    return max(v, rotate<1>(v));
+}
+template <class V>
+__device__ __forceinline__ V row_sum(V v)
+{
+    v += rotate<8>(v);
+    v += rotate<4>(v);
+    v += rotate<2>(v);
+    return v + rotate<1>(v);
+}
+
+// As keep_groups, for each row's token; the bits of a group's lanes in the row.
+template <class V, class F>
+__device__ __forceinline__ unsigned row_keep_groups(const RouteArgs &p, int per, int shift, F &&at, V &value, int &rank)
+{
+    const int lane = threadIdx.x & 63, q = lane & 15, g = q >> shift, e0 = min(g, p.groups - 1) * per;
+    const V none = -__builtin_inff();
+    V first = none, second = none;
+    for (int i = q & ((1 << shift) - 1); i < per; i += 4 << shift) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int x = i + (u << shift);
+            const V v = x < per ? at(e0 + x) : none;
+            second = fmax(second, fmin(first, v));
+            first = fmax(first, v);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2)
+        if (d < 1 << shift) {
+            const V f = other_half(first, d), h = other_half(second, d);
+            second = fmax(fmin(first, f), fmax(second, h));
+            first = fmax(first, f);
+        }
+    value = p.group_top == 1 ? first : second == none ? none : first + second;
+    int above = 0;  // lanes of better groups
+    each_other([&](auto i) {
+        constexpr int I = decltype(i)::value;
+        const V v = rotate<I>(value);
+        const int of = (int)rotate<I>((unsigned)g);
+        above += of < p.groups && (v > value || (v == value && of < g));
+    });
+    rank = above >> shift;
+    return (unsigned)(__ballot(g < p.groups && rank < p.top_groups) >> (lane & 48)) & 0xffffu;
+}
+
+template <class X, int R, int W, bool ALL>
+__global__ __launch_bounds__(64 * W) void route_rows_of_16_kernel(RouteArgs p)
+{
+    constexpr int tokens = 4 * W;
+    static_assert(tokens <= 64 && 16 * R <= 64 * W, "a mask's bits; a thread for each expert");
+    __shared__ unsigned mask[16 * R][2];  // the tokens that take an expert
+    __shared__ short slot[tokens * kRowTop];
+    __shared__ float rows[tokens][16 * R];
+    __shared__ unsigned first[16 * R], part[W];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane & 15, tid = threadIdx.x;
+    const int64_t t0 = linear_block() * tokens;
+    if (t0 >= p.T) return;  // the whole workgroup
+    if (tid < 16 * R) mask[tid][0] = mask[tid][1] = 0;
+    const int token = 4 * w + (lane >> 4);  // in the workgroup
+    const int64_t t = t0 + token;
+    const float inf = __builtin_inff();
+    float *row = rows[token];
+
+    const bool by_score = p.bias, sums = p.groups > 1 && p.group_top == 2;
+    float l[R], c[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)  // no branches: the last one's in the place of others
+        l[r] = load_logit<X>(p.logits, min(t, (int64_t)p.T - 1) * p.ld + min(q + 16 * r, p.E - 1));
+    float bias[R];
+    if (by_score) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) bias[r] = p.bias[min(q + 16 * r, p.E - 1)];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (t >= p.T || q + 16 * r >= p.E) l[r] = -inf;
+    float m = 0.f, total32 = 1.f;
+    double total = 1.0;
+    if (!p.sigmoid) {
+        unsigned top = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) top = max(top, ordered32(l[r]));
+        m = from_ordered32(row_max(top));
+        if (m == -inf) m = 0.f;
+        if (!(m < inf)) m = __builtin_nanf("");
+    }
+    const bool all_scores = !p.sigmoid && (by_score || !p.renormalize);
+    float s[R];
+    if (by_score || sums || all_scores) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            s[r] = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-l[r])) : expf(l[r] - m);
+    }
+    if (all_scores) {
+        if (by_score) {
+            double sum = 0;
+#pragma unroll
+            for (int r = 0; r < R; ++r) sum += exp((double)l[r] - (double)m);
+            total = row_sum(sum);
+            total32 = (float)total;
+        } else {
+            float sum = s[0];
+#pragma unroll
+            for (int r = 1; r < R; ++r) sum += s[r];
+            total = total32 = row_sum(sum);
+        }
+    }
+    if (by_score) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float score = p.sigmoid ? s[r] : total32 == 0.f ? 0.f : s[r] / total32;
+            c[r] = l[r] == -inf ? -inf : score + bias[r];
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) c[r] = l[r];
+    }
+    bool exact = false;  // the same in a row's lanes, like all below
+    unsigned kept = 0xffffu;
+    int shift = 0, per = p.E;
+    unsigned inverse = 0;  // e / per = e inverse >> 16: e < 256 times less than 1 too much is below 2^16 / per
+    if (p.groups > 1) {
+        per = __builtin_amdgcn_readfirstlane(p.E / p.groups);
+        inverse = __builtin_amdgcn_readfirstlane((65535 + per) / per);
+        while (2 * p.groups << shift <= 16) ++shift;
+        bool odd = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float v = by_score || !sums ? c[r] : l[r] == -inf ? -inf : s[r];
+            odd |= !(v < inf);
+            row[q + 16 * r] = v;
+        }
+        exact = (__ballot(odd) >> (lane & 48) & 0xffffu) != 0;
+        __builtin_amdgcn_wave_barrier();
+        float value;
+        int rank;
+        kept = row_keep_groups<float>(p, per, shift, [&](int e) { return row[e]; }, value, rank);
+        __builtin_amdgcn_wave_barrier();
+        if (p.top_groups < p.groups && (by_score || sums)) {
+            const float low = from_ordered32(row_max(rank == p.top_groups - 1 && q >> shift < p.groups ? ordered32(value) : 0u));
+            const float next = from_ordered32(row_max(rank == p.top_groups && q >> shift < p.groups ? ordered32(value) : 0u));
+            const bool close = !exact && next > -inf && !(low - next > 4 * slack(low));
+            if (__any(close)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) row[q + 16 * r] = c[r] == -inf ? -inf : l[r];
+                __builtin_amdgcn_wave_barrier();
+                auto wide = [&](int e) {
+                    const double x = row[e];
+                    if (x == -__builtin_inf()) return x;
+                    double v = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)m);
+                    if (by_score) v = (all_scores ? total == 0 ? 0.0 : v / total : v) + (double)p.bias[e];
+                    return v;
+                };
+                double value64;
+                int rank64;
+                const unsigned kept64 = row_keep_groups<double>(p, per, shift, wide, value64, rank64);
+                __builtin_amdgcn_wave_barrier();
+                if (close) kept = kept64;
+            }
+        }
+    }
+    unsigned key[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = q + 16 * r;
+        bool live = c[r] != -inf;
+        if (p.groups > 1) live &= (kept >> ((e * inverse >> 16) << shift & 31) & 1) != 0;
+        key[r] = live ? (ordered32(c[r]) & ~1023u) | (unsigned)(1023 - e) : 0u;
+        row[e] = l[r];
+    }
+    unsigned mine = 0, least = 0;
+    int n = 0;  // picks of the row's token
+    for (int i = 0;; ++i) {
+        unsigned best = key[0];
+#pragma unroll
+        for (int r = 1; r < R; ++r) best = max(best, key[r]);
+        best = row_max(best);
+        const bool live = best > least && !exact;
+        if (!__any(live)) break;
+        if (i == 16) {
+            exact |= live;
+            break;
+        }
+        if (live) {
+            if (q == i) mine = best;
+            n = i + 1;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (key[r] == best) key[r] = 0;
+        if (i == p.k - 1) {
+            if (by_score) {
+                const float v = from_ordered32(best & ~1023u);
+                exact |= live && !(fabsf(v) < inf);
+                least = live ? (ordered32(v - 2 * slack(v)) & ~1023u) - 1 : ~0u;
+            } else if (sizeof(X) == 2) {
+                break;
+            } else {
+                least = live ? (best & ~1023u) - 1 : ~0u;
+            }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    const bool has = q < n;
+    int index = has ? 1023 - (int)(mine & 1023u) : -1;
+    double score = 0;
+    uint64_t rank_value = 0;
+    if (has) {
+        const float x = row[index];
+        score = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)m);
+        if (all_scores) score = total == 0 ? 0.0 : score / total;
+        rank_value = by_score ? ordered(score + (double)p.bias[index]) : (uint64_t)ordered32(x);
+    }
+    if (by_score || sizeof(X) == 4) {
+        const uint64_t next = rotate<15>(rank_value);  // of the lane after this one
+        const int next_index = (int)rotate<15>((unsigned)index);
+        if (__any(q + 1 < n && (next > rank_value || (next == rank_value && next_index < index)))) {
+            int place = 0;
+            each_other([&](auto i) {
+                constexpr int I = decltype(i)::value;
+                const uint64_t v = rotate<I>(rank_value);
+                const int e = (int)rotate<I>((unsigned)index);
+                place += e >= 0 && (v > rank_value || (v == rank_value && e < index));
+            });
+            const uint64_t bits = __builtin_bit_cast(uint64_t, score);
+            const int to = 4 * ((lane & 48) | (has ? place : q));
+            index = __builtin_amdgcn_ds_permute(to, index);
+            const unsigned lo = (unsigned)__builtin_amdgcn_ds_permute(to, (int)bits);
+            const unsigned hi = (unsigned)__builtin_amdgcn_ds_permute(to, (int)(bits >> 32));
+            score = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+        }
+    }
+    if (q >= p.k || q >= n) {
+        index = -1;
+        score = 0;
+    }
+    if (p.renormalize) {
+        const double sum = row_sum(score);
+        score = sum == 0 || index < 0 ? 0.0 : score / sum;
+    }
+    __syncthreads();  // the masks are clear
+    auto keep = [&](int of, int chosen) {
+        slot[of] = (short)chosen;
+        if (chosen >= 0) atomicOr(&mask[chosen][of / p.k >> 5], 1u << (of / p.k & 31));
+    };
+    if (q < p.k && t < p.T && !exact) {
+        p.weights[t * p.k + q] = (float)(score * (double)p.scale);
+        p.experts[t * p.k + q] = index;
+        keep(token * p.k + q, index);
+    }
+    const unsigned long long again = __ballot(exact && t < p.T);
+    for (int i = 0; i < 4; ++i)
+        if (again >> (16 * i) & 1) {
+            const int chosen = route_token_exact<X, (R + 3) / 4>(p, t0 + 4 * w + i);
+            if (lane < p.k) keep((4 * w + i) * p.k + lane, chosen);
+        }
+    __syncthreads();
+    const unsigned count = tid < p.E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
+    if constexpr (ALL) {
+        unsigned all;
+        const unsigned at = block_scan<W>(count, part, all);
+        if (tid < p.E) {
+            first[tid] = at;
+            p.offsets[tid] = at;
+        }
+        if (tid == 0) p.offsets[p.E] = all;
+        __syncthreads();
+    } else if (tid < p.E) {
+        p.ws[linear_block() * p.E + tid] = (int)count;
+    }
+    const int slots = (int)min((int64_t)tokens, p.T - t0) * p.k;
+    for (int i = tid; i < slots; i += 64 * W) {
+        const int x = slot[i], of = i / p.k;
+        int r = -1;
+        if (x >= 0) {
+            r = of < 32 ? __popc(mask[x][0] & ((1u << of) - 1))
+                        : __popc(mask[x][0]) + __popc(mask[x][1] & ((1u << (of - 32)) - 1));
+            if (ALL) r += (int)first[x];
+        }
+        p.rows[t0 * p.k + i] = r;
+    }
+}
+
 // The workgroups' counts of an expert -> those of the workgroups before; the experts' totals behind them.
 // A workgroup takes 64 experts, 16 threads each.
 __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs p, int blocks)
@@ -615,11 +940,13 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs p, int block
     const bool live = e < p.E;
     constexpr int U = 16;
     const int each = (blocks + 15) / 16, lo = min(q * each, blocks), hi = min(lo + each, blocks);
-    unsigned sum = 0;
-    for (int b = lo; b < hi; b += U) {
-        unsigned v[U];
+    unsigned v[U], sum = 0;
+    auto load = [&](int b) {
 #pragma unroll
         for (int i = 0; i < U; ++i) v[i] = live && b + i < hi ? (unsigned)p.ws[(int64_t)(b + i) * p.E + e] : 0u;
+    };
+    for (int b = lo; b < hi; b += U) {
+        load(b);
 #pragma unroll
         for (int i = 0; i < U; ++i) sum += v[i];
     }
@@ -634,9 +961,7 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs p, int block
     if (!live) return;
     if (q == 0) p.ws[(int64_t)blocks * p.E + e] = (int)all;
     for (int b = lo; b < hi; b += U) {
-        unsigned v[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) v[i] = b + i < hi ? (unsigned)p.ws[(int64_t)(b + i) * p.E + e] : 0u;
+        if (each > U) load(b);  // else they are still there
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (b + i < hi) p.ws[(int64_t)(b + i) * p.E + e] = (int)at;
@@ -654,6 +979,14 @@ __global__ __launch_bounds__(1024) void route_rows_kernel(RouteArgs p, int block
     const int64_t bid = linear_block();
     if (bid >= blocks) return;
     const int e = threadIdx.x;
+    const int64_t s0 = bid * p.tokens * p.k;
+    const int slots = (int)min((int64_t)p.tokens * p.k, (int64_t)p.T * p.k - s0);
+    // the first slot of this thread, loaded ahead
+    int x = -1, row = -1;
+    if (e < slots) {
+        x = p.experts[s0 + e];
+        row = p.rows[s0 + e];
+    }
     unsigned all = 0, before = 0;
     if (e < p.E) {
         if constexpr (FEW) {
@@ -676,11 +1009,10 @@ __global__ __launch_bounds__(1024) void route_rows_kernel(RouteArgs p, int block
     }
     if (bid == 0 && e == 0) p.offsets[p.E] = total;
     __syncthreads();
-    const int64_t t0 = bid * p.tokens;
-    const int slots = (int)min((int64_t)p.tokens, p.T - t0) * p.k;
-    for (int i = threadIdx.x; i < slots; i += 1024) {
-        const int x = p.experts[t0 * p.k + i];
-        if (x >= 0) p.rows[t0 * p.k + i] += (int)first[x];
+    if (x >= 0) p.rows[s0 + e] = row + (int)first[x];
+    for (int i = e + 1024; i < slots; i += 1024) {
+        const int y = p.experts[s0 + i];
+        if (y >= 0) p.rows[s0 + i] += (int)first[y];
     }
 }
 
@@ -764,6 +1096,15 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p)
     }
 }
 
+// f(X()) with the type of number t (MM_TYPE_*).
+template <class F>
+void with_type(int t, F &&f)
+{
+    if (t == 0) f(float());
+    else if (t == 1) f(__bf16());
+    else f(_Float16());
+}
+
 // f(X(), R) with the logits' type and the registers of E experts in a wave.
 template <class F>
 hipError_t with_route(int type, int E, F &&f)
@@ -782,32 +1123,66 @@ hipError_t with_route(int type, int E, F &&f)
 
 }  // namespace
 
-// Tokens of a workgroup: one to a wave, so that more CUs take part, or four where all of them have work
-// (4001 tokens of 60 experts: 15 us with 64, 5 with 16).
-static int tokens_of(int64_t T) { return T <= 32 || T > 8192 ? kTokens : kWaves; }
+// Whether a call takes four tokens to a wave.
+static bool rows_of_16(int64_t E, int64_t k, int64_t groups) { return E <= kRowExperts && k <= kRowTop && groups <= kRowGroups; }
+
+// Tokens of a workgroup. Four to a wave: 4 waves, so that more CUs take part, or 16 where all of them have
+// work. Else one to a wave of 16, or four after each other (4001 tokens of 60 experts one by one: 15 us with
+// 64 to a workgroup, 7 with 16). One workgroup saves a launch.
+static int tokens_of(int64_t T, int64_t E, int64_t k, int64_t groups)
+{
+    if (rows_of_16(E, k, groups)) return T <= 16 || (T > 64 && T <= 8192) ? 16 : 64;
+    return T <= 32 || T > 8192 ? kTokens : kWaves;
+}
 
 int64_t route_ws_ints(int64_t T, int E, int k)
 {
-    (void)k;
-    const int64_t tokens = tokens_of(T), blocks = (T + tokens - 1) / tokens;
-    return blocks > 1 ? (blocks + 1) * E : 0;
+    int64_t ints = 0;  // the caller's groups may allow either
+    for (int groups : {1, kRowGroups + 1}) {
+        const int64_t tokens = tokens_of(T, E, k, groups), blocks = (T + tokens - 1) / tokens;
+        const int64_t need = blocks > 1 ? (blocks + 1) * E : 0;
+        ints = need > ints ? need : ints;
+    }
+    return ints;
 }
 
 hipError_t route_launch(const RouteArgs &a, hipStream_t stream)
 {
     RouteArgs arg = a;
-    arg.tokens = tokens_of(a.T);
+    arg.tokens = tokens_of(a.T, a.E, a.k, a.groups);
     int blocks = (int)(((int64_t)a.T + arg.tokens - 1) / arg.tokens);
     unsigned gx, gy;
     if (!grid_for(blocks, gx, gy)) return hipErrorInvalidConfiguration;
     void *args[] = {&arg};
-    hipError_t e = with_route(a.type, a.E, [&](auto x, auto r) {
-        typedef decltype(x) X;
-        constexpr int R = decltype(r)::value;
-        const void *fn = blocks == 1 ? reinterpret_cast<const void *>(&route_kernel<X, R, true>)
-                                     : reinterpret_cast<const void *>(&route_kernel<X, R, false>);
-        return hipLaunchKernel(fn, dim3(gx, gy), dim3(64 * kWaves), args, 0, stream);
-    });
+    const void *fn = nullptr;
+    int threads = 64 * kWaves;
+    if (rows_of_16(a.E, a.k, a.groups)) {
+        threads = 16 * arg.tokens;
+        with_type(a.type, [&](auto x) {
+            auto sized = [&](auto r) {
+                typedef decltype(x) X;
+                constexpr int R = decltype(r)::value;
+                if (arg.tokens == 16)
+                    fn = blocks == 1 ? reinterpret_cast<const void *>(&route_rows_of_16_kernel<X, R, 4, true>)
+                                     : reinterpret_cast<const void *>(&route_rows_of_16_kernel<X, R, 4, false>);
+                else
+                    fn = blocks == 1 ? reinterpret_cast<const void *>(&route_rows_of_16_kernel<X, R, 16, true>)
+                                     : reinterpret_cast<const void *>(&route_rows_of_16_kernel<X, R, 16, false>);
+            };
+            if (a.E <= 64) sized(std::integral_constant<int, 4>());
+            else if (a.E <= 128) sized(std::integral_constant<int, 8>());
+            else sized(std::integral_constant<int, 16>());
+        });
+    } else {
+        (void)with_route(a.type, a.E, [&](auto x, auto r) {
+            typedef decltype(x) X;
+            constexpr int R = decltype(r)::value;
+            fn = blocks == 1 ? reinterpret_cast<const void *>(&route_kernel<X, R, true>)
+                             : reinterpret_cast<const void *>(&route_kernel<X, R, false>);
+            return hipSuccess;
+        });
+    }
+    hipError_t e = hipLaunchKernel(fn, dim3(gx, gy), dim3(threads), args, 0, stream);
     if (e != hipSuccess || blocks == 1) return e;
     void *more[] = {&arg, &blocks};
     const bool few = blocks <= kFewBlocks;
