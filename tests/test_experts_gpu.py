@@ -520,3 +520,74 @@ def test_layer_captured_and_replayed(dev):
         torch.cuda.synchronize()
         for _, result in graphs:
             assert all(torch.equal(a, b) for a, b in zip(result, want)), i
+
+
+# --------------------------------------------------------- sizes at the kernels' borders, far rows
+
+@pytest.mark.parametrize("T,E,k,how", [
+    (17, 64, 4, {}), (40, 200, 12, dict(renormalize=True)), (64, 33, 5, dict(scoring="sigmoid")),
+    (50, 256, 13, {}), (50, 257, 8, {}), (70, 256, 12, dict(groups=16, top_groups=5, group_top=2)),
+    (70, 136, 6, dict(groups=17, top_groups=3, group_top=2)), (1025, 48, 3, dict(renormalize=True)),
+    (8192, 16, 2, {}), (8193, 16, 2, {}), (8200, 300, 2, {}), (9001, 130, 2, dict(groups=2)), (1000, 700, 3, {})])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_borders(dev, T, E, k, how, biased):
+    """Sizes on both sides of where another kernel or another number of launches takes over."""
+    rng = np.random.default_rng(T + E)
+    x = logits_of(rng, T, E, "f32", dev)
+    x[T - T // 9:] = -float("inf")
+    bias = torch.from_numpy((0.05 * rng.standard_normal(E)).astype(np.float32)) if biased else None
+    got = mm.route_topk(x, k, bias=bias.to(dev) if biased else None, **how)
+    check_route(x, got, bias=bias.double().numpy() if biased else None, **how)
+
+
+@pytest.mark.parametrize("E", [100, 600])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_many_alike(dev, E, biased):
+    """More experts next to the border than a token's candidates have room for, all equal or nearly:
+    those tokens among others."""
+    rng = np.random.default_rng(E)
+    T, k = 90, 6
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    x[::7] = 0.75
+    near = np.nextafter(np.float32(0.75), np.float32(1)) if not biased else np.float32(0.75) + np.float32(2.0 ** -20)
+    x[3::7] = np.where(rng.random((x[3::7].shape)) < 0.5, np.float32(0.75), near)
+    x = torch.from_numpy(x).to(dev)
+    bias = torch.zeros(E) if biased else None
+    for how in (dict(scoring="sigmoid", renormalize=True), dict(groups=E // 50, top_groups=1, group_top=2, renormalize=True)):
+        got = mm.route_topk(x, k, bias=bias.to(dev) if biased else None, **how)
+        check_route(x, got, bias=bias.double().numpy() if biased else None, **how)
+
+
+def test_rows_past_32_bits(dev):
+    """Rows that start past 2^32 bytes."""
+    D, total = 40000, 60000
+    y = torch.zeros((total, D), dtype=torch.bfloat16, device=dev)
+    rows = torch.tensor([[total - 1, 3], [-1, total - 2], [57000, total]], dtype=torch.int32, device=dev)
+    x = torch.randn(3, D, device=dev).to(torch.bfloat16)
+    mm.spread_rows(x, rows, out=y)
+    w = torch.tensor([[1.0, 2.0], [4.0, 0.5], [-1.0, 8.0]], device=dev)
+    out = mm.combine_rows(y, rows, w, out_dtype=torch.float32)
+    assert torch.equal(out, x.float() * torch.tensor([[3.0], [0.5], [-1.0]], device=dev))
+    dy, dw = mm.combine_rows_grad(x, y, rows, w, out=y.clone())
+    for t, j, r in ((0, 0, total - 1), (0, 1, 3), (1, 1, total - 2), (2, 0, 57000)):
+        assert torch.equal(dy[r], (x[t].float() * w[t, j]).to(torch.bfloat16))
+    assert dw[1, 0] == 0 and dw[2, 1] == 0 and float(dw[0, 0]) > 0
+
+
+def test_two_streams_at_once(dev):
+    """The same calls on two streams side by side, each with a workspace of its own."""
+    rng = np.random.default_rng(31)
+    xs = [logits_of(rng, 3000, 96, "f32", dev) for _ in range(2)]
+    how = dict(scoring="sigmoid", renormalize=True)
+    want = [mm.route_topk(x, 6, **how) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(mm.route_topk(xs[i], 6, **how))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))

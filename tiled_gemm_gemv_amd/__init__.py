@@ -997,6 +997,12 @@ def gemm_i8_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, s
 def _bytes_matrix(t, shape, name, device):
     """Leading dimension of a uint8 matrix of the given shape."""
     import torch
+    if isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.shape == shape and t.get_device() == device:
+        rows, cols = shape
+        if rows > 1 and cols > 1:  # the common case, with few questions
+            ld, unit = t.stride()
+            if unit == 1 and ld >= cols:
+                return ld
     ld = _matrix(t, name, (torch.uint8,))
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
