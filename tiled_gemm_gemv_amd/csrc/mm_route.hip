@@ -309,7 +309,7 @@ __device__ __forceinline__ unsigned long long keep_groups(const RouteArgs &p, in
     int rank = 0;
     for (int i = 0; i < p.groups; ++i) {
         const V v = readlane(value, i << shift);
-        rank += v > value || (v == value && i < g);
+        rank += (v > value) | ((v == value) & (i < g));
     }
     const unsigned long long a = __ballot(rank == p.top_groups - 1 && g < p.groups);
     const unsigned long long b = __ballot(rank == p.top_groups && g < p.groups);
@@ -484,7 +484,7 @@ __device__ __forceinline__ int route_token(const RouteArgs &p, int64_t t, const 
             for (int i = 0; i < n; ++i) {
                 const uint64_t v = readlane_u64(rank_value, i);
                 const int e = __builtin_amdgcn_readlane(index, i);
-                place += v > rank_value || (v == rank_value && e < index);
+                place += (v > rank_value) | ((v == rank_value) & (e < index));
             }
             // lane `place` takes this lane's: push
             const uint64_t bits = __builtin_bit_cast(uint64_t, score);
@@ -687,7 +687,7 @@ __device__ __forceinline__ unsigned row_keep_groups(const RouteArgs &p, int per,
         constexpr int I = decltype(i)::value;
         const V v = rotate<I>(value);
         const int of = (int)rotate<I>((unsigned)g);
-        above += of < p.groups && (v > value || (v == value && of < g));
+        above += (of < p.groups) & ((v > value) | ((v == value) & (of < g)));  // no branches
     });
     rank = above >> shift;
     return (unsigned)(__ballot(g < p.groups && rank < p.top_groups) >> (lane & 48)) & 0xffffu;
@@ -864,13 +864,13 @@ __global__ __launch_bounds__(64 * W) void route_rows_of_16_kernel(RouteArgs p)
     if (by_score || sizeof(X) == 4) {
         const uint64_t next = rotate<15>(rank_value);  // of the lane after this one
         const int next_index = (int)rotate<15>((unsigned)index);
-        if (__any(q + 1 < n && (next > rank_value || (next == rank_value && next_index < index)))) {
+        if (__any((q + 1 < n) & ((next > rank_value) | ((next == rank_value) & (next_index < index))))) {
             int place = 0;
             each_other([&](auto i) {
                 constexpr int I = decltype(i)::value;
                 const uint64_t v = rotate<I>(rank_value);
                 const int e = (int)rotate<I>((unsigned)index);
-                place += e >= 0 && (v > rank_value || (v == rank_value && e < index));
+                place += (e >= 0) & ((v > rank_value) | ((v == rank_value) & (e < index)));
             });
             const uint64_t bits = __builtin_bit_cast(uint64_t, score);
             const int to = 4 * ((lane & 48) | (has ? place : q));
@@ -889,20 +889,20 @@ __global__ __launch_bounds__(64 * W) void route_rows_of_16_kernel(RouteArgs p)
         score = sum == 0 || index < 0 ? 0.0 : score / sum;
     }
     __syncthreads();  // the masks are clear
-    auto keep = [&](int of, int chosen) {
-        slot[of] = (short)chosen;
-        if (chosen >= 0) atomicOr(&mask[chosen][of / p.k >> 5], 1u << (of / p.k & 31));
+    auto keep = [&](int of, int j, int chosen) {
+        slot[of * kRowTop + j] = (short)chosen;
+        if (chosen >= 0) atomicOr(&mask[chosen][of >> 5], 1u << (of & 31));
     };
     if (q < p.k && t < p.T && !exact) {
         p.weights[t * p.k + q] = (float)(score * (double)p.scale);
         p.experts[t * p.k + q] = index;
-        keep(token * p.k + q, index);
+        keep(token, q, index);
     }
     const unsigned long long again = __ballot(exact && t < p.T);
     for (int i = 0; i < 4; ++i)
         if (again >> (16 * i) & 1) {
             const int chosen = route_token_exact<X, (R + 3) / 4>(p, t0 + 4 * w + i);
-            if (lane < p.k) keep((4 * w + i) * p.k + lane, chosen);
+            if (lane < p.k) keep(4 * w + i, lane, chosen);
         }
     __syncthreads();
     const unsigned count = tid < p.E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
@@ -918,16 +918,15 @@ __global__ __launch_bounds__(64 * W) void route_rows_of_16_kernel(RouteArgs p)
     } else if (tid < p.E) {
         p.ws[linear_block() * p.E + tid] = (int)count;
     }
-    const int slots = (int)min((int64_t)tokens, p.T - t0) * p.k;
-    for (int i = tid; i < slots; i += 64 * W) {
-        const int x = slot[i], of = i / p.k;
+    if (q < p.k && t < p.T) {
+        const int x = slot[token * kRowTop + q];
         int r = -1;
         if (x >= 0) {
-            r = of < 32 ? __popc(mask[x][0] & ((1u << of) - 1))
-                        : __popc(mask[x][0]) + __popc(mask[x][1] & ((1u << (of - 32)) - 1));
+            r = token < 32 ? __popc(mask[x][0] & ((1u << token) - 1))
+                           : __popc(mask[x][0]) + __popc(mask[x][1] & ((1u << (token - 32)) - 1));
             if (ALL) r += (int)first[x];
         }
-        p.rows[t0 * p.k + i] = r;
+        p.rows[t * p.k + q] = r;
     }
 }
 
