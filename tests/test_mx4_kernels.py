@@ -182,6 +182,28 @@ def test_operands_past_32_bits(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,N,K", [("tile 64x64 in 2", 33, 2048), ("tile 128x128", 100, 512), ("tile 256x256", 256, 2048)])
+def test_last_row_past_32_bits(dev, name, N, K):
+    """Matrices whose last row starts past 2^32 bytes, 100 rows on, in either place: the rows of a tile
+    at the matrix' start go on past its 100th."""
+    rng = np.random.default_rng(K + N)
+    M, ld, distinct = 65536 + 100, 1 << 16, 701
+    a, sa, av = operand(rng, (distinct,), K, 0, dev)
+    b, sb, bv = operand(rng, (N,), K, 0, dev)
+    at = torch.arange(M, device=dev) * 7 % distinct  # rows of `a` and none like its neighbours
+    buf = torch.empty(M * ld, dtype=torch.uint8, device=dev)
+    far = torch.as_strided(buf, (M, K // 2), (ld, 1))
+    far.copy_(a[at])
+    scales = sa[at]
+    k2 = K // 2
+    assert selected(0, M, N, K, far, ld, scales, K // 32, b, k2, 0, sb, K // 32, 0) == name
+    assert selected(0, N, M, K, b, k2, sb, K // 32, far, ld, 0, scales, K // 32, 0) == name
+    want = torch.from_numpy(av @ bv.T).float().to(dev)[at]  # fp32: exact
+    assert torch.equal(mm.gemm_mx4(far, b, scales, sb), want)
+    assert torch.equal(mm.gemm_mx4(b, far, sb, scales), want.t())
+
+
+@pytest.mark.gpu
 def test_most_rows(dev):
     """2^31 - 1 rows of one block: element 0 of each row against element 0 of one column, 1.5 or 6."""
     M = 2 ** 31 - 1

@@ -314,7 +314,9 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         sc_base = sc_of_b ? p.mxb + g * p.stride_mxb + (int64_t)nb0 * p.ld_mxb : p.mxa + (int64_t)mb0 * p.ld_mxa;
         sc_voff = (unsigned)(min(row, last) * (sc_of_b ? p.ld_mxb : p.ld_mxa));
     }
-    const unsigned a_last = (unsigned)((m_end - 1 - mb0) * p.lda), b_last = (unsigned)((p.N - 1 - nb0) * p.ldb);
+    // the last row's offset, or the tile's where the matrix has more (whose offsets may pass 32 bits)
+    const unsigned a_last = (unsigned)(min(m_end - 1 - mb0, T::BM - 1) * p.lda);
+    const unsigned b_last = (unsigned)(min(p.N - 1 - nb0, T::BN - 1) * p.ldb);
     auto offsets_of = [&](int k_first) {
         if constexpr (T::MX) {
             const int r8 = 8 * w + lane / 8;
