@@ -512,7 +512,7 @@ int mm_route_topk_grad(int64_t T, int64_t E, int64_t k, const void *logits, int 
 /*
  * mm_spread_rows: tokens' rows to the experts' order, Y[rows[t][j]] = X[t], as bytes (elements of
  * any type, codes or scales).
- *   T, k, total   0 <= T, k, T k, total <= 2^31 - 1.
+ *   T, k, total   0 <= T, T k, total <= 2^31 - 1, 0 <= k <= 1024.
  *   row_bytes     bytes of a row, 0 .. 2^31 - 1.
  *   X, ldx    T rows, ldx (bytes) >= max(1, row_bytes); Y, ldy: total rows, likewise.
  *   rows      T x k, packed, device memory. Entries outside [0, total) are no row. Rows of Y that

@@ -148,6 +148,8 @@ BAD = [(call, change, why) for call in (quantize, dequantize) for change, why in
     (dict(total=-1), "negative size"),
     (dict(total=1 << 31), "size above"),
     (dict(T=1 << 30, k=2), "T k above"),
+    (dict(k=1025), "1024 slots"),
+    (dict(T=1, k=(1 << 31) - 1), "1024 slots"),
     (dict(rows=None), "rows is NULL"),
     (dict(rows=FAKE + 2), "rows not 4-byte"),
     (dict(Y=None), "Y is NULL"),

@@ -1213,8 +1213,8 @@ def _token_slots(rows):
 
 def spread_rows(x, rows, out=None, stream=None):
     """out[rows[t][j]] = x[t]: the tokens' rows in the experts' order. x is T x D of any of float32,
-    bfloat16, float16, int8 and uint8, rows T x k int32 as route_topk returns it; entries outside out's
-    rows are none. out has T k rows if it is not given; those that nothing names are left as they are
+    bfloat16, float16, int8 and uint8, rows T x k int32 as route_topk returns it (k at most 1024); entries
+    outside out's rows are none. out has T k rows if it is not given; those that nothing names are left as they are
     (uninitialised if out was not given). The gradient is combine_rows without weights."""
     import torch
     dtypes = (torch.float32, torch.bfloat16, torch.float16, torch.int8, torch.uint8)
@@ -1239,8 +1239,8 @@ def spread_rows(x, rows, out=None, stream=None):
 
 def combine_rows(y, rows, weights=None, out=None, out_dtype=None, stream=None):
     """out[t] = sum_j weights[t][j] y[rows[t][j]]: the experts' outputs y (float32, bfloat16 or float16)
-    back to the tokens. rows T x k int32 as route_topk returns it (entries outside y's rows add
-    nothing), weights T x k float32 or None for the plain sum; out T x D, float32 (default), bfloat16 or
+    back to the tokens. rows T x k int32 as route_topk returns it (k at most 1024; entries outside y's
+    rows add nothing), weights T x k float32 or None for the plain sum; out T x D, float32 (default), bfloat16 or
     float16."""
     import torch
     ldy = _matrix(y, "y", (torch.float32, torch.bfloat16, torch.float16))

@@ -465,7 +465,8 @@ int check_rows(int64_t T, int64_t k, int64_t D, int64_t total, const int32_t *ro
 {
     if (T < 0 || k < 0 || D < 0 || total < 0) return invalid("negative size");
     if (T > kMaxDim || D > kMaxDim || total > kMaxDim) return invalid("size above 2^31 - 1");
-    if (k > kMaxDim || (k > 0 && T > kMaxDim / k)) return invalid("T k above 2^31 - 1");
+    if (k > mm::kRowsMaxSlots) return invalid("more than 1024 slots to a token");
+    if (k > 0 && T > kMaxDim / k) return invalid("T k above 2^31 - 1");
     if (T > 0 && k > 0 && !rows) return invalid("rows is NULL");
     if ((uintptr_t)rows % 4) return invalid("rows not 4-byte aligned");
     return MM_OK;

@@ -242,7 +242,9 @@ struct RouteGradArgs {
 };
 hipError_t route_grad_launch(const RouteGradArgs &a, hipStream_t stream);
 
-// Tokens' rows to the experts' order and back (mm_expert_rows.hip); T, k, D >= 1.
+// Tokens' rows to the experts' order and back (mm_expert_rows.hip); T, k, D >= 1, k at most
+// kRowsMaxSlots (a workgroup takes them one after the other).
+constexpr int kRowsMaxSlots = 1024;
 struct RowsArgs {
     const void *x;             // spread: T x D; combine: total x D; gradient: T x D (of the output)
     void *out;                 // spread: total x D; combine: T x D; gradient: total x D
