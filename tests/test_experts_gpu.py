@@ -391,6 +391,34 @@ def test_combine_grad(dev, T, k, total, D, dtype, grad):
     assert bool(torch.isnan(buf[:, 0]).all()) and bool(torch.isnan(buf[:, 1 + D:]).all())
 
 
+@pytest.mark.parametrize("D", [2 ** 31 - 1, 2 ** 31 - 9])
+def test_longest_rows(dev, D):
+    """One token's row of 2^31 - 1 elements (and one whose last 8 are whole) and back, and its
+    gradients; what lies behind stays as it is. Values and sums are exact."""
+    x = torch.zeros((1, D), dtype=torch.bfloat16, device=dev)
+    x[0, :70] = torch.arange(70, device=dev)
+    x[0, -70:] = -torch.arange(70, device=dev).to(torch.bfloat16)
+    rows = torch.tensor([[0]], dtype=torch.int32, device=dev)
+    w = torch.full((1, 1), 0.5, device=dev)
+    out = torch.full((D + 16,), 3.0, dtype=torch.bfloat16, device=dev)
+    place = out[:D].view(1, D)
+
+    def check(factor):
+        assert torch.equal(place[0, :200], x[0, :200] * factor) and torch.equal(place[0, -200:], x[0, -200:] * factor)
+        assert int((place != 0).sum()) == 138 and bool((out[D:] == 3).all())
+        place.fill_(3)
+
+    mm.spread_rows(x[:, :D // 2], rows, out=place[:, :D // 2])
+    assert torch.equal(place[0, :D // 2], x[0, :D // 2]) and bool((place[0, D // 2:] == 3).all())  # 2^31 - 1 bytes at most
+    mm.combine_rows(x, rows, out=place)
+    check(1)
+    mm.combine_rows(x, rows, w, out=place)
+    check(0.5)
+    _, dw = mm.combine_rows_grad(x, x, rows, w, out=place)
+    check(0.5)
+    assert dw.item() == 2 * sum(i * i for i in range(70))
+
+
 def test_rows_empty(dev):
     rows = torch.zeros(0, 4, dtype=torch.int32, device=dev)
     assert mm.spread_rows(torch.zeros(0, 8, device=dev), rows).shape == (0, 8)

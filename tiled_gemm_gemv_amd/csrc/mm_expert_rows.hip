@@ -39,7 +39,7 @@ struct Eight {
     // not kept in the caches
     __device__ __forceinline__ void load_once(const void *base, int64_t at, int col, int D)
     {
-        if (col + 8 > D) return load(base, at, col, D);
+        if (D - col < 8) return load(base, at, col, D);  // not col + 8, which may pass 2^31 - 1
         const char *p = reinterpret_cast<const char *>(static_cast<const X *>(base) + at + col);
 #pragma unroll
         for (int c = 0; c < V; ++c) v[c] = __builtin_nontemporal_load(reinterpret_cast<const AnyWords *>(p) + c);
@@ -62,7 +62,7 @@ template <class O, bool ONCE = false>
 __device__ __forceinline__ void store_eight(void *base, int64_t at, int col, int D, const float (&x)[8])
 {
     O *out = static_cast<O *>(base) + at + col;
-    if (col + 8 <= D) {
+    if (D - col >= 8) {
         constexpr int W = sizeof(O) / 2;  // 16-byte pieces
         struct Row {
             O v[8];
