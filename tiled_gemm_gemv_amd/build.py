@@ -5,9 +5,12 @@
 The library is written in-tree, next to this file, so it travels with the source
 tree. Every HIP source is compiled with packed-fp32 instructions disabled.
 """
+import concurrent.futures
 import os
+import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -36,21 +39,31 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Compile libmm.so (always recompiles) and return its path."""
+    """Compile libmm.so (always recompiles), the sources side by side, and return its path."""
+    def run(args, sources, out):
+        cmd = [hipcc(), *HIPCC_FLAGS, *extra_flags, *args, *sources, "-o", out]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        # hipcc's host pass does not know the packed-fp32 feature and says so; drop
+        # that note and show anything else.
+        noise = "'-packed-fp32-ops' is not a recognized feature"
+        msgs = [l for l in (r.stdout + r.stderr).splitlines() if noise not in l]
+        if msgs and (verbose or r.returncode != 0):
+            print("\n".join(msgs), file=sys.stderr)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed with status {r.returncode}")
+
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}",
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    # hipcc's host pass does not know the packed-fp32 feature and says so; drop
-    # that note and show anything else.
-    noise = "'-packed-fp32-ops' is not a recognized feature"
-    msgs = [l for l in (r.stdout + r.stderr).splitlines() if noise not in l]
-    if msgs and (verbose or r.returncode != 0):
-        print("\n".join(msgs), file=sys.stderr)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed with status {r.returncode}")
+    objects = tempfile.mkdtemp(prefix="libmm")
+    try:
+        compiled = [os.path.join(objects, s + ".o") for s in SOURCES]
+        with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda s, o: run(["-c", f"-I{INCLUDE}", f"-I{CSRC}"], [os.path.join(CSRC, s)], o), SOURCES,
+                          compiled))
+        run([], compiled, tmp)
+    finally:
+        shutil.rmtree(objects)
     os.replace(tmp, LIB)
     return LIB
 
