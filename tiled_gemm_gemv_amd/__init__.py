@@ -7,9 +7,9 @@ torch tensor on the GPU; `stream` accepts a hipStream_t address (int), a
 torch.cuda.Stream, or None for torch's current stream on the current device.
 
 gemm(A, B, out=None), gemv(A, x, out=None), conv2d(x, w, ...), gemm16_grouped(A, B, offsets),
-gemm_i8(A, B, a_scale, b_scale), gemm_mx4(A, B, a_scale, b_scale), route_topk(logits, k) etc. are conveniences for torch tensors:
-they check dtypes, devices and strides (not those of empty tensors, which are arbitrary),
-allocate the output with torch when none is given, and call the C entry points. PyTorch
+gemm_i8(A, B, a_scale, b_scale), gemm_mx4(A, B, a_scale, b_scale), route_topk(logits, k)
+etc. are conveniences for torch tensors: they check dtypes, devices and strides (not those of
+empty tensors, which are arbitrary), allocate the output with torch when none is given, and call the C entry points. PyTorch
 only provides device memory and streams here.
 
 There is no fallback: if libmm.so is missing or fails to load, every call raises.

@@ -5,8 +5,8 @@
 // threads copy 64 bytes of k of both panels into LDS one element at a time (zeros outside
 // the matrices), as rows of consecutive k whatever the operands' layout, so each MFMA operand
 // is one 16-byte LDS read. Single elements make no demand on alignment or sizes, and bound
-// the kernel (i8 8192 x 14336 x 4096 in 8.6 ms, 112 TOP/s): it is the one for what the others do not
-// take, a single column of matrices stored K x N, gradients of fewer than 8 rows or columns or with
+// the kernel (i8 8192 x 14336 x 4096 in 8.6 ms, 112 TOP/s; 4-bit 4.9 ms): it is the one for what the
+// others do not take, a single column of matrices stored K x N, gradients of fewer than 8 rows or columns or with
 // strides that put a K-step's rows past 2^32 bytes, and sizes within 1024 of 2^31. The choice among all
 // of them is at the end of this file.
 #include "mm_group.h"

@@ -1,4 +1,4 @@
-// mm_group_tile.hip -- large tiles of the grouped products and of the 8-bit integer product
+// mm_group_tile.hip -- large tiles of the grouped products and of the 8-bit integer and 4-bit products
 // (see mm_group.h for the sums), with panels moved HBM -> LDS by the LDS DMA.
 //
 // A group of waves computes a BM x BN tile of C (256 x 256 or 128 x 128 on 8 waves, 64 x 64 on 2;
@@ -55,6 +55,14 @@
 // shapes: 32 x 32 MFMAs instead of 16 x 16 8-15% slower (they pass twice the accumulator bytes per
 // product); 4 waves of 128 x 128 the same with 32 x 32 MFMAs; a phase's reads in front of its MFMAs 5-8%
 // slower; workgroups that stay and load their next tile during the stores -1.7% to +8.6%.
+//
+// 4-bit elements (two to a byte, so a K-step is 256 of them, one 32-element block to a 16-byte chunk) take
+// the same tiles with other phases (phase_mx), since their scales need registers too, and
+// v_mfma_scale_f32_16x16x128, 10.3 ns of a SIMD against 7.8 for i8's of the same bytes. 8192 x 14336 x 4096:
+// 251-276 us, 3.5-3.8 PFLOP/s, 230 registers, MFMAs busy 44% of the cycles at 1.7-2 GHz. Taken apart: without
+// the scales' loads 9 us less, without spreading them to lanes another 16, without reading them 4, and with no
+// loads at all 217 us: what is left is the MFMAs, their operands from LDS and the clock under this load.
+// (32 x 32 x 64 MFMAs: 9% fewer cycles at a clock 8% lower, the same time.)
 #include "mm_group.h"
 
 namespace mm {
@@ -129,8 +137,9 @@ __device__ __forceinline__ void wait_vm()
 // A lane's scale bytes as the MFMA takes them. `raw`: the 8 scale bytes (chunk c of the K-step in byte
 // c) of the row that lane 16 s + r reads its operands' row r from in block s, s < 4. The operand of
 // block i and MFMA step ks in lane 16 g + r is chunk 4 ks + g of row r; its scale becomes byte
-// 2 (i / 2) + ks of word i % 2 (of two blocks: byte 2 i + ks of one word). Bytes change places with 16-lane rows in two steps: the 16-bit halves
-// between the halves of the wave, then the bytes between neighbouring rows.
+// 2 (i / 2) + ks of word i % 2 (of two blocks: byte 2 i + ks of one word). Bytes change places with
+// 16-lane rows in two steps: the 16-bit halves between the halves of the wave, then the bytes between
+// neighbouring rows.
 template <int W>
 __device__ __forceinline__ void scales_of_lane(u32x2 raw, unsigned (&out)[W])
 {

@@ -12,7 +12,8 @@
 // number.
 //
 // A lane takes 8 elements, so a block is a quad of lanes: the maximum takes two DPP steps. Bound by
-// memory: each x is read once, each code written once.
+// memory: each x is read once, each code written once, x past the caches. 8192 x 14336 bf16: 50 us (5.9
+// TB/s), back 43 us (6.9 TB/s); x through the caches both together 113 instead of 92.
 #include "mm_group.h"
 
 namespace mm {

@@ -9,12 +9,12 @@
 // (0 where that is 0).
 //
 // The ranks are those of 64-bit values: with 16384 tokens and 256 experts some pair of neighbouring
-// scores lies closer than 32-bit rounding, and the choice would go by it. A wave takes a token. It
-// computes c in 32 bits, off by at most `slack`, and picks the best one after the other by a 32-bit key
+// scores lies closer than 32-bit rounding, and the choice would go by it. A wave takes four tokens, 16
+// lanes each, or (more than 256 experts, 12 chosen or 16 groups) one. It computes c in 32 bits, off by at most `slack`, and picks the best one after the other by a 32-bit key
 // of 22 leading bits and the index: k of them, and all others that could be above the k-th by slack and
 // truncation. Those few, one to a lane, get their values in 64 bits and are put in that order. Where
-// groups lie closer than the slack, values are NaN or infinite, or more than 64 experts are that close,
-// the token is done in 64 bits throughout.
+// groups lie closer than the slack, they are ranked in 64 bits; where values are NaN or infinite, or more
+// experts than the token has lanes are that close, the token is done in 64 bits throughout.
 //
 // The rows' order: slots by (expert, token, slot). A workgroup routes 16 or 64 tokens; a token takes an expert
 // once, so a 64-bit mask for each expert says which of them have it, and counts of its bits number the
@@ -22,9 +22,10 @@
 // kernel itself for up to 16 workgroups, else by one in between). No atomics but the masks' bits: the
 // order is fixed.
 //
-// Many tokens are bound by instructions (some 650 for a token of 256 experts, 8 of them chosen: 16384
-// tokens 19 us, with groups and a bias 32, of 8 MB that could be read in 2), few by the launches: 3 to 5 us
-// each, three of them (8 tokens of 64 experts: one, 5 us).
+// Many tokens are bound by instructions, some 2000 of a wave for four tokens of 256 experts, 8 of them
+// chosen: all three kernels for 16384 tokens 19-23 us, with groups and a bias 28 (one token to a wave 39),
+// of 8 MB that could be read in 2. Few are bound by the launches: 3 to 5 us each, three of them (4001 tokens
+// of 60 experts 7 + 4 + 3 us; 8 tokens of 64 experts: one, 5 us).
 #include "mm_group.h"
 
 namespace mm {
