@@ -41,10 +41,18 @@ class MMError(RuntimeError):
 
 
 _lib = None
+_torch = None  # once a front end has been called; an import statement takes 0.1 us of each function
 
 
 def _lib_or_none():
     return _lib
+
+
+def _import_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
 
 
 def lib_path() -> str:
@@ -564,7 +572,7 @@ def _workspace_bytes(ws, device):
 
 
 def _matrix(t, name, dtypes=None):
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     dtypes = dtypes or (torch.float32,)
@@ -774,7 +782,7 @@ def conv2d(x, w, stride=(1, 1), pad=(0, 0), dilation=(1, 1), out=None, config=No
 
 def _run(name, device, stream, *args):
     """Call the C entry point `name` with `args` and the stream, `device` (an index) current."""
-    import torch
+    torch = _torch or _import_torch()
     fn = getattr(_lib or load(), name)
     # the current stream's address without a Stream object around it (2.9 us of a 12 us call)
     s = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
@@ -789,7 +797,7 @@ def _run(name, device, stream, *args):
 
 def _mm_type(dtype, name):
     """MM_TYPE_* of a torch dtype."""
-    import torch
+    torch = _torch or _import_torch()
     if dtype is torch.float32:
         return MM_TYPE_F32
     if dtype is torch.bfloat16:
@@ -807,7 +815,7 @@ def _same_device(t, name, device):
 
 def _stack(t, name, dtypes):
     """Leading dimension and group stride of a 3-D tensor of matrices."""
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -836,7 +844,7 @@ def _apart(count, stride, rows, ld, cols):
 
 
 def _offsets(t, groups, device):
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int64:
         raise TypeError("offsets must be an int64 tensor")
     if t.dim() != 1 or t.shape[0] != groups + 1 or not t.is_contiguous():
@@ -845,7 +853,7 @@ def _offsets(t, groups, device):
 
 
 def _scale(t, shape, name, device):
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
         raise TypeError(f"{name} must be a float32 tensor")
     if t.shape != shape or not t.is_contiguous():
@@ -856,12 +864,13 @@ def _scale(t, shape, name, device):
 def _output(out, out_dtype, shape, like):
     """(the output tensor, its MM_TYPE_*, leading dimension, group stride): `out` if given (its dtype
     must be out_dtype where that is given too), else a new one of out_dtype (float32 by default)."""
-    import torch
+    torch = _torch or _import_torch()
     if out is None:
         dtype = torch.float32 if out_dtype is None else out_dtype
         c_type = _mm_type(dtype, "out_dtype")
         cols = max(shape[-1], 1)
-        return like.new_empty(shape, dtype=dtype), c_type, cols, shape[-2] * cols
+        new = like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+        return new, c_type, cols, shape[-2] * cols
     if not isinstance(out, torch.Tensor):
         raise TypeError("out must be a torch.Tensor")
     c_type = _mm_type(out.dtype, "out")
@@ -883,7 +892,7 @@ def gemm16_grouped(A, B, offsets, trans_b=False, out=None, out_dtype=None, strea
     not decrease; the host never reads it. out is float32, bfloat16 or float16 (out_dtype,
     float32 by default); its rows of no group are left as they are (uninitialised if out was
     not given). The gradient with respect to A is gemm16_grouped(dout, B, offsets, not trans_b)."""
-    import torch
+    torch = _torch or _import_torch()
     lda = _matrix(A, "A", (torch.bfloat16, torch.float16))
     ldb, stride_b = _stack(B, "B", (A.dtype,))
     device = A.get_device()
@@ -933,7 +942,7 @@ def gemm16_grouped_grad_b(A, G, offsets, out=None, out_dtype=None, stream=None):
 def quantize_i8(x, out=None, scale=None, stream=None):
     """(q, scale): the rows of x (float32, bfloat16 or float16) as int8 with q[i] * scale[i] ~ x[i],
     scale[i] = max |x[i]| / 127; values are rounded to the nearest integer, halves to even."""
-    import torch
+    torch = _torch or _import_torch()
     ldx = _matrix(x, "x", (torch.float32, torch.bfloat16, torch.float16))
     device = x.get_device()
     rows, cols = x.shape
@@ -956,7 +965,7 @@ def quantize_i8(x, out=None, scale=None, stream=None):
 def gemm_i8(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
     """out[i][j] = a_scale[i] b_scale[j] sum_k A[i][k] B[j][k] for int8 GPU tensors A (M x K) and
     B (N x K), any row strides; out float32 (default), bfloat16 or float16."""
-    import torch
+    torch = _torch or _import_torch()
     lda = _matrix(A, "A", (torch.int8,))
     ldb = _matrix(B, "B", (torch.int8,))
     device = A.get_device()
@@ -976,7 +985,7 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
 def gemm_i8_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, stream=None):
     """gemm_i8 with rows grouped by expert: B groups x N x K, b_scale groups x N, offsets as for
     gemm16_grouped; rows of no group are left as they are."""
-    import torch
+    torch = _torch or _import_torch()
     lda = _matrix(A, "A", (torch.int8,))
     ldb, stride_b = _stack(B, "B", (torch.int8,))
     device = A.get_device()
@@ -996,7 +1005,7 @@ def gemm_i8_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, s
 
 def _bytes_matrix(t, shape, name, device):
     """Leading dimension of a uint8 matrix of the given shape."""
-    import torch
+    torch = _torch or _import_torch()
     if isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.shape == shape and t.get_device() == device:
         rows, cols = shape
         if rows > 1 and cols > 1:  # the common case, with few questions
@@ -1016,7 +1025,7 @@ def quantize_mx4(x, out=None, scale=None, stream=None):
     uint8, rows x 16 ceil(cols / 32), two elements to a byte, the even one low (the last block filled
     up with zeros); scale is uint8, rows x ceil(cols / 32), the exponent + 127. An element is x / 2^e
     rounded to the nearest value, halves to the even code, e = floor(log2 max |x|) - 2 in its block."""
-    import torch
+    torch = _torch or _import_torch()
     ldx = _matrix(x, "x", (torch.float32, torch.bfloat16, torch.float16))
     device = x.get_device()
     rows, cols = x.shape
@@ -1026,7 +1035,7 @@ def quantize_mx4(x, out=None, scale=None, stream=None):
     else:
         ldq = _bytes_matrix(out, (rows, 16 * blocks), "out", device)
     if scale is None:
-        scale, lds = x.new_empty((rows, blocks), dtype=torch.uint8), max(blocks, 1)
+        scale, lds = out.new_empty((rows, blocks)), max(blocks, 1)
     else:
         lds = _bytes_matrix(scale, (rows, blocks), "scale", device)
     _run("mm_quantize_mx4", device, stream, rows, cols, x.data_ptr(), _mm_type(x.dtype, "x"), ldx, out.data_ptr(), ldq,
@@ -1037,7 +1046,7 @@ def quantize_mx4(x, out=None, scale=None, stream=None):
 def dequantize_mx4(q, scale, cols=None, out=None, out_dtype=None, stream=None):
     """The values that quantize_mx4's codes and scales stand for: rows x cols (all elements of the
     blocks by default) of out_dtype, float32 (default), bfloat16 (both exact) or float16."""
-    import torch
+    torch = _torch or _import_torch()
     ldq = _matrix(q, "q", (torch.uint8,))
     device = q.get_device()
     rows, width = q.shape
@@ -1058,7 +1067,7 @@ def gemm_mx4(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
     """out[i][j] = sum_k a[i][k] b[j][k] of the values of quantize_mx4's codes A (M x K / 2 bytes) and B
     (N x K / 2) with scales M x K / 32 and N x K / 32, all uint8, any row strides; out float32
     (default), bfloat16 or float16."""
-    import torch
+    torch = _torch or _import_torch()
     lda = _matrix(A, "A", (torch.uint8,))
     ldb = _matrix(B, "B", (torch.uint8,))
     device = A.get_device()
@@ -1080,7 +1089,7 @@ def gemm_mx4(A, B, a_scale, b_scale, out=None, out_dtype=None, stream=None):
 def gemm_mx4_grouped(A, B, offsets, a_scale, b_scale, out=None, out_dtype=None, stream=None):
     """gemm_mx4 with rows grouped by expert: B groups x N x K / 2, b_scale groups x N x K / 32, offsets as
     for gemm16_grouped (and as route_topk returns them); rows of no group are left as they are."""
-    import torch
+    torch = _torch or _import_torch()
     lda = _matrix(A, "A", (torch.uint8,))
     ldb, stride_b = _stack(B, "B", (torch.uint8,))
     device = A.get_device()
@@ -1114,7 +1123,7 @@ def _scoring(name):
 
 def _slots(t, shape, dtype, name, device):
     """Check a packed tensor with an entry for each slot of each token."""
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
     if t.shape != shape or not t.is_contiguous():
@@ -1156,7 +1165,7 @@ def route_topk(logits, k, scoring="softmax", bias=None, groups=1, top_groups=1, 
     slot, -1 without an expert, and offsets (E + 1, int64) says where each expert's rows begin, as the
     grouped products take it. workspace: a device tensor of mm_route_topk_workspace_bytes bytes (e.g.
     from route_topk_workspace); allocated for the call if not given."""
-    import torch
+    torch = _torch or _import_torch()
     ld = _matrix(logits, "logits", (torch.float32, torch.bfloat16, torch.float16))
     device = logits.get_device()
     T, E = logits.shape
@@ -1175,7 +1184,7 @@ def route_topk(logits, k, scoring="softmax", bias=None, groups=1, top_groups=1, 
         size = 0
     weights = logits.new_empty((T, k), dtype=torch.float32)
     experts = logits.new_empty((T, k), dtype=torch.int32)
-    rows = logits.new_empty((T, k), dtype=torch.int32)
+    rows = torch.empty_like(experts)
     offsets = logits.new_empty(E + 1, dtype=torch.int64)
     _run("mm_route_topk", device, stream, T, E, k, logits.data_ptr(), _mm_type(logits.dtype, "logits"), ld, how,
          None if bias is None else bias.data_ptr(), groups, top_groups, group_top, 1 if renormalize else 0, scale,
@@ -1187,7 +1196,7 @@ def route_topk(logits, k, scoring="softmax", bias=None, groups=1, top_groups=1, 
 def route_topk_grad(logits, experts, dweights, scoring="softmax", renormalize=False, scale=1.0, out=None, stream=None):
     """The gradient of route_topk's weights with respect to the logits, T x E of the logits' dtype, from
     dweights (T x k, float32) and the experts that route_topk returned."""
-    import torch
+    torch = _torch or _import_torch()
     ld = _matrix(logits, "logits", (torch.float32, torch.bfloat16, torch.float16))
     device = logits.get_device()
     T, E = logits.shape
@@ -1205,7 +1214,7 @@ def route_topk_grad(logits, experts, dweights, scoring="softmax", renormalize=Fa
 
 def _token_slots(rows):
     """(T, k) of a router's rows."""
-    import torch
+    torch = _torch or _import_torch()
     if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
         raise TypeError("rows must be a 2-D tensor")
     return rows.shape
@@ -1216,7 +1225,7 @@ def spread_rows(x, rows, out=None, stream=None):
     bfloat16, float16, int8 and uint8, rows T x k int32 as route_topk returns it (k at most 1024); entries
     outside out's rows are none. out has T k rows if it is not given; those that nothing names are left as they are
     (uninitialised if out was not given). The gradient is combine_rows without weights."""
-    import torch
+    torch = _torch or _import_torch()
     dtypes = (torch.float32, torch.bfloat16, torch.float16, torch.int8, torch.uint8)
     ldx = _matrix(x, "x", dtypes)
     device = x.get_device()
@@ -1242,7 +1251,7 @@ def combine_rows(y, rows, weights=None, out=None, out_dtype=None, stream=None):
     back to the tokens. rows T x k int32 as route_topk returns it (k at most 1024; entries outside y's
     rows add nothing), weights T x k float32 or None for the plain sum; out T x D, float32 (default), bfloat16 or
     float16."""
-    import torch
+    torch = _torch or _import_torch()
     ldy = _matrix(y, "y", (torch.float32, torch.bfloat16, torch.float16))
     device = y.get_device()
     T, k = _token_slots(rows)
@@ -1261,7 +1270,7 @@ def combine_rows_grad(dout, y, rows, weights, out=None, stream=None):
     float32, bfloat16 or float16): dy[rows[t][j]] = weights[t][j] dout[t], of y's shape and dtype (out
     if given), rows that nothing names left as they are (uninitialised if out was not given);
     dweights[t][j] = <y[rows[t][j]], dout[t]>, float32."""
-    import torch
+    torch = _torch or _import_torch()
     types = (torch.float32, torch.bfloat16, torch.float16)
     ldg = _matrix(dout, "dout", types)
     ldy = _matrix(y, "y", types)
