@@ -30,12 +30,12 @@ CASES = [
     ("rows 32x16", 0, 323, 244, 32, False),
     ("rows 32x16", 40, 416, 3, 96, False),
     ("rows 32x16", 12, 148, 2, 320, True),
-    ("rows 32x32", 0, 851, 916, 32, True),
-    ("rows 32x32", 7, 1831, 419, 32, False),
+    ("rows 32x32", 0, 1007, 737, 160, False),
+    ("rows 32x32", 13, 265, 2500, 128, True),
     ("rows 64x16", 0, 299, 1222, 32, True),
     ("rows 64x16", 2, 750, 527, 32, False),
     ("rows 64x32", 0, 982, 1508, 32, False),
-    ("rows 64x32", 3, 2726, 567, 32, False),
+    ("rows 64x32", 19, 419, 2438, 576, False),
     ("tile 64x64 in 4", 0, 69, 2755, 2144, False),
     ("tile 64x64 in 4", 0, 270, 1168, 800, True),
     ("tile 64x64 in 4", 0, 130, 1100, 4096, False),
@@ -46,11 +46,19 @@ CASES = [
     ("tile 64x64 in 2", 0, 700, 1000, 1280, False),
     ("tile 64x64 in 2", 8, 1652, 451, 352, False),
     ("tile 64x64 in 2", 53, 1079, 247, 256, True),
+    ("tile 64x64 in 2", 0, 2478, 415, 32, False),
+    ("tile 64x64 in 2", 55, 2118, 352, 64, False),
+    ("tile 64x64 in 2", 29, 1589, 385, 224, True),
     ("tile 128x128", 0, 481, 1577, 256, False),
     ("tile 128x128", 0, 2000, 1300, 1024, False),
     ("tile 128x128", 0, 2000, 1300, 1312, True),
     ("tile 128x128", 15, 2860, 399, 256, False),
     ("tile 128x128", 4, 793, 745, 256, True),
+    ("tile 128x128", 0, 851, 916, 32, True),
+    ("tile 128x128", 7, 1831, 419, 32, False),
+    ("tile 128x128", 3, 2726, 567, 32, False),
+    ("tile 128x128", 0, 951, 1608, 160, False),
+    ("tile 128x128", 2, 1013, 2660, 96, True),
     ("tile 256x256", 0, 2974, 2925, 544, False),
     ("tile 256x256", 0, 2858, 2911, 864, True),
     ("tile 256x256", 0, 3100, 2900, 256, False),
@@ -60,6 +68,10 @@ CASES = [
     ("tile 256x256", 0, 3100, 2900, 1312, False),
     ("tile 256x256", 16, 2811, 2712, 288, False),
     ("tile 256x256", 3, 3000, 3001, 1568, False),
+    ("tile 256x256", 0, 2960, 2959, 64, False),
+    ("tile 256x256", 0, 2991, 2925, 32, True),
+    ("tile 256x256", 7, 2827, 2717, 96, False),
+    ("tile 256x256", 22, 2935, 2210, 64, True),
 ]
 
 

@@ -331,7 +331,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
             const int r8 = 8 * w + lane / 8;
             a_row = (unsigned)(r8 * p.lda);
             b_row = (unsigned)(r8 * p.ldb);
-            mx_chunk = 16u * ((lane % 8) ^ swz_d(r8));
+            mx_chunk = min(16u * ((lane % 8) ^ swz_d(r8)), (unsigned)(min(p.K, T::BK) - 16));  // chunks past K: cleared
             static_assert(8 * T::WAVES % 16 == 0, "a wave's loads share their rows' swizzle");
             return;
         }
@@ -467,10 +467,16 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
             u32x2 v;
         };
         const unsigned char *q = sc_base + sc_voff;
-        u32x4 v = {};
-        const u32x2 x = reinterpret_cast<const Eight *>(q + first_k(0) / 16)->v;
-        v[0] = x[0];
-        v[1] = x[1];
+        u32x4 v = {0x7f7f7f7fu, 0x7f7f7f7fu};
+        if (p.K >= T::BK) {
+            const u32x2 x = reinterpret_cast<const Eight *>(q + first_k(0) / 16)->v;
+            v[0] = x[0];
+            v[1] = x[1];
+        } else {  // a row of fewer, the chunks past them zeros of scale 1
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (16 * i < p.K) v[i / 4] = (v[i / 4] & ~(0xffu << (8 * (i % 4)))) | (unsigned)q[i] << (8 * (i % 4));
+        }
         if (nk > 1) {
             const u32x2 y = reinterpret_cast<const Eight *>(q + first_k(1) / 16)->v;
             v[2] = y[0];
@@ -930,8 +936,7 @@ bool tile_ok(const GroupArgs &a)
     constexpr int largest = 0x7fffffff - 1024;  // a tile's row and column numbers fit an int
     if (a.M > largest || a.N > largest || a.K > largest) return false;
     if (!GRAD && a.K * T::ES < 16) return false;  // a chunk
-    // a row has a K-step's scales, and their lane offsets fit 32 bits
-    if (T::MX && (a.K < T::BK || (T::BM - 1) * a.ld_mxa >= limit || (T::BN - 1) * a.ld_mxb >= limit)) return false;
+    if (T::MX && ((T::BM - 1) * a.ld_mxa >= limit || (T::BN - 1) * a.ld_mxb >= limit)) return false;
     if ((T::AT && a.K < 8) || (T::BT && a.N < 8)) return false;  // a chunk of a T operand's columns
     const int64_t a_rows = T::AT ? T::BK : T::BM, b_rows = T::BT ? T::BK : T::BN;
     return ((a_rows - 1) * a.lda + T::BM) * T::ES + 128 < limit && ((b_rows - 1) * a.ldb + T::BN) * T::ES + 128 < limit;
