@@ -315,7 +315,7 @@ def slots_of(rng, T, k, total, dev):
 
 
 ROWS = [(1, 1, 1, 1), (2, 3, 6, 7), (5, 2, 8, 64), (8, 8, 64, 4096), (3, 9, 40, 130), (17, 4, 68, 2049), (70, 1, 70, 100),
-        (33, 6, 250, 777), (4, 32, 128, 5000)]
+        (33, 6, 250, 777), (4, 32, 128, 5000), (300, 3, 850, 512), (130, 2, 260, 513), (1000, 9, 9000, 16)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32", "i8", "u8"])

@@ -86,13 +86,31 @@ __device__ __forceinline__ void store_eight(void *base, int64_t at, int col, int
     }
 }
 
-// Workgroup: token and 4 KB of its row.
-__global__ __launch_bounds__(256) void spread_kernel(RowsArgs p, unsigned parts)
+// This thread's token and its number in the token's threads. Wide rows: a workgroup has a token and
+// the part'th of `parts` pieces of 256 threads' units. NARROW, rows of at most 64 threads' units: 2^shift
+// threads to a token, the others of the workgroup to those behind it.
+struct Place {
+    int64_t t, unit;
+};
+template <bool NARROW>
+__device__ __forceinline__ Place place_of(unsigned parts, int shift)
 {
-    const int64_t bid = linear_block(), t = bid / parts;
-    if (t >= p.T) return;
-    const int64_t at = (bid - t * parts) * 4096 + 16 * threadIdx.x;
-    if (at >= p.D) return;
+    const int64_t bid = linear_block();
+    if constexpr (NARROW) {
+        return {(bid << (8 - shift)) + (threadIdx.x >> shift), (int64_t)(threadIdx.x & ((1u << shift) - 1))};
+    } else {
+        const int64_t t = bid / parts;
+        return {t, (bid - t * parts) * 256 + threadIdx.x};
+    }
+}
+
+// 16 bytes of a token's row to a thread.
+template <bool NARROW>
+__global__ __launch_bounds__(256) void spread_kernel(RowsArgs p, unsigned parts, int shift)
+{
+    const Place place = place_of<NARROW>(parts, shift);
+    const int64_t t = place.t, at = 16 * place.unit;
+    if (t >= p.T || at >= p.D) return;
     const int valid = (int)min((int64_t)16, p.D - at);
     const u32x4 v = load16_upto<unsigned char>(static_cast<const char *>(p.x) + t * p.ldx + at, valid, p.D);
     for (int j = 0; j < p.k; ++j) {
@@ -111,14 +129,13 @@ __global__ __launch_bounds__(256) void spread_kernel(RowsArgs p, unsigned parts)
 
 constexpr int kSlots = 4;
 
-// Workgroup: token and 2048 columns.
-template <class X, class O>
-__global__ __launch_bounds__(256) void combine_kernel(RowsArgs p, unsigned parts)
+// 8 columns of a token to a thread.
+template <class X, class O, bool NARROW>
+__global__ __launch_bounds__(256) void combine_kernel(RowsArgs p, unsigned parts, int shift)
 {
-    const int64_t bid = linear_block(), t = bid / parts;
-    if (t >= p.T) return;
-    const int64_t first = (bid - t * parts) * 2048 + 8 * threadIdx.x;
-    if (first >= p.D) return;
+    const Place place = place_of<NARROW>(parts, shift);
+    const int64_t t = place.t, first = 8 * place.unit;
+    if (t >= p.T || first >= p.D) return;
     const int col = (int)first;
     float sum[8] = {};
     // kSlots loads on their way at once (one after the other: 79-93 us for 8192 x 4 rows of 4096 bf16)
@@ -144,16 +161,17 @@ __global__ __launch_bounds__(256) void combine_kernel(RowsArgs p, unsigned parts
     store_eight<O>(p.out, t * p.ldo, col, p.D, sum);
 }
 
-// Workgroup: token.
-template <class G, class Y>
-__global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs p)
+// Wide: a workgroup to a token, narrow: 2^shift threads, 8 columns each at a time.
+template <class G, class Y, bool NARROW>
+__global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs p, unsigned, int shift)
 {
     __shared__ float part[4][8];
-    const int64_t t = linear_block();
-    if (t >= p.T) return;
+    const Place place = place_of<NARROW>(1, shift);
+    const int64_t t = place.t;
+    if (t >= p.T) return;  // narrow: whole tokens, whose threads' sums are their own
     for (int j0 = 0; j0 < p.k; j0 += 8) {
         float dot[8] = {};
-        for (int64_t first = 8 * threadIdx.x; first < p.D; first += 2048) {
+        for (int64_t first = 8 * place.unit; first < p.D; first += 2048) {
             const int col = (int)first;
             Eight<G> g;
             g.load(p.x, t * p.ldx, col, p.D);
@@ -182,6 +200,15 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs p)
                 }
             }
         }
+        if constexpr (NARROW) {
+            for (int d = 1 << shift >> 1; d > 0; d >>= 1)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dot[j] += __shfl_xor(dot[j], d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (place.unit == 0 && j0 + j < p.k) p.dweights[t * p.k + j0 + j] = dot[j];
+            continue;
+        }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -200,15 +227,22 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs p)
     }
 }
 
-hipError_t launch(const void *fn, const RowsArgs &a, int64_t part, hipStream_t stream)
+// `unit`: what a thread takes of a row. `split`: a wide row's pieces go to workgroups of their own.
+// Narrow rows would leave most of a workgroup idle (65536 x 2 rows of 128 bf16: spread 7.4 us, combine 13, its
+// gradient 23; with one token to a workgroup 26, 41 and 217).
+hipError_t launch(const void *wide, const void *narrow, const RowsArgs &a, int unit, bool split, hipStream_t stream)
 {
-    const int64_t parts = part ? (a.D + part - 1) / part : 1;
+    const int64_t units = ((int64_t)a.D + unit - 1) / unit;
+    int shift = 0;
+    while (shift < 6 && (int64_t)1 << shift < units) ++shift;
+    const bool few = units <= 64;
+    const int64_t parts = few || !split ? 1 : (units + 255) / 256, tokens = few ? 256 >> shift : 1;
     unsigned gx, gy;
-    if (!grid_for(parts * a.T, gx, gy)) return hipErrorInvalidConfiguration;
+    if (!grid_for(parts * ((a.T + tokens - 1) / tokens), gx, gy)) return hipErrorInvalidConfiguration;
     RowsArgs arg = a;
     unsigned n = (unsigned)parts;
-    void *args[] = {&arg, &n};
-    return hipLaunchKernel(fn, dim3(gx, gy), dim3(256), args, 0, stream);
+    void *args[] = {&arg, &n, &shift};
+    return hipLaunchKernel(few ? narrow : wide, dim3(gx, gy), dim3(256), args, 0, stream);
 }
 
 // f(X()) with the type of number t (MM_TYPE_*).
@@ -224,14 +258,16 @@ auto with_type(int t, F &&f)
 
 hipError_t spread_rows_launch(const RowsArgs &a, hipStream_t stream)
 {
-    return launch(reinterpret_cast<const void *>(&spread_kernel), a, 4096, stream);
+    return launch(reinterpret_cast<const void *>(&spread_kernel<false>), reinterpret_cast<const void *>(&spread_kernel<true>),
+                  a, 16, true, stream);
 }
 
 hipError_t combine_rows_launch(const RowsArgs &a, hipStream_t stream)
 {
     return with_type(a.x_type, [&](auto x) {
         return with_type(a.o_type, [&](auto o) {
-            return launch(reinterpret_cast<const void *>(&combine_kernel<decltype(x), decltype(o)>), a, 2048, stream);
+            return launch(reinterpret_cast<const void *>(&combine_kernel<decltype(x), decltype(o), false>),
+                          reinterpret_cast<const void *>(&combine_kernel<decltype(x), decltype(o), true>), a, 8, true, stream);
         });
     });
 }
@@ -240,7 +276,8 @@ hipError_t combine_rows_grad_launch(const RowsArgs &a, hipStream_t stream)
 {
     return with_type(a.x_type, [&](auto x) {
         return with_type(a.y_type, [&](auto y) {
-            return launch(reinterpret_cast<const void *>(&combine_grad_kernel<decltype(x), decltype(y)>), a, 0, stream);
+            return launch(reinterpret_cast<const void *>(&combine_grad_kernel<decltype(x), decltype(y), false>),
+                          reinterpret_cast<const void *>(&combine_grad_kernel<decltype(x), decltype(y), true>), a, 8, false, stream);
         });
     });
 }
