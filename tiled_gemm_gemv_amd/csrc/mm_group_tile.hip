@@ -91,7 +91,10 @@ struct GroupTile {
     static constexpr int SC_PAIR = MX ? 16 * (BN + BM) : 0;  // bytes of LDS, two of them
     static constexpr int SC_SEGMENTS = (BN + BM) / 64;       // 64 rows each
     static_assert(!MX || SC_SEGMENTS <= WAVES, "one load brings all rows' scales");
-    static constexpr int SAW = FM > 2 ? 2 : 1;  // words of the scales of a half's blocks of A; of B: one
+    // Few blocks of A: a lane reads its row's 8 scale bytes itself for every block, and picks its own; else 64
+    // rows are read at once and spread over the lanes (scales_of_lane). Words of a half's scales of A and B.
+    static constexpr bool DIRECT = FM <= 2;
+    static constexpr int SAW = DIRECT ? FM : 2, SBW = DIRECT ? FN : 1;
     static constexpr int GROUP_LDS = 2 * (STAGE + SC_PAIR);  // of a group of waves
     static constexpr int A_LD = A_HALF / 1024 / WAVES, B_LD = B_HALF / 1024 / WAVES;  // 1 KB loads per wave
     // offsets of the half panels in a stage
@@ -137,7 +140,7 @@ __device__ __forceinline__ void wait_vm()
 // A lane's scale bytes as the MFMA takes them. `raw`: the 8 scale bytes (chunk c of the K-step in byte
 // c) of the row that lane 16 s + r reads its operands' row r from in block s, s < 4. The operand of
 // block i and MFMA step ks in lane 16 g + r is chunk 4 ks + g of row r; its scale becomes byte
-// 2 (i / 2) + ks of word i % 2 (of two blocks: byte 2 i + ks of one word). Bytes change places with
+// 2 (i / 2) + ks of word i % 2 (of B's two blocks: byte 2 i + ks of one word). Bytes change places with
 // 16-lane rows in two steps: the 16-bit halves between the halves of the wave, then the bytes between
 // neighbouring rows.
 template <int W>
@@ -158,12 +161,12 @@ __device__ __forceinline__ void scales_of_lane(u32x2 raw, unsigned (&out)[W])
 
 // The MFMA of A's block i and B's block j in step ks (constants once unrolled), the operands exchanged.
 template <class T, class Acc>
-__device__ __forceinline__ Acc mma_scaled(u32x4 b, unsigned sb, int j, u32x4 a, const unsigned (&sa)[T::SAW], int i, int ks,
-                                          Acc c)
+__device__ __forceinline__ Acc mma_scaled(u32x4 b, const unsigned (&sbs)[T::SBW], int j, u32x4 a,
+                                          const unsigned (&sa)[T::SAW], int i, int ks, Acc c)
 {
     typedef typename T::E E;
-    const unsigned y = T::SAW == 2 ? sa[i & (T::SAW - 1)] : sa[0];
-    const int x_byte = 2 * j + ks, y_byte = T::SAW == 2 ? 2 * (i >> 1) + ks : 2 * i + ks;
+    const unsigned sb = sbs[T::DIRECT ? j : 0], y = sa[T::DIRECT ? i : i & 1];
+    const int x_byte = T::DIRECT ? ks : 2 * j + ks, y_byte = T::DIRECT ? ks : 2 * (i >> 1) + ks;
     switch (4 * x_byte + y_byte) {  // the same step ks on both sides
     case 0: return E::template mma<16, 0, 0>(b, sb, a, y, c);
     case 2: return E::template mma<16, 0, 2>(b, sb, a, y, c);
@@ -451,15 +454,31 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
     };
 
     // Mx4: a half panel's scales as read, and as the MFMAs take them (like a and b)
-    u32x2 raw_a = {}, raw_b = {};
-    unsigned sa[2][T::SAW] = {}, sb4[2][1] = {};
+    u32x2 raw_a[T::DIRECT ? T::FM : 1] = {}, raw_b[T::SBW] = {};
+    unsigned sa[2][T::SAW] = {}, sb4[2][T::SBW] = {};
     typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
-    auto read_scales = [&](int kt, bool of_b, int half, u32x2 &raw) {
+    auto read_scales = [&](int kt, bool of_b, int half, auto &raw) {
         const lds_char *sc = (const lds_char *)lds + 2 * T::STAGE + (kt / 2 & 1) * T::SC_PAIR;
         const int second = (kt & 1) != 0 || (kt == nk - 1 && kt > 0) ? 8 : 0;
         // B's, of at most two blocks, come from the first 32 lanes; the rows that the others read lie in A's
-        const int row = of_b ? half * T::CH + wn * T::QN + lane : T::BN + half * T::RH + wm * T::QM + lane % T::QM;
-        raw = *(const lds_u32x2 *)(sc + second + 16 * row);
+        const int row0 = of_b ? half * T::CH + wn * T::QN : T::BN + half * T::RH + wm * T::QM;
+        if constexpr (T::DIRECT) {
+            constexpr int blocks = sizeof raw / sizeof raw[0];
+#pragma unroll
+            for (int i = 0; i < blocks; ++i) raw[i] = *(const lds_u32x2 *)(sc + second + 16 * (row0 + 16 * i + lane % 16));
+        } else {
+            raw[0] = *(const lds_u32x2 *)(sc + second + 16 * (row0 + (of_b ? lane : lane % T::QM)));
+        }
+    };
+    auto spread = [&](auto &raw, auto &words) {
+        if constexpr (T::DIRECT) {  // chunks g and 4 + g to bytes 0 and 1
+            constexpr int blocks = sizeof raw / sizeof raw[0];
+#pragma unroll
+            for (int i = 0; i < blocks; ++i)
+                words[i] = __builtin_amdgcn_perm(raw[i][1], raw[i][0], (unsigned)(lane >> 4) * 0x0101u | 0x0c0c0400u);
+        } else {
+            scales_of_lane(raw[0], words);
+        }
     };
     // of the first two K-steps, through registers
     auto first_scales = [&] {
@@ -569,13 +588,13 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         auto mfma = [&](int m) {  // operands in the order in which the next half replaces them
             const int ks = m / (T::FM * T::FN);
             const int i = I == 2 ? m % T::FM : m / T::FN % T::FM, j = I == 2 ? m / T::FM % T::FN : m % T::FN;
-            acc[qa][qb][i][j] = mma_scaled<T>(b[qb][ks][j], sb4[qb][0], j, a[0][ks][i], sa[0], i, ks, acc[qa][qb][i][j]);
+            acc[qa][qb][i][j] = mma_scaled<T>(b[qb][ks][j], sb4[qb], j, a[0][ks][i], sa[0], i, ks, acc[qa][qb][i][j]);
         };
         // the offsets of the loads and reads anew for each K-step: kept, they would take some 20 registers
         if constexpr (I == 0) asm volatile("" : "+v"(a_row), "+v"(b_row), "+v"(d_off[0]), "+v"(d_off[1]));
         // the scales that the phase before read
-        if constexpr (reads_a) scales_of_lane(raw_b, sb4[1]);
-        else scales_of_lane(raw_a, sa[0]);
+        if constexpr (reads_a) spread(raw_b, sb4[1]);
+        else spread(raw_a, sa[0]);
 #pragma unroll
         for (int m = 0; m < pre; ++m) mfma(m);
         // half panels issued after number 4 kt + 2 + I, which is read next
@@ -584,7 +603,12 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         // at most the reads of the phase before are left: those before it are done
         asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(T::KS * (reads_a ? T::FN : T::FM)) : "memory");
         bare_barrier();
-        if constexpr (later >= 0) read_scales(kt + (I >= 2), !reads_a, I < 2, reads_a ? raw_a : raw_b);
+        if constexpr (later < 0) {
+        } else if constexpr (reads_a) {
+            read_scales(kt + (I >= 2), false, I < 2, raw_a);
+        } else {
+            read_scales(kt + (I >= 2), true, I < 2, raw_b);
+        }
         auto read = [&](int r) {
             if constexpr (later < 0) return;
             else if constexpr (reads_a) read_a(half, r, a[0]);
@@ -608,7 +632,8 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         for (int ks = 0; ks < T::KS; ++ks)
 #pragma unroll
             for (int j = 0; j < T::FN; ++j) b[0][ks][j] = b[1][ks][j];
-        sb4[0][0] = sb4[1][0];
+#pragma unroll
+        for (int j = 0; j < T::SBW; ++j) sb4[0][j] = sb4[1][j];
         phase_mx(kt, std::integral_constant<int, 0>(), LEFT);
         phase_mx(kt, std::integral_constant<int, 1>(), LEFT);
         phase_mx(kt, std::integral_constant<int, 2>(), LEFT);
@@ -633,12 +658,12 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         auto mfma = [&](int m) {
             const int ks = m / (T::FM * T::FN), i = m / T::FN % T::FM, j = m % T::FN;
             if constexpr (T::MX)
-                acc[0][I][i][j] = mma_scaled<T>(b[I][ks][j], sb4[I][0], j, a[S][ks][i], sa[S], i, ks, acc[0][I][i][j]);
+                acc[0][I][i][j] = mma_scaled<T>(b[I][ks][j], sb4[I], j, a[S][ks][i], sa[S], i, ks, acc[0][I][i][j]);
             else acc[0][I][i][j] = E::template mma<T::MB>(b[I][ks][j], a[S][ks][i], acc[0][I][i][j]);
         };
         if constexpr (T::MX) {
-            scales_of_lane(raw_b, sb4[I]);
-            if constexpr (I == 0) scales_of_lane(raw_a, sa[S]);
+            spread(raw_b, sb4[I]);
+            if constexpr (I == 0) spread(raw_a, sa[S]);
         }
 #pragma unroll
         for (int m = 0; m < pre; ++m) mfma(m);
@@ -735,7 +760,7 @@ __device__ __forceinline__ void tile_body(const GroupArgs &p, char *lds, int g, 
         if constexpr (T::MX) {
             read_scales(0, false, 0, raw_a);
             read_scales(0, true, 0, raw_b);
-            if constexpr (!LO) scales_of_lane(raw_b, sb4[1]);
+            if constexpr (!LO) spread(raw_b, sb4[1]);
         }
         wait_reads();
         bare_barrier();
