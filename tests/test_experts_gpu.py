@@ -556,7 +556,9 @@ def test_layer_captured_and_replayed(dev):
     (17, 64, 4, {}), (40, 200, 12, dict(renormalize=True)), (64, 33, 5, dict(scoring="sigmoid")),
     (50, 256, 13, {}), (50, 257, 8, {}), (70, 256, 12, dict(groups=16, top_groups=5, group_top=2)),
     (70, 136, 6, dict(groups=17, top_groups=3, group_top=2)), (1025, 48, 3, dict(renormalize=True)),
-    (8192, 16, 2, {}), (8193, 16, 2, {}), (8200, 300, 2, {}), (9001, 130, 2, dict(groups=2)), (1000, 700, 3, {})])
+    (8192, 16, 2, {}), (8193, 16, 2, {}), (8200, 300, 2, {}), (9001, 130, 2, dict(groups=2)), (1000, 700, 3, {}),
+    (16, 256, 8, {}), (17, 129, 7, {}), (64, 256, 8, dict(scoring="sigmoid", groups=8, top_groups=4, group_top=2)),
+    (64, 128, 9, {}), (65, 128, 9, {})])
 @pytest.mark.parametrize("biased", [False, True])
 def test_route_borders(dev, T, E, k, how, biased):
     """Sizes on both sides of where another kernel or another number of launches takes over."""

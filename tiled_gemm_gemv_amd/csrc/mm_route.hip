@@ -1128,10 +1128,12 @@ static bool rows_of_16(int64_t E, int64_t k, int64_t groups) { return E <= kRowE
 
 // Tokens of a workgroup. Four to a wave: 4 waves, so that more CUs take part, or 16 where all of them have
 // work. Else one to a wave of 16, or four after each other (4001 tokens of 60 experts one by one: 15 us with
-// 64 to a workgroup, 7 with 16). One workgroup saves a launch.
+// 64 to a workgroup, 7 with 16). One workgroup saves a launch, which pays up to 64 tokens of at most 128
+// experts (both kernels against one, in a graph: 32 of 64 experts 7.2 and 5.9 us, 64 of 128 8.5 and 9.2, 64 of
+// 256 10.5 and 13.4, in groups 13.2 and 17.9).
 static int tokens_of(int64_t T, int64_t E, int64_t k, int64_t groups)
 {
-    if (rows_of_16(E, k, groups)) return T <= 16 || (T > 64 && T <= 8192) ? 16 : 64;
+    if (rows_of_16(E, k, groups)) return T <= 16 || (T <= 8192 && (T > 64 || E > 128)) ? 16 : 64;
     return T <= 32 || T > 8192 ? kTokens : kWaves;
 }
 
