@@ -258,6 +258,25 @@ __device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int lane)
 // the bias 2^-24 |c|.
 __device__ __forceinline__ float slack(float c) { return 0x1p-22f + 0x1p-23f * fabsf(c); }
 
+// The same for a group's value, first or (two) first + second: its summands' slack, however small the sum
+// of summands of either sign is. Half of 2^-23 |c| is c's own rounding, the other half the sum's. A sum
+// past fp32's range may be anything; one with -inf is -inf in 64 bits too.
+template <class V>
+__device__ __forceinline__ float group_slack(V first, V second, V value, bool two)
+{
+    if constexpr (sizeof(V) == 8) return 0.f;
+    else if ((two ? second : first) == -__builtin_inff()) return 0.f;
+    else if (!(fabsf(value) < __builtin_inff())) return __builtin_inff();
+    else return slack(first) + (two ? slack(second) : 0.f);
+}
+// Whether values of 64 bits may stand in another order than `low`, the last kept group's, and `next`, the
+// best other's: `off` is the largest slack of any group (a hundredth more for the rounding of these bounds).
+__device__ __forceinline__ bool groups_close(float low, float next, float off)
+{
+    const float inf = __builtin_inff();
+    return off == inf || (next > -inf && !(low - next > 2.01f * off));
+}
+
 // v of the lane that differs in the bit d (a lane of the other half of 2 d lanes, where those of a half
 // are equal).
 template <class V>
@@ -283,9 +302,11 @@ __device__ __forceinline__ double readlane(double v, int lane)
 }
 
 // The kept groups, 2^shift lanes to a group, the bit of a group that of its first lane; at(e) is the
-// value of expert e, no NaN. low, next: the last kept group's value and the first other's.
+// value of expert e, no NaN. low, next: the last kept group's value and the first other's; off: group_slack,
+// of the lane's group.
 template <class V, class F>
-__device__ __forceinline__ unsigned long long keep_groups(const RouteArgs &p, int per, int shift, F &&at, V &low, V &next)
+__device__ __forceinline__ unsigned long long keep_groups(const RouteArgs &p, int per, int shift, F &&at, V &low, V &next,
+                                                          float &off)
 {
     const int lane = threadIdx.x & 63, g = lane >> shift, e0 = min(g, p.groups - 1) * per;
     const V none = -__builtin_inff();
@@ -307,6 +328,7 @@ __device__ __forceinline__ unsigned long long keep_groups(const RouteArgs &p, in
             first = fmax(first, f);
         }
     const V value = p.group_top == 1 ? first : second == none ? none : first + second;
+    off = group_slack(first, second, value, p.group_top == 2);
     int rank = 0;
     for (int i = 0; i < p.groups; ++i) {
         const V v = readlane(value, i << shift);
@@ -406,10 +428,11 @@ __device__ __forceinline__ int route_token(const RouteArgs &p, int64_t t, const 
         }
         exact = __any(odd);
         __builtin_amdgcn_wave_barrier();
-        float low, next;
-        kept = keep_groups<float>(p, per, shift, [&](int e) { return row[e]; }, low, next);
+        float low, next, off;
+        kept = keep_groups<float>(p, per, shift, [&](int e) { return row[e]; }, low, next, off);
         __builtin_amdgcn_wave_barrier();
-        if (!exact && p.top_groups < p.groups && (by_score || sums) && next > -inf && !(low - next > 4 * slack(low))) {
+        off = __builtin_bit_cast(float, wave_max_u32(__builtin_bit_cast(unsigned, off)));  // not negative
+        if (!exact && p.top_groups < p.groups && (by_score || sums) && groups_close(low, next, off)) {
             // too close to tell: the same in 64 bits (softmax without a bias: without the quotient)
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -423,7 +446,8 @@ __device__ __forceinline__ int route_token(const RouteArgs &p, int64_t t, const 
                 return v;
             };
             double low64, next64;
-            kept = keep_groups<double>(p, per, shift, wide, low64, next64);
+            float none;
+            kept = keep_groups<double>(p, per, shift, wide, low64, next64, none);
             __builtin_amdgcn_wave_barrier();
         }
     }
@@ -661,7 +685,8 @@ __device__ __forceinline__ V row_sum(V v)
 
 // As keep_groups, for each row's token; the bits of a group's lanes in the row.
 template <class V, class F>
-__device__ __forceinline__ unsigned row_keep_groups(const RouteArgs &p, int per, int shift, F &&at, V &value, int &rank)
+__device__ __forceinline__ unsigned row_keep_groups(const RouteArgs &p, int per, int shift, F &&at, V &value, int &rank,
+                                                    float &off)
 {
     const int lane = threadIdx.x & 63, q = lane & 15, g = q >> shift, e0 = min(g, p.groups - 1) * per;
     const V none = -__builtin_inff();
@@ -683,6 +708,7 @@ __device__ __forceinline__ unsigned row_keep_groups(const RouteArgs &p, int per,
             first = fmax(first, f);
         }
     value = p.group_top == 1 ? first : second == none ? none : first + second;
+    off = group_slack(first, second, value, p.group_top == 2);
     int above = 0;  // lanes of better groups
     each_other([&](auto i) {
         constexpr int I = decltype(i)::value;
@@ -783,14 +809,15 @@ __global__ __launch_bounds__(64 * W) void route_rows_of_16_kernel(RouteArgs p)
         }
         exact = (__ballot(odd) >> (lane & 48) & 0xffffu) != 0;
         __builtin_amdgcn_wave_barrier();
-        float value;
+        float value, off;
         int rank;
-        kept = row_keep_groups<float>(p, per, shift, [&](int e) { return row[e]; }, value, rank);
+        kept = row_keep_groups<float>(p, per, shift, [&](int e) { return row[e]; }, value, rank, off);
         __builtin_amdgcn_wave_barrier();
         if (p.top_groups < p.groups && (by_score || sums)) {
             const float low = from_ordered32(row_max(rank == p.top_groups - 1 && q >> shift < p.groups ? ordered32(value) : 0u));
             const float next = from_ordered32(row_max(rank == p.top_groups && q >> shift < p.groups ? ordered32(value) : 0u));
-            const bool close = !exact && next > -inf && !(low - next > 4 * slack(low));
+            off = __builtin_bit_cast(float, row_max(__builtin_bit_cast(unsigned, off)));  // not negative
+            const bool close = !exact && groups_close(low, next, off);
             if (__any(close)) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) row[q + 16 * r] = c[r] == -inf ? -inf : l[r];
@@ -804,7 +831,8 @@ __global__ __launch_bounds__(64 * W) void route_rows_of_16_kernel(RouteArgs p)
                 };
                 double value64;
                 int rank64;
-                const unsigned kept64 = row_keep_groups<double>(p, per, shift, wide, value64, rank64);
+                float none;
+                const unsigned kept64 = row_keep_groups<double>(p, per, shift, wide, value64, rank64, none);
                 __builtin_amdgcn_wave_barrier();
                 if (close) kept = kept64;
             }
