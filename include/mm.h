@@ -501,7 +501,8 @@ int mm_route_topk(int64_t T, int64_t E, int64_t k, const void *logits, int type,
  *   sigmoid   dlogits_e = s_e (1 - s_e) g_e
  *   g_e       of the expert of slot j: scale dw_j; renormalised, with S the sum of the chosen
  *             scores, scale (dw_j - sum over i of dw_i s_i / S) / S (0 where S is 0); else 0
- * dlogits is T x E of the logits' type, ldd >= max(1, E), written. Computed in fp32, rounded once.
+ * dlogits is T x E of the logits' type, ldd >= max(1, E), written. The shares s_i / S are computed in
+ * 64 bits, as the weights are (scores may be below fp32's smallest), all else in fp32, rounded once.
  * Other arguments as for mm_route_topk. T == 0 or E == 0: nothing is enqueued.
  */
 int mm_route_topk_grad(int64_t T, int64_t E, int64_t k, const void *logits, int type, int64_t ld,

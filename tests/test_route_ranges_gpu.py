@@ -68,3 +68,81 @@ def test_groups_past_the_range_of_32_bits(dev, E, top_groups, group_top):
     how = dict(scoring="sigmoid", groups=groups, top_groups=top_groups, group_top=group_top)
     got = mm.route_topk(x, 2, bias=bias.to(dev), **how)
     check_route(x, got, bias=bias.double().numpy(), **how)
+
+
+# ------------------------------------------------------------ gradient of renormalised weights
+
+def differences(x, experts, dw, scoring, scale, e, h):
+    """The derivative of sum w_j dw_j with respect to x[e] from two values of it; weights from logarithms
+    of scores, which do not leave any range."""
+    def value(v):
+        l = v[experts] if scoring == "softmax" else -np.logaddexp(0, -v[experts])
+        w = np.exp(l - l.max())
+        return scale * (w / w.sum() * dw).sum()
+    up, down = x.copy(), x.copy()
+    up[e] += h
+    down[e] -= h
+    return (value(up) - value(down)) / (2 * h)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("level", [-80, -88, -92, -95, -100, -104, -110, -200, -700])
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 6), (130, 12), (1024, 32)])
+def test_grad_of_small_scores(dev, E, k, level, scoring, dtype):
+    """Scores around and below fp32's smallest, 2^-126 and 2^-149, whose shares are ordinary numbers: all
+    of a sigmoid's; a softmax's but the first expert's, which a bias keeps from being chosen."""
+    rng = np.random.default_rng(E - level)
+    T = 7
+    x = level + rng.standard_normal((T, E))
+    if scoring == "softmax":
+        x[:, 0] = 0
+    x = on(x, dev, dtype)
+    bias = torch.ones(E)
+    bias[0] = -1.0
+    w, experts, _, _ = mm.route_topk(x, k, scoring=scoring, renormalize=True, scale=1.5, bias=bias.to(dev))
+    assert bool((w.double().sum(dim=1) - 1.5).abs().max() <= 1e-6) and bool((experts > 0).all())
+    dw = on(rng.standard_normal((T, k)), dev)
+    got = mm.route_topk_grad(x, experts, dw, scoring=scoring, renormalize=True, scale=1.5)
+    xh, eh, dh = x.cpu().double().numpy(), experts.cpu().numpy(), dw.cpu().double().numpy()
+    want, size = gradient(xh, eh, dh, scoring, True, 1.5)
+    err = np.abs(got.cpu().double().numpy() - want)
+    assert (err <= (E + 32) * U * size + half_step(want, DT[dtype]) + 1e-38).all()
+    for t in (0, T - 1):
+        for e in (0, eh[t, 0], eh[t, -1]):
+            # a term h^2 |third derivative| <= 1e-8 size, and 2^-53 level / h of the values
+            assert abs(differences(xh[t], eh[t], dh[t], scoring, 1.5, e, 1e-4) - want[t, e]) <= 1e-7 * max(1, size[t].max())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_grad_where_scores_vanish_or_are_none(dev, scoring):
+    """Rows whose chosen scores are 0 in 64 bits too, whose weights then are 0; masked ones; NaN."""
+    x = np.full((6, 10), -1000.0)
+    x[:, 0] = 0 if scoring == "softmax" else -1000
+    x[1] = -np.inf
+    x[2, 2:] = -np.inf
+    x[2, :2] = -95, -95.5
+    x[4] = np.linspace(-1, 1, 10)
+    x[5] = np.linspace(-1, 1, 10)
+    x[5, 9] = np.nan
+    experts = torch.tensor([[3, 4], [-1, -1], [1, -1], [1, 5], [7, 8], [9, 2]], dtype=torch.int32, device=dev)
+    dw = torch.ones(6, 2, device=dev)
+    dw[:, 0] = -2
+    dw[4, 1] = float("nan")
+    got = mm.route_topk_grad(on(x, dev), experts, dw, scoring=scoring, renormalize=True).cpu()
+    assert bool((got[:4] == 0).all())  # one chosen expert's share is 1 whatever its logit
+    assert bool(torch.isnan(got[4, 7:9]).all()) and bool(torch.isnan(got[5, [9, 2]]).all())
+    if scoring == "softmax":
+        assert bool(torch.isnan(got[4:]).all())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_grad_of_odd_experts_renormalised(dev, scoring):
+    """Entries that are no expert add nothing; one that stands twice counts twice."""
+    rng = np.random.default_rng(5)
+    x = on(rng.standard_normal((3, 10)) - 100, dev)
+    experts = torch.tensor([[-1, 4, 10], [2, 2, 7], [-5, 2 ** 30, -1]], dtype=torch.int32, device=dev)
+    dw = on(rng.standard_normal((3, 3)), dev)
+    got = mm.route_topk_grad(x, experts, dw, scoring=scoring, renormalize=True).cpu().double().numpy()
+    want, size = gradient(x.cpu().double().numpy(), experts.cpu().numpy(), dw.cpu().double().numpy(), scoring, True, 1.0)
+    assert (np.abs(got - want) <= 42 * U * size + 1e-38).all()

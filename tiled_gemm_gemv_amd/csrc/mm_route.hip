@@ -1045,15 +1045,17 @@ __global__ __launch_bounds__(1024) void route_rows_kernel(RouteArgs p, int block
 }
 
 // dl_e of one token by one wave: with g_e the gradient of s_e (0 where e was not chosen),
-// softmax s_e (g_e - sum over i of s_i g_i), sigmoid s_e (1 - s_e) g_e. For w_j = scale s_j,
-// g = scale dw; renormalised, with S the sum of the chosen s: g_j = scale / S (dw_j - sum_i dw_i s_i / S).
+// softmax s_e (g_e - sum over i of s_i g_i), sigmoid s_e (1 - s_e) g_e. For w_j = scale s_j, g = scale dw.
+// Renormalised, with S the sum of the chosen s and shares r_j = s_j / S: g_j = scale / S (dw_j - sum_i dw_i r_i),
+// so that softmax's sum of s g vanishes and s_j g_j = scale r_j (dw_j - sum_i dw_i r_i). The shares are the
+// weights that the token got, taken in 64 bits as there: the chosen s may be far below fp32's smallest.
 template <class X, int R>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p)
 {
     const int lane = threadIdx.x & 63;
     const int64_t t = linear_block() * 4 + (threadIdx.x >> 6);
     if (t >= p.T) return;
-    float l[R], s[R], d[R], g[R];  // d: s (1 - s) of a sigmoid
+    float l[R], s[R], g[R];
     float m = -__builtin_inff();
     bool nan = false;
 #pragma unroll
@@ -1064,47 +1066,27 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p)
         nan |= l[r] != l[r];
         g[r] = 0;
     }
-    float sum = 0;
-    if (p.sigmoid) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float q = expf(-fabsf(l[r])), n = 1.f / (1.f + q);
-            s[r] = l[r] < 0 ? q * n : n;
-            d[r] = q * n * n;
-        }
-    } else {
+    if (!p.sigmoid) {
 #pragma unroll
         for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
         if (m == -__builtin_inff()) m = 0;
-        if (__any(nan)) m = __builtin_nanf("");
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            s[r] = lane + 64 * r < p.E ? expf(l[r] - m) : 0.f;
-            sum += s[r];
-        }
-        sum = wave_add(sum);
-#pragma unroll
-        for (int r = 0; r < R; ++r) s[r] = sum == 0 ? 0.f : s[r] / sum;
+        if (__any(nan) || !(m < __builtin_inff())) m = __builtin_nanf("");  // all scores are NaN
     }
     // lane j: slot j
     int e = lane < p.k ? p.experts[t * p.k + lane] : -1;
     if (e < 0 || e >= p.E) e = -1;
-    float dw = e >= 0 ? p.scale * p.dweights[t * p.k + lane] : 0.f, mine = 0;
-    for (int j = 0; j < p.k; ++j) {
-        const int of = __shfl(e, j);
-        float v = 0;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (of >= 0 && of >> 6 == r) v = s[r];
-        v = __shfl(v, of & 63);
-        if (lane == j && of >= 0) mine = v;
-    }
+    float dw = e >= 0 ? p.scale * p.dweights[t * p.k + lane] : 0.f;
+    float rest = 0;  // softmax: what the sum of s g leaves to the experts not chosen, 0 or NaN
     if (p.renormalize) {
-        float total = wave_add(mine);
-        const float mean = total == 0 ? 0.f : wave_add(dw * (mine / total));
-        dw = total == 0 || e < 0 ? 0.f : (dw - mean) / total;
+        const float x = e >= 0 ? load_logit<X>(p.logits, t * p.ld + e) : 0.f;
+        const double score = e < 0 ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)m);
+        const double total = wave_add(score);
+        const float share = total == 0 ? 0.f : (float)(score / total);
+        const float mean = total == 0 ? 0.f : wave_add(dw * share);
+        const float q = expf(-fabsf(x)), not_s = x < 0 ? 1.f / (1.f + q) : q / (1.f + q);
+        dw = total == 0 || e < 0 ? 0.f : share * (dw - mean) * (p.sigmoid ? not_s : 1.f);
+        rest = p.sigmoid ? 0.f : 0.f * fabsf(mean) + 0.f * m;
     }
-    float dot = 0;
     for (int j = 0; j < p.k; ++j) {
         const int of = __shfl(e, j);
         const float v = __shfl(dw, j);
@@ -1112,15 +1094,36 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p)
         for (int r = 0; r < R; ++r)
             if (of == lane + 64 * r) g[r] += v;
     }
-    if (!p.sigmoid) {
+    if (p.renormalize) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) dot = fmaf(s[r], g[r], dot);
+        for (int r = 0; r < R; ++r) g[r] = l[r] != l[r] ? l[r] : g[r] + rest;
+    } else if (p.sigmoid) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float q = expf(-fabsf(l[r])), n = 1.f / (1.f + q);
+            g[r] *= q * n * n;
+        }
+    } else {
+        float sum = 0, dot = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] = lane + 64 * r < p.E ? expf(l[r] - m) : 0.f;
+            sum += s[r];
+        }
+        sum = wave_add(sum);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] = sum == 0 ? 0.f : s[r] / sum;
+            dot = fmaf(s[r], g[r], dot);
+        }
         dot = wave_add(dot);
+#pragma unroll
+        for (int r = 0; r < R; ++r) g[r] = s[r] * (g[r] - dot);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = lane + 64 * r;
-        if (i < p.E) static_cast<X *>(p.dlogits)[t * p.ldd + i] = (X)(p.sigmoid ? d[r] * g[r] : s[r] * (g[r] - dot));
+        if (i < p.E) static_cast<X *>(p.dlogits)[t * p.ldd + i] = (X)g[r];
     }
 }
 
