@@ -461,7 +461,8 @@ int mm_gemm_mx4_grouped(int64_t groups, int64_t M, int64_t N, int64_t K, const i
  *   choice    experts are ranked by c_e = s_e + bias_e; without a bias by l_e (which ranks them
  *             as s_e does). With groups > 1 the experts stand in groups of E / groups neighbours,
  *             a group's value is the sum of its group_top largest c_e (without a bias: of l_e
- *             for group_top 1, of s_e for 2), and only the top_groups best groups' experts can be
+ *             for group_top 1, of s_e for 2; of all it has, where that is one), experts that cannot
+ *             be chosen counting as -infinity, and only the top_groups best groups' experts can be
  *             chosen. The k best experts are, in falling order. All of this is computed in 64
  *             bits; equal values rank by the lower index, NaN above every number.
  *   weights   w_j = scale * s_j for the expert of slot j; with renormalize scale * s_j / (the sum

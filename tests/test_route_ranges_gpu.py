@@ -146,3 +146,48 @@ def test_grad_of_odd_experts_renormalised(dev, scoring):
     got = mm.route_topk_grad(x, experts, dw, scoring=scoring, renormalize=True).cpu().double().numpy()
     want, size = gradient(x.cpu().double().numpy(), experts.cpu().numpy(), dw.cpu().double().numpy(), scoring, True, 1.0)
     assert (np.abs(got - want) <= 42 * U * size + 1e-38).all()
+
+
+# ------------------------------------------------------------------ groups of a single expert
+
+def routed_alone(x, k, scoring, bias, top_groups, renormalize):
+    """experts and weights where each expert is a group, whose value is the sum of the one it has."""
+    T, E = x.shape
+    s = scores(x, scoring)
+    experts, weights = np.full((T, k), -1), np.zeros((T, k))
+    for t in range(T):
+        c = s[t] + bias if bias is not None else x[t]
+        dead = np.isneginf(x[t]) | np.isneginf(c)
+        value = np.where(dead, -np.inf, c if bias is not None else s[t])
+        kept = best_first(value)[:top_groups]
+        c = np.where(dead | ~np.isin(np.arange(E), kept), -np.inf, c)
+        order = [e for e in best_first(c) if not np.isneginf(c[e])][:k]
+        experts[t, :len(order)] = order
+        w = s[t][order]
+        weights[t, :len(order)] = w / w.sum() if renormalize and w.sum() != 0 else w
+    return experts, weights
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,top_groups,k", [(2, 1, 1), (12, 4, 2), (16, 3, 3), (17, 5, 4), (40, 30, 20), (64, 8, 8)])
+def test_groups_of_one_expert(dev, E, top_groups, k, biased, scoring, dtype):
+    rng = np.random.default_rng(E + k)
+    x = rng.standard_normal((60, E)) * 1.5
+    x[3] = -np.inf
+    x[4, 1:] = -np.inf
+    x[5] = 40 + np.arange(E) % 3  # a sigmoid of 1 in 64 bits: equal groups, the lower index first
+    if scoring == "sigmoid":
+        x[6, E // 2] = np.nan  # done in 64 bits throughout
+        x[7, E - 1] = np.inf
+    x = on(x, dev, dtype)
+    bias = torch.from_numpy((0.1 * rng.standard_normal(E)).astype(np.float32)) if biased else None
+    got = mm.route_topk(x, k, scoring=scoring, bias=bias.to(dev) if biased else None, groups=E, top_groups=top_groups,
+                        group_top=2, renormalize=True)
+    experts, weights = routed_alone(x.cpu().double().numpy(), k, scoring, bias.double().numpy() if biased else None,
+                                    top_groups, True)
+    assert np.array_equal(got[1].cpu().numpy(), experts)
+    w = got[0].cpu().double().numpy()
+    assert np.array_equal(np.isnan(w), np.isnan(weights))
+    assert (np.abs(w - weights) <= 2 * U * np.abs(weights) + 2.0 ** -150)[~np.isnan(weights)].all()

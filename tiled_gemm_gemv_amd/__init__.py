@@ -1158,13 +1158,14 @@ def route_topk(logits, k, scoring="softmax", bias=None, groups=1, top_groups=1, 
     """(weights, experts, rows, offsets): the k best of E experts for each row of logits (T x E; float32,
     bfloat16 or float16), and the order of their rows. Scores are the softmax or the sigmoid of the
     logits; experts are chosen by score + bias (float32, E entries), with groups > 1 among the
-    top_groups groups of E / groups neighbours whose group_top (1 or 2) best add up highest; equal ones
-    by the lower index. weights (T x k, float32) are the chosen scores times scale, with renormalize
-    divided by their sum. experts (T x k, int32) holds -1 where none is left (logits of -inf are never
-    chosen: give padded tokens only those). rows (T x k, int32) numbers the slots by expert, token and
-    slot, -1 without an expert, and offsets (E + 1, int64) says where each expert's rows begin, as the
-    grouped products take it. workspace: a device tensor of mm_route_topk_workspace_bytes bytes (e.g.
-    from route_topk_workspace); allocated for the call if not given."""
+    top_groups groups of E / groups neighbours whose group_top (1 or 2) best add up highest (a single
+    expert's own value, where a group has no more); equal ones by the lower index. weights (T x k,
+    float32) are the chosen scores times scale, with renormalize divided by their sum. experts (T x k,
+    int32) holds -1 where none is left (logits of -inf are never chosen: give padded tokens only
+    those). rows (T x k, int32) numbers the slots by expert, token and slot, -1 without an expert, and
+    offsets (E + 1, int64) says where each expert's rows begin, as the grouped products take it.
+    workspace: a device tensor of mm_route_topk_workspace_bytes bytes (e.g. from
+    route_topk_workspace); allocated for the call if not given."""
     torch = _torch or _import_torch()
     ld = _matrix(logits, "logits", (torch.float32, torch.bfloat16, torch.float16))
     device = logits.get_device()

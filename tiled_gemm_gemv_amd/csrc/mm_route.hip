@@ -3,7 +3,7 @@
 // Scores of token t: s_e = exp(l_e - m) / sum exp(l - m), m = max l, or s_e = 1 / (1 + exp(-l_e)).
 // Experts are ranked by c_e = s_e + b_e, without a bias by l_e, which ranks them as s_e does; groups
 // of E / G neighbouring experts by the sum of their group_top best c_e (without a bias and with
-// group_top 2: s_e). The best top_groups groups are kept, then the best k experts in them; equal
+// group_top 2: s_e; of a single expert, its own). The best top_groups groups are kept, then the best k experts in them; equal
 // values go to the lowest index, NaN is above every number. An expert whose l_e or c_e is -inf is not
 // chosen; slots left over get expert -1 and weight 0. w_j = scale s_j, or scale s_j / sum of the chosen s
 // (0 where that is 0).
@@ -145,7 +145,7 @@ __device__ __forceinline__ int route_token_exact(const RouteArgs &p, int64_t t)
         for (int g = 0; g < p.groups; ++g) {
             double sum = 0;
             int taken = -1;
-            for (int n = 0; n < p.group_top; ++n) {
+            for (int n = 0; n < min(p.group_top, per); ++n) {
                 uint64_t best = 0;
                 int index = 0x7fffffff;
                 double value = -__builtin_inf();
@@ -164,7 +164,7 @@ __device__ __forceinline__ int route_token_exact(const RouteArgs &p, int64_t t)
                 wave_best(best, index);
                 const unsigned long long who = __ballot(own == index);
                 value = __shfl(value, who ? __ffsll(who) - 1 : 0);
-                sum = n == 0 ? value : index == 0x7fffffff ? -__builtin_inf() : sum + value;
+                sum = n == 0 ? value : sum + value;
                 taken = index;
             }
             if (lane == g) mine = ordered(sum);
@@ -327,8 +327,9 @@ __device__ __forceinline__ unsigned long long keep_groups(const RouteArgs &p, in
             second = fmax(fmin(first, f), fmax(second, h));
             first = fmax(first, f);
         }
-    const V value = p.group_top == 1 ? first : second == none ? none : first + second;
-    off = group_slack(first, second, value, p.group_top == 2);
+    const bool two = p.group_top == 2 && per > 1;
+    const V value = !two ? first : second == none ? none : first + second;
+    off = group_slack(first, second, value, two);
     int rank = 0;
     for (int i = 0; i < p.groups; ++i) {
         const V v = readlane(value, i << shift);
@@ -707,8 +708,9 @@ __device__ __forceinline__ unsigned row_keep_groups(const RouteArgs &p, int per,
             second = fmax(fmin(first, f), fmax(second, h));
             first = fmax(first, f);
         }
-    value = p.group_top == 1 ? first : second == none ? none : first + second;
-    off = group_slack(first, second, value, p.group_top == 2);
+    const bool two = p.group_top == 2 && per > 1;
+    value = !two ? first : second == none ? none : first + second;
+    off = group_slack(first, second, value, two);
     int above = 0;  // lanes of better groups
     each_other([&](auto i) {
         constexpr int I = decltype(i)::value;
