@@ -393,3 +393,19 @@ def test_other_stream(dev):
     got = mm.gemm_mx4(a, b, sa, sb, stream=stream)
     stream.synchronize()
     check(got.cpu().double().numpy(), av @ bv.T, None, True, torch.float32)
+
+
+@pytest.mark.parametrize("exponent", [-120, 0, 5, 127])
+def test_quantize_every_bf16_below(dev, exponent):
+    """Every 16-bit pattern below 2^(exponent + 1) in size, in blocks whose largest element is 2^exponent or
+    another of its binade: all quotients from there down to 0, the halfway points among them."""
+    x = (np.arange(65536, dtype=np.uint32) << 16).view(np.float32)
+    x = x[np.abs(x.astype(np.float64)) < 2.0 ** (exponent + 1)]
+    x = np.concatenate([x, np.zeros(-len(x) % 31, np.float32)])
+    x = np.random.default_rng(0).permutation(x).reshape(-1, 31)
+    x = np.concatenate([np.full((len(x), 1), 2.0 ** exponent, np.float32), x], axis=1)
+    t = torch.from_numpy(x).to(dev)
+    for v in (t, t.to(torch.bfloat16)):
+        q, s = mm.quantize_mx4(v)
+        assert bool((s == max(exponent - 2, -127) + 127).all())
+        same(x.astype(np.float64), q.cpu().numpy(), s.cpu().numpy())
