@@ -223,6 +223,7 @@ struct RouteArgs {
     int64_t ld;
     int T, E, k, groups, top_groups, group_top;
     int tokens;                // of a workgroup, set by route_launch
+    bool sums;                 // groups by the scores' sums where there is no bias, set by route_launch
     int type;                  // MM_TYPE_*
     bool sigmoid, renormalize;
     float scale;

@@ -145,7 +145,7 @@ __device__ __forceinline__ int route_token_exact(const RouteArgs &p, int64_t t)
         for (int g = 0; g < p.groups; ++g) {
             double sum = 0;
             int taken = -1;
-            for (int n = 0; n < min(p.group_top, per); ++n) {
+            for (int n = 0; n < p.group_top; ++n) {
                 uint64_t best = 0;
                 int index = 0x7fffffff;
                 double value = -__builtin_inf();
@@ -155,8 +155,8 @@ __device__ __forceinline__ int route_token_exact(const RouteArgs &p, int64_t t)
                     const bool dead = l[r] == -__builtin_inff();
                     const double c = dead                                   ? -__builtin_inf()
                                      : p.bias                               ? s[r] + (double)(e < p.E ? p.bias[e] : 0.f)
-                                     : p.group_top == 1                     ? (double)l[r]
-                                                                            : s[r];
+                                     : p.sums                               ? s[r]
+                                                                            : (double)l[r];
                     const uint64_t k = ordered(c);
                     if (e / per == g && e < p.E && e != taken && k > best) best = k, index = e, value = c;
                 }
@@ -327,9 +327,8 @@ __device__ __forceinline__ unsigned long long keep_groups(const RouteArgs &p, in
             second = fmax(fmin(first, f), fmax(second, h));
             first = fmax(first, f);
         }
-    const bool two = p.group_top == 2 && per > 1;
-    const V value = !two ? first : second == none ? none : first + second;
-    off = group_slack(first, second, value, two);
+    const V value = p.group_top == 1 ? first : second == none ? none : first + second;
+    off = group_slack(first, second, value, p.group_top == 2);
     int rank = 0;
     for (int i = 0; i < p.groups; ++i) {
         const V v = readlane(value, i << shift);
@@ -372,7 +371,7 @@ __device__ __forceinline__ int route_token(const RouteArgs &p, int64_t t, const 
 {
     const int lane = threadIdx.x & 63;
     const float inf = __builtin_inff();
-    const bool by_score = p.bias, sums = p.groups > 1 && p.group_top == 2;
+    const bool by_score = p.bias, sums = p.sums;
     // scores in 32 bits (softmax: without the quotient) where the choice or the sum needs them
     float m = 0.f, total32 = 1.f;
     float s[R];
@@ -708,9 +707,8 @@ __device__ __forceinline__ unsigned row_keep_groups(const RouteArgs &p, int per,
             second = fmax(fmin(first, f), fmax(second, h));
             first = fmax(first, f);
         }
-    const bool two = p.group_top == 2 && per > 1;
-    value = !two ? first : second == none ? none : first + second;
-    off = group_slack(first, second, value, two);
+    value = p.group_top == 1 ? first : second == none ? none : first + second;
+    off = group_slack(first, second, value, p.group_top == 2);
     int above = 0;  // lanes of better groups
     each_other([&](auto i) {
         constexpr int I = decltype(i)::value;
@@ -740,7 +738,7 @@ __global__ __launch_bounds__(64 * W) void route_rows_of_16_kernel(RouteArgs p)
     const float inf = __builtin_inff();
     float *row = rows[token];
 
-    const bool by_score = p.bias, sums = p.groups > 1 && p.group_top == 2;
+    const bool by_score = p.bias, sums = p.sums;
     float l[R], c[R];
 #pragma unroll
     for (int r = 0; r < R; ++r)  // no branches: the last one's in the place of others
@@ -1184,6 +1182,8 @@ int64_t route_ws_ints(int64_t T, int E, int k)
 hipError_t route_launch(const RouteArgs &a, hipStream_t stream)
 {
     RouteArgs arg = a;
+    arg.sums = a.groups > 1 && a.group_top == 2;
+    arg.group_top = a.group_top < a.E / a.groups ? a.group_top : a.E / a.groups;  // a group's only expert: its own
     arg.tokens = tokens_of(a.T, a.E, a.k, a.groups);
     int blocks = (int)(((int64_t)a.T + arg.tokens - 1) / arg.tokens);
     unsigned gx, gy;
