@@ -59,10 +59,12 @@
 // 4-bit elements (two to a byte, so a K-step is 256 of them, one 32-element block to a 16-byte chunk) take
 // the same tiles with other phases (phase_mx), since their scales need registers too, and
 // v_mfma_scale_f32_16x16x128, 10.3 ns of a SIMD against 7.8 for i8's of the same bytes. 8192 x 14336 x 4096:
-// 251-276 us, 3.5-3.8 PFLOP/s, 230 registers, MFMAs busy 44% of the cycles at 1.7-2 GHz. Taken apart: without
+// 255-276 us in long runs, 3.5-3.8 PFLOP/s (290-330, 2.9-3.3, in the first 40 calls after a pause, until the
+// clock has settled), 230 registers, MFMAs busy 44% of the cycles at 1.7-2 GHz. Taken apart, of 255 us: without
 // the scales' loads 9 us less, without spreading them to lanes another 16, without reading them 4, and with no
-// loads at all 217 us: what is left is the MFMAs, their operands from LDS and the clock under this load.
-// (32 x 32 x 64 MFMAs: 9% fewer cycles at a clock 8% lower, the same time.)
+// loads at all 217 us. Of these the MFMAs alone are 148; an 8-wave tile's K-step also moves 192 KB of operands
+// from LDS and 64 KB into it, 2048 cycles at 128 bytes each, as many as its MFMAs take, and the two overlap in
+// part only. (32 x 32 x 64 MFMAs: 9% fewer cycles at a clock 8% lower, the same time.)
 #include "mm_group.h"
 
 namespace mm {

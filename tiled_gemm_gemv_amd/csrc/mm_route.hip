@@ -3,18 +3,19 @@
 // Scores of token t: s_e = exp(l_e - m) / sum exp(l - m), m = max l, or s_e = 1 / (1 + exp(-l_e)).
 // Experts are ranked by c_e = s_e + b_e, without a bias by l_e, which ranks them as s_e does; groups
 // of E / G neighbouring experts by the sum of their group_top best c_e (without a bias and with
-// group_top 2: s_e; of a single expert, its own). The best top_groups groups are kept, then the best k experts in them; equal
-// values go to the lowest index, NaN is above every number. An expert whose l_e or c_e is -inf is not
-// chosen; slots left over get expert -1 and weight 0. w_j = scale s_j, or scale s_j / sum of the chosen s
-// (0 where that is 0).
+// group_top 2: s_e; of a single expert, its own). The best top_groups groups are kept, then the best k
+// experts in them; equal values go to the lowest index, NaN is above every number. An expert whose l_e or
+// c_e is -inf is not chosen; slots left over get expert -1 and weight 0. w_j = scale s_j, or scale s_j / sum
+// of the chosen s (0 where that is 0).
 //
 // The ranks are those of 64-bit values: with 16384 tokens and 256 experts some pair of neighbouring
 // scores lies closer than 32-bit rounding, and the choice would go by it. A wave takes four tokens, 16
-// lanes each, or (more than 256 experts, 12 chosen or 16 groups) one. It computes c in 32 bits, off by at most `slack`, and picks the best one after the other by a 32-bit key
-// of 22 leading bits and the index: k of them, and all others that could be above the k-th by slack and
-// truncation. Those few, one to a lane, get their values in 64 bits and are put in that order. Where
-// groups lie closer than the slack, they are ranked in 64 bits; where values are NaN or infinite, or more
-// experts than the token has lanes are that close, the token is done in 64 bits throughout.
+// lanes each, or (more than 256 experts, 12 chosen or 16 groups) one. It computes c in 32 bits, off by at
+// most `slack`, and picks the best one after the other by a 32-bit key of 22 leading bits and the index: k
+// of them, and all others that could be above the k-th by slack and truncation. Those few, one to a lane,
+// get their values in 64 bits and are put in that order. Where groups lie closer than their summands'
+// slack, they are ranked in 64 bits; where values are NaN or infinite, or more experts than the token has
+// lanes are that close, the token is done in 64 bits throughout.
 //
 // The rows' order: slots by (expert, token, slot). A workgroup routes 16 or 64 tokens; a token takes an expert
 // once, so a 64-bit mask for each expert says which of them have it, and counts of its bits number the
@@ -23,9 +24,19 @@
 // order is fixed.
 //
 // Many tokens are bound by instructions, some 2000 of a wave for four tokens of 256 experts, 8 of them
-// chosen: all three kernels for 16384 tokens 19-23 us, with groups and a bias 28 (one token to a wave 39),
-// of 8 MB that could be read in 2. Few are bound by the launches: 3 to 5 us each, three of them (4001 tokens
-// of 60 experts 7 + 4 + 3 us; 8 tokens of 64 experts: one, 5 us).
+// chosen, and by waits for chains of maxima (0.46 of the waves' cycles): all three kernels for 16384 tokens,
+// in a graph, 21-23 us, with groups and a bias 27 (one token to a wave 39), of 8 MB that could be read in 2.
+// One token to a wave: 16384 tokens of 384 experts in groups 51 us, of 512 (10 chosen) 47, of 1024 (32
+// chosen) 173; with so many experts the kernel keeps part of its values in memory. Few tokens are bound by
+// the launches: 3 to 5 us each, three of them (4001 tokens of 60 experts 12 us in a graph; 8 tokens of 64
+// experts: one launch, 5.5).
+//
+// Tokens done in 64 bits throughout take turns in their wave: 16384 tokens whose 256 logits are all equal
+// 56 us, biased and in groups 147; of 512 experts 148. Biases of +-1000 (256 experts in 8 groups), which
+// leave most choices to 64 bits: 119 us.
+//
+// The gradient takes a wave for a token: 16384 tokens of 64, 256 and 512 experts, 16-bit logits, 9, 14 and
+// 20 us (4, 17 and 34 MB read and written), of 1024, fp32, 48 (134 MB); 4001 of 60, fp32, 4.4.
 #include "mm_group.h"
 
 namespace mm {
